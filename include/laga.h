@@ -97,6 +97,10 @@ typedef enum {
  * L = x * gamma / sqrt(mean(x^2) + eps). */
 typedef enum { LAGA_NORM_LAYER = 0, LAGA_NORM_RMS = 1 } laga_norm;
 
+/* A residual half without a norm behind the block (laga_res_dims.norm_post
+ * only; laga_dims.norm refuses it). */
+#define LAGA_NORM_NONE ((laga_norm)2)
+
 /* Element type of q, c, W_kv_b, O, dO and dq.  Compute is bf16 operands with
  * fp32 accumulation in both cases; fp32 I/O is rounded to bf16 on-device. */
 typedef enum { LAGA_BF16 = 0, LAGA_FP32 = 1 } laga_dtype;
@@ -282,6 +286,117 @@ laga_status laga_norm_rope_bwd_noalloc(const laga_dims* dims, const void* c, con
                                        const float* cos, const float* sin,
                                        const float* d_latent, const float* d_kpe_rot,
                                        float* dc, float* dgamma, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The residual stream around a block, and activations kept in 8 bits.  The
+ * paper's blocks sit in a transformer whose residual stream and norms it
+ * leaves open; these calls are the plain form of both, with the paper's
+ * subject, the activation memory held between the passes, in view.
+ *
+ * Per row (token) of d channels, with N the latent norm's LayerNorm or RMS
+ * norm over the d channels:
+ *   residual half (post = 1)   x' = x + alpha s (N_post(y) gamma_post)
+ *   input half    (pre = 1)    h  = N_pre(x') gamma_pre       (x' = x if !post)
+ * y is a block's output, alpha one device-resident fp32 number, s the
+ * sigmoid of the gate logits: of every element (LAGA_GATE_FULL, [rows, d]), of
+ * the token (LAGA_GATE_TOKEN, [rows]) or 1 (LAGA_GATE_NONE).  With
+ * norm_post = LAGA_NORM_NONE, N_post(y) gamma_post is y.  The input half
+ * takes x' before its rounding to the I/O type.
+ *
+ * The backward needs y^ = N_post(y) and x^ = N_pre(x') without their gains.
+ * With ckpt = 0 it is given y and x' again; with ckpt = 1 it is given the
+ * 8-bit checkpoints of y^ and x^ that the forward wrote.
+ *
+ * An 8-bit checkpoint of a [rows, d] activation is a byte matrix of
+ * laga_ckpt_row_bytes(d) bytes per row:
+ *   [ codes: d e4m3 bytes, zero-padded to a multiple of 128
+ *   | one scale byte per 128 channels, zero-padded to a multiple of 16 ]
+ * Scale byte b stands for 2^(b - 127): the smallest power of two 2^e with
+ * max |v| <= 448 2^e over the group's 128 channels, e clamped to [-117,
+ * 119]; a code is v 2^-e rounded to nearest even (values above 448 2^119
+ * saturate).  A group that holds an infinity or a NaN has the scale byte
+ * 255 and stands for NaN throughout.  A value is code * 2^e, exact in bf16.
+ * ------------------------------------------------------------------------ */
+typedef enum { LAGA_GATE_NONE = 0, LAGA_GATE_TOKEN = 1, LAGA_GATE_FULL = 2 } laga_gate;
+
+typedef struct {
+  int rows;              /* tokens, >= 0 (0: nothing is read; sums are zero)  */
+  int d;                 /* channels, 1 .. 16384                              */
+  int post;              /* 1: the residual half                              */
+  int pre;               /* 1: the input half (at least one of the two)       */
+  laga_norm norm_post;   /* LAGA_NORM_LAYER, _RMS or _NONE                    */
+  laga_norm norm_pre;    /* LAGA_NORM_LAYER or _RMS                           */
+  float eps;             /* of both norms, > 0                                */
+  laga_gate gate;
+  int ckpt;              /* 1: y^ and x^ kept as 8-bit checkpoints            */
+  laga_dtype io_dtype;   /* x, y, gate, h and their gradients                 */
+} laga_res_dims;
+
+/* Forward.  Tensors are row-major and contiguous; every pointer 16-byte
+ * aligned; outputs overlap neither inputs nor each other.  A tensor of a half
+ * or an option that is off is ignored.
+ *   x [rows, d]; y [rows, d] (post); gate [rows, d] or [rows] (post);
+ *   alpha [1] fp32 (post); gamma_post [d] fp32 (post, norm_post not NONE);
+ *   gamma_pre [d] fp32 (pre)
+ *   x_out [rows, d] (output, post)   x' in the I/O type
+ *   h     [rows, d] (output, pre)
+ *   ck_y, ck_x  [rows, laga_ckpt_row_bytes(d)] (outputs, ckpt; of y^ with
+ *         post, of x^ with pre)
+ *   stat_post, stat_pre [rows, 2] fp32 (outputs): mean and 1/std of y / x'
+ *         (mean 0 for RMS; 0 and 1 without a norm) */
+laga_status laga_res_fwd(const laga_res_dims* dims, const void* x, const void* y,
+                         const void* gate, const float* alpha, const float* gamma_post,
+                         const float* gamma_pre, void* x_out, void* h, void* ck_y, void* ck_x,
+                         float* stat_post, float* stat_pre, void* stream);
+
+/* Bytes of scratch laga_res_bwd needs (0 if the dims are invalid or no
+ * scratch is needed).  Host-only, no CUDA call. */
+size_t laga_res_workspace_bytes(const laga_res_dims* dims);
+
+/* Backward, for gradients dx_out of x' and dh of h.
+ *   dx_out [rows, d]: may be NULL with pre (no other use of x')
+ *   dh     [rows, d] (pre)
+ *   kept_y, kept_x: the forward's y and x_out (x without post), or, with
+ *          ckpt, its ck_y and ck_x
+ *   stat_post, stat_pre, gate, alpha, gamma_post, gamma_pre: as in the forward
+ *   dx     [rows, d] (output, pre): gradient of x.  Without pre that is
+ *          dx_out itself, and nothing is written.
+ *   dy     [rows, d] (output, post); dgate as gate (output, gate not NONE);
+ *   dalpha [1] fp32 (output, post); dgamma_post [d] fp32 (output, post,
+ *   norm_post not NONE); dgamma_pre [d] fp32 (output, pre)
+ *   ws / ws_bytes: scratch, free again once the call's kernels are done
+ * The gain, alpha and token-gate gradients are sums in fp32 in an order that
+ * the dims fix: repeated calls give the same bits. */
+laga_status laga_res_bwd(const laga_res_dims* dims, const void* dx_out, const void* dh,
+                         const void* kept_y, const void* kept_x, const float* stat_post,
+                         const float* stat_pre, const void* gate, const float* alpha,
+                         const float* gamma_post, const float* gamma_pre, void* dx, void* dy,
+                         void* dgate, float* dalpha, float* dgamma_post, float* dgamma_pre,
+                         void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of one checkpoint row of d channels (0 unless 1 <= d <= 16384).
+ * Host-only. */
+size_t laga_ckpt_row_bytes(int d);
+
+/* x [rows, d] (dtype) into the checkpoint rows ck, and back. */
+laga_status laga_ckpt_pack(int rows, int d, laga_dtype dtype, const void* x, void* ck,
+                           void* stream);
+laga_status laga_ckpt_unpack(int rows, int d, laga_dtype dtype, const void* ck, void* x,
+                             void* stream);
+
+/* Bytes of scratch laga_ckpt_dw needs (0 for invalid sizes or none).
+ * Host-only. */
+size_t laga_ckpt_dw_workspace_bytes(int rows, int d, int n, laga_dtype dy_dtype);
+
+/* Weight gradient behind a checkpointed activation v [rows, d]:
+ *   dw[c, j] = gamma[c] * sum_t v[t, c] dy[t, j]
+ *   dy [rows, n] (dy_dtype), 1 <= n <= 2^20; gamma [d] fp32 or NULL (1);
+ *   dw [d, n] fp32 (output)
+ * Products and sums are in fp32 (an fp32 dy is not rounded to bf16), in an
+ * order that the sizes fix. */
+laga_status laga_ckpt_dw(int rows, int d, int n, laga_dtype dy_dtype, const void* ck,
+                         const void* dy, const float* gamma, float* dw, void* ws,
+                         size_t ws_bytes, void* stream);
 
 /* Per-kernel timing for measurement.  While enabled, every kernel the
  * library launches is bracketed by two CUDA events recorded on its own

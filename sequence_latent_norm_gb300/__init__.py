@@ -8,5 +8,7 @@ build script and a thin binding.
 """
 
 from .api import Laga, Shard, attention_flops, upproj_flops  # noqa: F401
+from .checkpoint import Checkpoint8, pack8, weight_grad8  # noqa: F401
+from .residual import ResidualGrads, ResidualNorm, ResidualOut, ResidualSaved  # noqa: F401
 from . import _lib  # noqa: F401
 from ._lib import LagaError, WS_BWD, WS_SAVED  # noqa: F401

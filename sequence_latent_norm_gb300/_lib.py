@@ -19,13 +19,17 @@ LAGA_ERR_UNSUPPORTED, LAGA_ERR_CUDA, LAGA_ERR_TIMEOUT = 4, 5, 6
 FORMS = {"laga": 0, "explicit": 1, "absorbed": 2, "laga_fused": 3}
 DTYPES = {"bf16": 0, "fp32": 1}
 NORMS = {"layer": 0, "rms": 1}
+POST_NORMS = {**NORMS, "none": 2}
+GATES = {"none": 0, "token": 1, "full": 2}
 WS_SAVED, WS_BWD, WS_FWD = 0, 1, 2
 
 EXPORTED = ("laga_workspace_bytes", "laga_workspace_tensor", "laga_fwd", "laga_fwd_scratch",
             "laga_bwd",
             "laga_bwd_overlap", "laga_sync_check", "laga_status_string", "laga_last_launch_count",
             "laga_profile_enable", "laga_profile_reset", "laga_profile_read",
-            "laga_norm_rope_bwd_noalloc", "laga_selftest_wait_timeout", "laga_diag_mma_rate")
+            "laga_norm_rope_bwd_noalloc", "laga_selftest_wait_timeout", "laga_diag_mma_rate",
+            "laga_res_fwd", "laga_res_bwd", "laga_res_workspace_bytes", "laga_ckpt_row_bytes",
+            "laga_ckpt_pack", "laga_ckpt_unpack", "laga_ckpt_dw", "laga_ckpt_dw_workspace_bytes")
 
 
 class LagaDims(ctypes.Structure):
@@ -35,6 +39,13 @@ class LagaDims(ctypes.Structure):
                 ("d_kv", ctypes.c_int), ("scale", ctypes.c_float), ("ln_eps", ctypes.c_float),
                 ("causal", ctypes.c_int), ("io_dtype", ctypes.c_int), ("form", ctypes.c_int),
                 ("norm", ctypes.c_int)]
+
+
+class LagaResDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int), ("d", ctypes.c_int), ("post", ctypes.c_int),
+                ("pre", ctypes.c_int), ("norm_post", ctypes.c_int), ("norm_pre", ctypes.c_int),
+                ("eps", ctypes.c_float), ("gate", ctypes.c_int), ("ckpt", ctypes.c_int),
+                ("io_dtype", ctypes.c_int)]
 
 
 class LagaError(RuntimeError):
@@ -90,6 +101,23 @@ def load(path: str = LIB_PATH):
     lib.laga_norm_rope_bwd_noalloc.restype = I
     lib.laga_diag_mma_rate.argtypes = [I, I, I, I, I, I, P, P]
     lib.laga_diag_mma_rate.restype = I
+    R = ctypes.POINTER(LagaResDims)
+    lib.laga_res_fwd.argtypes = [R] + [P] * 13
+    lib.laga_res_fwd.restype = I
+    lib.laga_res_bwd.argtypes = [R] + [P] * 17 + [S, P]
+    lib.laga_res_bwd.restype = I
+    lib.laga_res_workspace_bytes.argtypes = [R]
+    lib.laga_res_workspace_bytes.restype = S
+    lib.laga_ckpt_row_bytes.argtypes = [I]
+    lib.laga_ckpt_row_bytes.restype = S
+    lib.laga_ckpt_pack.argtypes = [I, I, I, P, P, P]
+    lib.laga_ckpt_pack.restype = I
+    lib.laga_ckpt_unpack.argtypes = [I, I, I, P, P, P]
+    lib.laga_ckpt_unpack.restype = I
+    lib.laga_ckpt_dw.argtypes = [I, I, I, I, P, P, P, P, P, S, P]
+    lib.laga_ckpt_dw.restype = I
+    lib.laga_ckpt_dw_workspace_bytes.argtypes = [I, I, I, I]
+    lib.laga_ckpt_dw_workspace_bytes.restype = S
     _lib = lib
     return lib
 
@@ -204,3 +232,54 @@ def diag_mma_rate(form: int, n: int, n_acc: int, run: int, n_instr: int, n_cta: 
     (a device address of n_cta uint64)."""
     _check(load().laga_diag_mma_rate(form, n, n_acc, run, n_instr, n_cta, cycles, stream),
            "laga_diag_mma_rate")
+
+
+def make_res_dims(rows, d, *, post=True, pre=True, norm_post="rms", norm_pre="rms", eps=1e-5,
+                  gate="none", ckpt=False, io_dtype="bf16") -> LagaResDims:
+    return LagaResDims(rows, d, int(post), int(pre), POST_NORMS[norm_post], NORMS[norm_pre], eps,
+                       GATES[gate], int(ckpt), DTYPES[io_dtype])
+
+
+def res_fwd(dims: LagaResDims, x, y, gate, alpha, gamma_post, gamma_pre, x_out, h, ck_y, ck_x,
+            stat_post, stat_pre, stream=0):
+    """laga_res_fwd with raw device addresses (ints; 0 for what is off)."""
+    _check(load().laga_res_fwd(ctypes.byref(dims), x, y, gate, alpha, gamma_post, gamma_pre, x_out,
+                               h, ck_y, ck_x, stat_post, stat_pre, stream), "laga_res_fwd")
+
+
+def res_workspace_bytes(dims: LagaResDims) -> int:
+    return int(load().laga_res_workspace_bytes(ctypes.byref(dims)))
+
+
+def res_bwd(dims: LagaResDims, dx_out, dh, kept_y, kept_x, stat_post, stat_pre, gate, alpha,
+            gamma_post, gamma_pre, dx, dy, dgate, dalpha, dgamma_post, dgamma_pre, ws, ws_bytes,
+            stream=0):
+    """laga_res_bwd with raw device addresses (ints; 0 for what is off)."""
+    _check(load().laga_res_bwd(ctypes.byref(dims), dx_out, dh, kept_y, kept_x, stat_post, stat_pre,
+                               gate, alpha, gamma_post, gamma_pre, dx, dy, dgate, dalpha,
+                               dgamma_post, dgamma_pre, ws, ws_bytes, stream), "laga_res_bwd")
+
+
+def ckpt_row_bytes(d: int) -> int:
+    """Bytes of one checkpoint row of d channels (0: not a valid width)."""
+    return int(load().laga_ckpt_row_bytes(d))
+
+
+def ckpt_pack(rows, d, dtype, x, ck, stream=0):
+    """laga_ckpt_pack with raw device addresses (ints); dtype "bf16" or "fp32"."""
+    _check(load().laga_ckpt_pack(rows, d, DTYPES[dtype], x, ck, stream), "laga_ckpt_pack")
+
+
+def ckpt_unpack(rows, d, dtype, ck, x, stream=0):
+    """laga_ckpt_unpack with raw device addresses (ints)."""
+    _check(load().laga_ckpt_unpack(rows, d, DTYPES[dtype], ck, x, stream), "laga_ckpt_unpack")
+
+
+def ckpt_dw_workspace_bytes(rows, d, n, dy_dtype) -> int:
+    return int(load().laga_ckpt_dw_workspace_bytes(rows, d, n, DTYPES[dy_dtype]))
+
+
+def ckpt_dw(rows, d, n, dy_dtype, ck, dy, gamma, dw, ws, ws_bytes, stream=0):
+    """laga_ckpt_dw with raw device addresses (ints; gamma 0: no row gain)."""
+    _check(load().laga_ckpt_dw(rows, d, n, DTYPES[dy_dtype], ck, dy, gamma, dw, ws, ws_bytes,
+                               stream), "laga_ckpt_dw")

@@ -8,6 +8,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "ops.h"
 #include "sm100.cuh"
 
 namespace laga {
@@ -305,6 +306,192 @@ laga_status laga_bwd_overlap(const laga_dims* dims, const void* q, const void* c
                   saved_bytes, ws_bwd, bwd_bytes, static_cast<cudaStream_t>(stream),
                   static_cast<cudaStream_t>(aux_stream), static_cast<cudaEvent_t>(fork_event),
                   static_cast<cudaEvent_t>(join_event));
+}
+
+}  // extern "C"
+
+// ------------------------------------------------- residual stream, 8 bits
+namespace {
+// One tensor argument: required tensors must be there, every given pointer
+// must be aligned.  The first problem in argument order wins, missing
+// pointers before misaligned ones.
+struct PtrCheck {
+  bool missing = false, crooked = false;
+  void need(bool required, const void* p) {
+    if (!required) return;
+    if (!p) missing = true;
+    else if (!aligned16(p)) crooked = true;
+  }
+  laga_status status() const {
+    return missing ? LAGA_ERR_ARG : crooked ? LAGA_ERR_ALIGN : LAGA_OK;
+  }
+};
+
+// Launches under `f`; nothing thrown on the host side crosses the ABI.
+template <typename F>
+laga_status run_launches(const char* name, F f) {
+  try {
+    NvtxCall range_(name);
+    return f();
+  } catch (...) {
+    return LAGA_ERR_CUDA;
+  }
+}
+
+bool dtype_ok(laga_dtype t) { return t == LAGA_BF16 || t == LAGA_FP32; }
+}  // namespace
+
+extern "C" {
+
+laga_status laga_res_fwd(const laga_res_dims* dims, const void* x, const void* y,
+                         const void* gate, const float* alpha, const float* gamma_post,
+                         const float* gamma_pre, void* x_out, void* h, void* ck_y, void* ck_x,
+                         float* stat_post, float* stat_pre, void* stream) {
+  t_launches = 0;
+  laga_status s = res_check(dims);
+  if (s != LAGA_OK) return s;
+  const laga_res_dims& d = *dims;
+  if (d.rows == 0) return LAGA_OK;
+  const bool post = d.post, pre = d.pre, ckpt = d.ckpt;
+  PtrCheck c;
+  c.need(true, x);
+  c.need(post, y);
+  c.need(post && d.gate != LAGA_GATE_NONE, gate);
+  c.need(post, alpha);
+  c.need(post && d.norm_post != LAGA_NORM_NONE, gamma_post);
+  c.need(pre, gamma_pre);
+  c.need(post, x_out);
+  c.need(pre, h);
+  c.need(post && ckpt, ck_y);
+  c.need(pre && ckpt, ck_x);
+  c.need(post, stat_post);
+  c.need(pre, stat_pre);
+  if ((s = c.status()) != LAGA_OK) return s;
+  ResPtrs p;
+  p.x = x; p.y = y; p.gate = gate; p.alpha = alpha;
+  p.gamma_post = gamma_post; p.gamma_pre = gamma_pre;
+  p.x_out = x_out; p.h = h; p.ck_y = ck_y; p.ck_x = ck_x;
+  p.stat_post = stat_post; p.stat_pre = stat_pre;
+  return run_launches("laga_res_fwd", [&] {
+    const laga_status e = err_word(&p.err);
+    return e != LAGA_OK ? e
+                        : cuda_status(launch_res_fwd(d, p, static_cast<cudaStream_t>(stream)));
+  });
+}
+
+size_t laga_res_workspace_bytes(const laga_res_dims* dims) {
+  return res_check(dims) == LAGA_OK ? res_ws_bytes(*dims) : 0;
+}
+
+laga_status laga_res_bwd(const laga_res_dims* dims, const void* dx_out, const void* dh,
+                         const void* kept_y, const void* kept_x, const float* stat_post,
+                         const float* stat_pre, const void* gate, const float* alpha,
+                         const float* gamma_post, const float* gamma_pre, void* dx, void* dy,
+                         void* dgate, float* dalpha, float* dgamma_post, float* dgamma_pre,
+                         void* ws, size_t ws_bytes, void* stream) {
+  t_launches = 0;
+  laga_status s = res_check(dims);
+  if (s != LAGA_OK) return s;
+  const laga_res_dims& d = *dims;
+  const bool post = d.post, pre = d.pre, some = d.rows > 0;
+  const bool gated = post && d.gate != LAGA_GATE_NONE;
+  const bool gain = post && d.norm_post != LAGA_NORM_NONE;
+  const size_t need_bytes = res_ws_bytes(d);
+  PtrCheck c;
+  c.need(some && (!pre || dx_out), dx_out);
+  c.need(some && pre, dh);
+  c.need(some && post, kept_y);
+  c.need(some && pre, kept_x);
+  c.need(some && post, stat_post);
+  c.need(some && pre, stat_pre);
+  c.need(some && gated, gate);
+  c.need(some && post, alpha);
+  c.need(some && gain, gamma_post);
+  c.need(some && pre, gamma_pre);
+  c.need(some && pre, dx);
+  c.need(some && post, dy);
+  c.need(some && gated, dgate);
+  c.need(post, dalpha);
+  c.need(gain, dgamma_post);
+  c.need(pre, dgamma_pre);
+  c.need(need_bytes > 0 && ws, ws);
+  if ((s = c.status()) != LAGA_OK) return s;
+  if (need_bytes > 0 && (!ws || ws_bytes < need_bytes)) return LAGA_ERR_WORKSPACE;
+  ResPtrs p;
+  p.dx_out = dx_out; p.dh = dh; p.kept_y = kept_y; p.kept_x = kept_x;
+  p.stat_post = const_cast<float*>(stat_post); p.stat_pre = const_cast<float*>(stat_pre);
+  p.gate = gate; p.alpha = alpha; p.gamma_post = gamma_post; p.gamma_pre = gamma_pre;
+  p.dx = dx; p.dy = dy; p.dgate = dgate; p.dalpha = dalpha;
+  p.dgamma_post = dgamma_post; p.dgamma_pre = dgamma_pre;
+  p.ws = static_cast<unsigned char*>(ws);
+  return run_launches("laga_res_bwd", [&] {
+    const laga_status e = err_word(&p.err);
+    return e != LAGA_OK ? e
+                        : cuda_status(launch_res_bwd(d, p, static_cast<cudaStream_t>(stream)));
+  });
+}
+
+size_t laga_ckpt_row_bytes(int d) { return d >= 1 && d <= CK_MAX_D ? (size_t)ck_pitch(d) : 0; }
+
+laga_status laga_ckpt_pack(int rows, int d, laga_dtype dtype, const void* x, void* ck,
+                           void* stream) {
+  t_launches = 0;
+  if (rows < 0 || d < 1 || d > CK_MAX_D || !dtype_ok(dtype)) return LAGA_ERR_ARG;
+  PtrCheck c;
+  c.need(rows > 0, x);
+  c.need(rows > 0, ck);
+  if (c.status() != LAGA_OK) return c.status();
+  return run_launches("laga_ckpt_pack", [&] {
+    return cuda_status(launch_ckpt_pack(rows, d, dtype == LAGA_FP32, x, ck,
+                                        static_cast<cudaStream_t>(stream)));
+  });
+}
+
+laga_status laga_ckpt_unpack(int rows, int d, laga_dtype dtype, const void* ck, void* x,
+                             void* stream) {
+  t_launches = 0;
+  if (rows < 0 || d < 1 || d > CK_MAX_D || !dtype_ok(dtype)) return LAGA_ERR_ARG;
+  PtrCheck c;
+  c.need(rows > 0, ck);
+  c.need(rows > 0, x);
+  if (c.status() != LAGA_OK) return c.status();
+  return run_launches("laga_ckpt_unpack", [&] {
+    return cuda_status(launch_ckpt_unpack(rows, d, dtype == LAGA_FP32, ck, x,
+                                          static_cast<cudaStream_t>(stream)));
+  });
+}
+
+static bool dw_sizes_ok(int rows, int d, int n, laga_dtype dy_dtype) {
+  return rows >= 0 && d >= 1 && d <= CK_MAX_D && n >= 1 && n <= CK_MAX_N && dtype_ok(dy_dtype);
+}
+
+size_t laga_ckpt_dw_workspace_bytes(int rows, int d, int n, laga_dtype dy_dtype) {
+  return dw_sizes_ok(rows, d, n, dy_dtype) ? ckpt_dw_ws_bytes(rows, d, n, dy_dtype == LAGA_FP32)
+                                           : 0;
+}
+
+laga_status laga_ckpt_dw(int rows, int d, int n, laga_dtype dy_dtype, const void* ck,
+                         const void* dy, const float* gamma, float* dw, void* ws,
+                         size_t ws_bytes, void* stream) {
+  t_launches = 0;
+  if (!dw_sizes_ok(rows, d, n, dy_dtype)) return LAGA_ERR_ARG;
+  const size_t need_bytes = ckpt_dw_ws_bytes(rows, d, n, dy_dtype == LAGA_FP32);
+  PtrCheck c;
+  c.need(rows > 0, ck);
+  c.need(rows > 0, dy);
+  c.need(gamma != nullptr, gamma);
+  c.need(true, dw);
+  c.need(need_bytes > 0 && ws, ws);
+  if (c.status() != LAGA_OK) return c.status();
+  if (need_bytes > 0 && (!ws || ws_bytes < need_bytes)) return LAGA_ERR_WORKSPACE;
+  return run_launches("laga_ckpt_dw", [&] {
+    int* err = nullptr;
+    const laga_status e = err_word(&err);
+    return e != LAGA_OK ? e
+                        : cuda_status(launch_ckpt_dw(rows, d, n, dy_dtype == LAGA_FP32, ck, dy,
+                                                     gamma, dw, static_cast<unsigned char*>(ws),
+                                                     err, static_cast<cudaStream_t>(stream)));
+  });
 }
 
 laga_status laga_selftest_wait_timeout(void* stream) {
