@@ -16,30 +16,10 @@
 
 #include <algorithm>
 
-#include "ckpt8.cuh"
-#include "common.cuh"
-#include "kernels.h"
-#include "ops.h"
+#include "residual.cuh"
 
 namespace laga {
 namespace {
-
-constexpr int kSms = 152;           // persistent CTAs of a launch are counted against this
-
-struct ResArgs {
-  int rows, d;
-  int post, pre, norm_post, norm_pre, gate, ckpt;
-  float eps, inv_d;
-  ResPtrs x;
-  float *part_post, *part_pre, *part_alpha;   // column partials [slots, d], [slots]
-};
-
-// sigmoid(a) and 1 - sigmoid(a), each to fp32 accuracy (no cancellation)
-LAGA_DEVINL float2 sigmoid_pair(float a) {
-  const float e = expf(-fabsf(a));
-  const float r = __fdividef(1.f, 1.f + e);
-  return a >= 0.f ? make_float2(r, e * r) : make_float2(e * r, r);
-}
 
 template <typename T>
 LAGA_DEVINL float ld1(const void* p, long long i) { return to_f32(static_cast<const T*>(p)[i]); }
@@ -267,7 +247,9 @@ __global__ void __launch_bounds__(512) res_colsum_kernel(const float* part_post,
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Column partial slots of a backward launch
-int bwd_slots(const laga_res_dims& d) { return std::min(d.rows, 2 * kSms); }
+int bwd_slots(const laga_res_dims& d) {
+  return ring_ok(d, true) ? ring_slots(d) : std::min(d.rows, 2 * kSms);
+}
 
 ResArgs make_args(const laga_res_dims& d, const ResPtrs& x) {
   ResArgs a{};
@@ -315,6 +297,7 @@ size_t res_ws_bytes(const laga_res_dims& d) {
 cudaError_t launch_res_fwd(const laga_res_dims& d, const ResPtrs& x, cudaStream_t st) {
   if (d.rows == 0) return cudaSuccess;
   const ResArgs a = make_args(d, x);
+  if (ring_ok(d, false)) return launch_ring_fwd(d, a, st);
   const size_t smem = (size_t)d.d * 4;
   auto k = d.io_dtype == LAGA_FP32 ? res_fwd_rows_kernel<float> : res_fwd_rows_kernel<__nv_bfloat16>;
   cudaError_t e = allow_smem(k, smem);
@@ -331,7 +314,9 @@ cudaError_t launch_res_bwd(const laga_res_dims& d, const ResPtrs& x, cudaStream_
   a.part_pre = reinterpret_cast<float*>(x.ws + up256((size_t)slots * d.d * 4));
   a.part_alpha = reinterpret_cast<float*>(x.ws + 2 * up256((size_t)slots * d.d * 4));
   cudaError_t e;
-  if (d.rows > 0) {
+  if (d.rows > 0 && ring_ok(d, true)) {
+    if ((e = launch_ring_bwd(d, a, st)) != cudaSuccess) return e;
+  } else if (d.rows > 0) {
     const size_t smem = (size_t)d.d * 4;
     auto k = d.io_dtype == LAGA_FP32 ? res_bwd_rows_kernel<float>
                                      : res_bwd_rows_kernel<__nv_bfloat16>;
