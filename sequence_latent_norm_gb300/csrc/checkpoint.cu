@@ -26,14 +26,15 @@ __global__ void __launch_bounds__(256) ckpt_pack_kernel(const T* __restrict__ x,
     for (int k = 0; k < 4; ++k) {
       const int c = g * CK_GROUP + 4 * lane + k;
       t[k] = c < d ? to_f32(x[r * d + c]) : 0.f;
-      m = fmaxf(m, ck_mag(t[k]));
+      m = ck_max(m, t[k]);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 16; o > 0; o >>= 1) m = ck_max(m, __shfl_xor_sync(0xffffffffu, m, o));
     float inv;
     const int s = ck_scale(m, &inv);
-    *reinterpret_cast<uint32_t*>(row + g * CK_GROUP + 4 * lane) =
-        ck_code2(t[0], t[1], inv) | ck_code2(t[2], t[3], inv) << 16;
+    const uint32_t q = ck_code2(make_float2(t[0], t[1]), inv) |
+                       ck_code2(make_float2(t[2], t[3]), inv) << 16;
+    *reinterpret_cast<uint32_t*>(row + g * CK_GROUP + 4 * lane) = s == CK_NAN ? 0u : q;
     if (lane == 0) row[cols + g] = (uint8_t)s;
     if (g == 0)
       for (int i = cols + groups + lane; i < pitch; i += 32) row[i] = 0;

@@ -69,15 +69,16 @@ LAGA_DEVINL void quantise_row(int d, uint8_t* row, F v) {
     for (int k = 0; k < 4; ++k) {
       const int c = g * CK_GROUP + k * 32 + lane;
       t[k] = c < d ? v(c) : 0.f;
-      m = fmaxf(m, ck_mag(t[k]));
+      m = ck_max(m, t[k]);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 16; o > 0; o >>= 1) m = ck_max(m, __shfl_xor_sync(0xffffffffu, m, o));
     float inv;
     const int s = ck_scale(m, &inv);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      row[g * CK_GROUP + k * 32 + lane] = (uint8_t)ck_code2(t[k], 0.f, inv);
+      row[g * CK_GROUP + k * 32 + lane] =
+          s == CK_NAN ? 0 : (uint8_t)ck_code2(make_float2(t[k], 0.f), inv);
     if (lane == 0) row[cols + g] = (uint8_t)s;
   }
   for (int i = cols + cols / CK_GROUP + threadIdx.x; i < ck_pitch(d); i += GT) row[i] = 0;

@@ -19,11 +19,17 @@ struct ResArgs {
   float *part_post, *part_pre, *part_alpha;   // column partials [slots, d], [slots]
 };
 
-// sigmoid(a) and 1 - sigmoid(a), each to fp32 accuracy (no cancellation)
+// sigmoid(a) = 1 / (1 + e^-a) and 1 - sigmoid(a) = e^-a sigmoid(a), without
+// cancellation on either side.  e^-a is 2^(-a log2 e) by the hardware's
+// exponential: the product's rounding leaves it within 0.7 |a| 2^-24 and 2 ulp
+// of itself.  Below -87 the sigmoid stays at e^-87, the end of the normal
+// range, so that e^-a is finite.
 LAGA_DEVINL float2 sigmoid_pair(float a) {
-  const float e = expf(-fabsf(a));
-  const float r = __fdividef(1.f, 1.f + e);
-  return a >= 0.f ? make_float2(r, e * r) : make_float2(e * r, r);
+  float e, s;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(a), "f"(-87.f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return make_float2(s, e * s);
 }
 
 // Launches of the ring kernels (residual_ring.cu); ring_ok says whether they

@@ -47,51 +47,50 @@ LAGA_DEVINL void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t*
       : "memory");
 }
 
-// 8 consecutive elements
-template <typename T>
-struct Vec;
-template <>
-struct Vec<__nv_bfloat16> {
-  static LAGA_DEVINL void load(const uint8_t* p, int v, float (&f)[8]) {
-    const uint4 w = reinterpret_cast<const uint4*>(p)[v];
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// 8 consecutive elements, as pairs for the packed fp32 instructions
+struct V8 {
+  float2 v[4];
+};
+LAGA_DEVINL float2 both(float a) { return make_float2(a, a); }
+LAGA_DEVINL float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+LAGA_DEVINL float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+LAGA_DEVINL float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
+LAGA_DEVINL void load8(const uint8_t* p, int v, V8& f, __nv_bfloat16) {
+  const uint4 w = reinterpret_cast<const uint4*>(p)[v];
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      f[2 * k] = __uint_as_float(u[k] << 16);
-      f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-    }
-  }
-  static LAGA_DEVINL void store(void* p, long long v, const float (&f)[8]) {
-    reinterpret_cast<uint4*>(p)[v] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
-                                                pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-  }
-};
-template <>
-struct Vec<float> {
-  static LAGA_DEVINL void load(const uint8_t* p, int v, float (&f)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[2 * v];
-    const float4 b = reinterpret_cast<const float4*>(p)[2 * v + 1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  }
-  static LAGA_DEVINL void store(void* p, long long v, const float (&f)[8]) {
-    reinterpret_cast<float4*>(p)[2 * v] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[2 * v + 1] = make_float4(f[4], f[5], f[6], f[7]);
-  }
-};
+  for (int k = 0; k < 4; ++k)
+    f.v[k] = make_float2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xffff0000u));
+}
+LAGA_DEVINL void load8(const uint8_t* p, int v, V8& f, float) {
+  const float4 a = reinterpret_cast<const float4*>(p)[2 * v];
+  const float4 b = reinterpret_cast<const float4*>(p)[2 * v + 1];
+  f.v[0] = make_float2(a.x, a.y); f.v[1] = make_float2(a.z, a.w);
+  f.v[2] = make_float2(b.x, b.y); f.v[3] = make_float2(b.z, b.w);
+}
+LAGA_DEVINL void store8(void* p, long long v, const V8& f, __nv_bfloat16) {
+  reinterpret_cast<uint4*>(p)[v] =
+      make_uint4(pack_bf16(f.v[0].x, f.v[0].y), pack_bf16(f.v[1].x, f.v[1].y),
+                 pack_bf16(f.v[2].x, f.v[2].y), pack_bf16(f.v[3].x, f.v[3].y));
+}
+LAGA_DEVINL void store8(void* p, long long v, const V8& f, float) {
+  reinterpret_cast<float4*>(p)[2 * v] = make_float4(f.v[0].x, f.v[0].y, f.v[1].x, f.v[1].y);
+  reinterpret_cast<float4*>(p)[2 * v + 1] = make_float4(f.v[2].x, f.v[2].y, f.v[3].x, f.v[3].y);
+}
 
 // A row's gain: in shared memory as two planes of four floats per vector, so
 // that 16-byte accesses of neighbouring threads do not collide, or global.
 struct Gain {
   const float *sm, *g;
   int nvec;
-  LAGA_DEVINL void load(int v, float (&f)[8]) const {
+  LAGA_DEVINL void load(int v, V8& f) const {
     const float4 a = sm ? reinterpret_cast<const float4*>(sm)[v]
                         : __ldg(reinterpret_cast<const float4*>(g) + 2 * v);
     const float4 b = sm ? reinterpret_cast<const float4*>(sm)[nvec + v]
                         : __ldg(reinterpret_cast<const float4*>(g) + 2 * v + 1);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    f.v[0] = make_float2(a.x, a.y); f.v[1] = make_float2(a.z, a.w);
+    f.v[2] = make_float2(b.x, b.y); f.v[3] = make_float2(b.z, b.w);
   }
 };
 
@@ -132,39 +131,36 @@ LAGA_DEVINL void team_sum(float (&v)[K], float (*red)[THREADS / 32][4], int team
 
 // One vector of normalised values as codes, with its group's scale (16
 // neighbouring lanes hold the group; every lane of the warp takes part).
-LAGA_DEVINL void quantise8(uint8_t* row, int v, int cols, const float (&f)[8]) {
+LAGA_DEVINL void quantise8(uint8_t* row, int v, int cols, const V8& f) {
   float m = 0.f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) m = fmaxf(m, ck_mag(f[k]));
+  for (int k = 0; k < 4; ++k) m = ck_max(ck_max(m, f.v[k].x), f.v[k].y);
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 8; o > 0; o >>= 1) m = ck_max(m, __shfl_xor_sync(0xffffffffu, m, o));
   float inv;
   const int s = ck_scale(m, &inv);
   if (v * 8 < cols) {
-    reinterpret_cast<uint2*>(row)[v] =
-        make_uint2(ck_code2(f[0], f[1], inv) | ck_code2(f[2], f[3], inv) << 16,
-                   ck_code2(f[4], f[5], inv) | ck_code2(f[6], f[7], inv) << 16);
+    const uint32_t lo = ck_code2(f.v[0], inv) | ck_code2(f.v[1], inv) << 16;
+    const uint32_t hi = ck_code2(f.v[2], inv) | ck_code2(f.v[3], inv) << 16;
+    reinterpret_cast<uint2*>(row)[v] = s == CK_NAN ? make_uint2(0, 0) : make_uint2(lo, hi);
     if ((v & 15) == 0) row[cols + (v >> 4)] = (uint8_t)s;
   }
 }
 
 // One vector of a kept row: the checkpoint's values, or (kept - mean) / std.
 template <typename T>
-LAGA_DEVINL void kept8(const uint8_t* row, int ckpt, int cols, int v, float2 st, float (&f)[8]) {
+LAGA_DEVINL void kept8(const uint8_t* row, int ckpt, int cols, int v, float2 st, V8& f) {
   if (ckpt) {
     const uint2 q = reinterpret_cast<const uint2*>(row)[v];
     const float unit = ck_unit(row[cols + (v >> 4)]);
-    const uint32_t c[4] = {q.x & 0xffffu, q.x >> 16, q.y & 0xffffu, q.y >> 16};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 t = ck_value2(c[k], unit);
-      f[2 * k] = t.x;
-      f[2 * k + 1] = t.y;
-    }
+    f.v[0] = ck_value2(q.x & 0xffffu, unit);
+    f.v[1] = ck_value2(q.x >> 16, unit);
+    f.v[2] = ck_value2(q.y & 0xffffu, unit);
+    f.v[3] = ck_value2(q.y >> 16, unit);
   } else {
-    Vec<T>::load(row, v, f);
+    load8(row, v, f, T());
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = (f[k] - st.x) * st.y;
+    for (int k = 0; k < 4; ++k) f.v[k] = mul2(add2(f.v[k], both(-st.x)), both(st.y));
   }
 }
 
@@ -246,36 +242,41 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (!mbar_wait(&ring.bar[stage], phase, p.x.err)) return;
     const uint8_t* buf = ring.buf + stage * q.stage_bytes;
     const uint8_t *bx = buf + q.src[F_X].off, *by = buf + q.src[F_Y].off, *bg = buf + q.src[F_G].off;
-    float x[NV][8];
+    V8 x[NV];
     if (p.post) {
       float2 st = make_float2(0.f, 1.f);
       if (p.norm_post != LAGA_NORM_NONE) {
         if (p.norm_post == LAGA_NORM_LAYER) {
-          float s[1] = {0.f};
+          float2 t = both(0.f);
 #pragma unroll
           for (int i = 0; i < NV; ++i) {
             const int v = i * TEAM + tl;
             if (v < nvec) {
-              float y[8];
-              Vec<T>::load(by, v, y);
+              V8 y;
+              load8(by, v, y, T());
 #pragma unroll
-              for (int k = 0; k < 8; ++k) s[0] += y[k];
+              for (int k = 0; k < 4; ++k) t = add2(t, y.v[k]);
             }
           }
+          float s[1] = {t.x + t.y};
           team_sum<TEAM, 1>(s, red, ring.team, slot);
           st.x = s[0] * p.inv_d;
         }
-        float s[1] = {0.f};
+        float2 t = both(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int v = i * TEAM + tl;
           if (v < nvec) {
-            float y[8];
-            Vec<T>::load(by, v, y);
+            V8 y;
+            load8(by, v, y, T());
 #pragma unroll
-            for (int k = 0; k < 8; ++k) s[0] += (y[k] - st.x) * (y[k] - st.x);
+            for (int k = 0; k < 4; ++k) {
+              const float2 c = add2(y.v[k], both(-st.x));
+              t = fma2(c, c, t);
+            }
           }
         }
+        float s[1] = {t.x + t.y};
         team_sum<TEAM, 1>(s, red, ring.team, slot);
         st.y = 1.f / sqrtf(s[0] * p.inv_d + p.eps);
       }
@@ -283,35 +284,35 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = i * TEAM + tl;
-        float y[8];
+        V8 y;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[i][k] = y[k] = 0.f;
+        for (int k = 0; k < 4; ++k) x[i].v[k] = y.v[k] = both(0.f);
         if (v < nvec) {
-          float a[8], g[8];
-          Vec<T>::load(bx, v, x[i]);
-          Vec<T>::load(by, v, y);
+          V8 g;
+          load8(bx, v, x[i], T());
+          load8(by, v, y, T());
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y.v[k] = mul2(add2(y.v[k], both(-st.x)), both(st.y));
           if (p.norm_post != LAGA_NORM_NONE) {
             g_post.load(v, g);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) g.v[k] = mul2(g.v[k], y.v[k]);
           } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) g[k] = 1.f;
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            y[k] = (y[k] - st.x) * st.y;
-            g[k] *= y[k];
+            g = y;
           }
           if (p.gate == LAGA_GATE_FULL) {
-            Vec<T>::load(bg, v, a);
+            V8 a;
+            load8(bg, v, a, T());
 #pragma unroll
-            for (int k = 0; k < 8; ++k) g[k] *= sigmoid_pair(a[k]).x;
-          } else {
+            for (int k = 0; k < 4; ++k)
+              g.v[k] = mul2(g.v[k], make_float2(sigmoid_pair(a.v[k].x).x, sigmoid_pair(a.v[k].y).x));
+          } else if (p.gate == LAGA_GATE_TOKEN) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) g[k] *= tok_s;
+            for (int k = 0; k < 4; ++k) g.v[k] = mul2(g.v[k], both(tok_s));
           }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[i][k] += alpha * g[k];
-          Vec<T>::store(p.x.x_out, r * nvec + v, x[i]);
+          for (int k = 0; k < 4; ++k) x[i].v[k] = fma2(both(alpha), g.v[k], x[i].v[k]);
+          store8(p.x.x_out, r * nvec + v, x[i], T());
         }
         if (p.ckpt) quantise8(static_cast<uint8_t*>(p.x.ck_y) + r * pitch, v, cols, y);
       }
@@ -323,8 +324,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int i = 0; i < NV; ++i) {
         const int v = i * TEAM + tl;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[i][k] = 0.f;
-        if (v < nvec) Vec<T>::load(bx, v, x[i]);
+        for (int k = 0; k < 4; ++k) x[i].v[k] = both(0.f);
+        if (v < nvec) load8(bx, v, x[i], T());
       }
     }
     // the row buffer has been read by everyone: refill it
@@ -333,34 +334,39 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (p.pre) {
       float2 st = make_float2(0.f, 1.f);
       if (p.norm_pre == LAGA_NORM_LAYER) {
-        float s[1] = {0.f};
+        float2 t = both(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) s[0] += x[i][k];
+          for (int k = 0; k < 4; ++k) t = add2(t, x[i].v[k]);
+        float s[1] = {t.x + t.y};
         team_sum<TEAM, 1>(s, red, ring.team, slot);
         st.x = s[0] * p.inv_d;
       }
-      float s[1] = {0.f};
+      float2 t = both(0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (i * TEAM + tl < nvec)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) s[0] += (x[i][k] - st.x) * (x[i][k] - st.x);
+          for (int k = 0; k < 4; ++k) {
+            const float2 c = add2(x[i].v[k], both(-st.x));
+            t = fma2(c, c, t);
+          }
+      float s[1] = {t.x + t.y};
       team_sum<TEAM, 1>(s, red, ring.team, slot);
       st.y = 1.f / sqrtf(s[0] * p.inv_d + p.eps);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = i * TEAM + tl;
         if (v < nvec) {
-          float g[8];
+          V8 g;
           g_pre.load(v, g);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            x[i][k] = (x[i][k] - st.x) * st.y;
-            g[k] *= x[i][k];
+          for (int k = 0; k < 4; ++k) {
+            x[i].v[k] = mul2(add2(x[i].v[k], both(-st.x)), both(st.y));
+            g.v[k] = mul2(g.v[k], x[i].v[k]);
           }
-          Vec<T>::store(p.x.h, r * nvec + v, g);
+          store8(p.x.h, r * nvec + v, g, T());
         }
         if (p.ckpt) quantise8(static_cast<uint8_t*>(p.x.ck_x) + r * pitch, v, cols, x[i]);
       }
@@ -391,11 +397,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int s = 0; s < min(q.depth, n_it); ++s) ring.issue(q, s, first + s * G);
   const bool gain = p.norm_post != LAGA_NORM_NONE;
   const float alpha = p.post ? *p.x.alpha : 0.f;
-  float acc_post[NV][8], acc_pre[NV][8], d_alpha = 0.f;
+  V8 acc_post[NV], acc_pre[NV];
+  float d_alpha = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc_post[i][k] = acc_pre[i][k] = 0.f;
+    for (int k = 0; k < 4; ++k) acc_post[i].v[k] = acc_pre[i].v[k] = both(0.f);
   int slot = 0, stage = 0;
   uint32_t phase = 0;
   for (int it = 0; it < n_it; ++it) {
@@ -411,77 +418,89 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint8_t *bx = buf + q.src[B_X].off, *by = buf + q.src[B_Y].off, *bg = buf + q.src[B_G].off;
     float m0 = 0.f, m1 = 0.f;
     if (p.pre) {
-      float s[2] = {0.f, 0.f};
+      float2 t0 = both(0.f), t1 = both(0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = i * TEAM + tl;
         if (v < nvec) {
-          float dh[8], xh[8], g[8];
-          Vec<T>::load(bh, v, dh);
+          V8 dh, xh, g;
+          load8(bh, v, dh, T());
           kept8<T>(bx, p.ckpt, cols, v, st_pre, xh);
           g_pre.load(v, g);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            acc_pre[i][k] += dh[k] * xh[k];
-            const float e = dh[k] * g[k];
-            s[0] += e;
-            s[1] += e * xh[k];
+          for (int k = 0; k < 4; ++k) {
+            acc_pre[i].v[k] = fma2(dh.v[k], xh.v[k], acc_pre[i].v[k]);
+            const float2 e = mul2(dh.v[k], g.v[k]);
+            t0 = add2(t0, e);
+            t1 = fma2(e, xh.v[k], t1);
           }
         }
       }
+      float s[2] = {t0.x + t0.y, t1.x + t1.y};
       team_sum<TEAM, 2>(s, red, ring.team, slot);
       m0 = p.norm_pre == LAGA_NORM_LAYER ? s[0] * p.inv_d : 0.f;
       m1 = s[1] * p.inv_d;
     }
-    float f[NV][8], s[4] = {0.f, 0.f, 0.f, 0.f};   // sums: f, f y^, dx s z, token gate
+    V8 f[NV];
+    float2 t0 = both(0.f), t1 = t0, t2 = t0, t3 = t0;   // sums: f, f y^, dx s z, token gate
     float2 tok_s = make_float2(1.f, 0.f);
     if (p.gate == LAGA_GATE_TOKEN) tok_s = sigmoid_pair(tok);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = i * TEAM + tl;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[i][k] = 0.f;
+      for (int k = 0; k < 4; ++k) f[i].v[k] = both(0.f);
       if (v < nvec) {
-        float D[8];
+        V8 D;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) D[k] = 0.f;
-        if (p.x.dx_out) Vec<T>::load(bd, v, D);
+        for (int k = 0; k < 4; ++k) D.v[k] = both(0.f);
+        if (p.x.dx_out) load8(bd, v, D, T());
         if (p.pre) {
-          float dh[8], xh[8], g[8];
-          Vec<T>::load(bh, v, dh);
+          V8 dh, xh, g;
+          load8(bh, v, dh, T());
           kept8<T>(bx, p.ckpt, cols, v, st_pre, xh);
           g_pre.load(v, g);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) D[k] += st_pre.y * (dh[k] * g[k] - m0 - xh[k] * m1);
-          Vec<T>::store(p.x.dx, r * nvec + v, D);
+          for (int k = 0; k < 4; ++k) {
+            const float2 e = fma2(xh.v[k], both(-m1), fma2(dh.v[k], g.v[k], both(-m0)));
+            D.v[k] = fma2(both(st_pre.y), e, D.v[k]);
+          }
+          store8(p.x.dx, r * nvec + v, D, T());
         }
         if (p.post) {
-          float y[8], g[8], da[8];
+          V8 y, g, a;
           kept8<T>(by, p.ckpt, cols, v, st_post, y);
           if (gain) {
             g_post.load(v, g);
           } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) g[k] = 1.f;
+            for (int k = 0; k < 4; ++k) g.v[k] = both(1.f);
           }
-          if (p.gate == LAGA_GATE_FULL) Vec<T>::load(bg, v, da);
+          if (p.gate == LAGA_GATE_FULL) load8(bg, v, a, T());
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float2 sg = p.gate == LAGA_GATE_FULL ? sigmoid_pair(da[k]) : tok_s;
-            const float z = y[k] * g[k], dz = alpha * D[k] * sg.x;
-            s[2] += D[k] * sg.x * z;
-            da[k] = dz * sg.y * z;
-            s[3] += da[k];
-            acc_post[i][k] += dz * y[k];
-            f[i][k] = dz * g[k];
-            s[0] += f[i][k];
-            s[1] += f[i][k] * y[k];
+          for (int k = 0; k < 4; ++k) {
+            float2 s = both(tok_s.x), c = both(tok_s.y);
+            if (p.gate == LAGA_GATE_FULL) {
+              const float2 u = sigmoid_pair(a.v[k].x), w = sigmoid_pair(a.v[k].y);
+              s = make_float2(u.x, w.x);
+              c = make_float2(u.y, w.y);
+            }
+            const float2 Ds = mul2(D.v[k], s), z = mul2(y.v[k], g.v[k]);
+            const float2 u = mul2(Ds, z), dz = mul2(both(alpha), Ds);
+            t2 = add2(t2, u);
+            a.v[k] = mul2(mul2(both(alpha), u), c);
+            t3 = add2(t3, a.v[k]);
+            acc_post[i].v[k] = fma2(dz, y.v[k], acc_post[i].v[k]);
+            f[i].v[k] = mul2(dz, g.v[k]);
+            t0 = add2(t0, f[i].v[k]);
+            t1 = fma2(f[i].v[k], y.v[k], t1);
           }
-          if (p.gate == LAGA_GATE_FULL) Vec<T>::store(p.x.dgate, r * nvec + v, da);
+          if (p.gate == LAGA_GATE_FULL) store8(p.x.dgate, r * nvec + v, a, T());
         }
       }
     }
     if (p.post) {
+      float s[4] = {t0.x + t0.y, t1.x + t1.y, t2.x + t2.y, t3.x + t3.y};
       team_sum<TEAM, 4>(s, red, ring.team, slot);
       d_alpha += s[2];
       if (p.gate == LAGA_GATE_TOKEN && tl == 0) static_cast<T*>(p.x.dgate)[r] = from_f32<T>(s[3]);
@@ -492,12 +511,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int v = i * TEAM + tl;
         if (v < nvec) {
           if (gain) {
-            float y[8];
+            V8 y;
             kept8<T>(by, p.ckpt, cols, v, st_post, y);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) f[i][k] = st_post.y * (f[i][k] - m0 - y[k] * m1);
+            for (int k = 0; k < 4; ++k)
+              f[i].v[k] = mul2(both(st_post.y),
+                               fma2(y.v[k], both(-m1), add2(f[i].v[k], both(-m0))));
           }
-          Vec<T>::store(p.x.dy, r * nvec + v, f[i]);
+          store8(p.x.dy, r * nvec + v, f[i], T());
         }
       }
     }
@@ -512,8 +533,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   for (int i = 0; i < NV; ++i) {
     const int v = i * TEAM + tl;
     if (v < nvec) {
-      if (p.post && gain) Vec<float>::store(p.part_post + first * p.d, v, acc_post[i]);
-      if (p.pre) Vec<float>::store(p.part_pre + first * p.d, v, acc_pre[i]);
+      if (p.post && gain) store8(p.part_post + first * p.d, v, acc_post[i], 0.f);
+      if (p.pre) store8(p.part_pre + first * p.d, v, acc_pre[i], 0.f);
     }
   }
   if (p.post && tl == 0) p.part_alpha[first] = d_alpha;
