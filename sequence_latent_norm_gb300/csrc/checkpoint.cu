@@ -1,5 +1,4 @@
-// 8-bit checkpoints (include/laga.h: laga_ckpt_pack, laga_ckpt_unpack,
-// laga_ckpt_dw).
+// 8-bit checkpoints (include/laga.h: laga_ckpt_pack, laga_ckpt_unpack).
 #include <algorithm>
 
 #include "ckpt8.cuh"
@@ -63,43 +62,6 @@ __global__ void __launch_bounds__(256) ckpt_unpack_kernel(const uint8_t* __restr
   }
 }
 
-// dw tile of 64 channels x 64 columns per CTA, tokens in steps of 16.
-template <typename T>
-__global__ void __launch_bounds__(256) ckpt_dw_kernel(const uint8_t* __restrict__ ck,
-                                                      const T* __restrict__ dy,
-                                                      const float* __restrict__ gamma, float* dw,
-                                                      int rows, int d, int n) {
-  __shared__ float a[16][64], b[16][64];
-  const int c0 = blockIdx.x * 64, n0 = blockIdx.y * 64;
-  const int pitch = ck_pitch(d), cols = ck_cols(d);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (long long t0 = 0; t0 < rows; t0 += 16) {
-    for (int i = threadIdx.x; i < 16 * 64; i += 256) {
-      const int t = i >> 6, c = i & 63;
-      const bool in = t0 + t < rows;
-      const uint8_t* row = ck + (t0 + t) * pitch;
-      a[t][c] = in && c0 + c < d
-                    ? ck_value2(row[c0 + c], ck_unit(row[cols + (c0 + c) / CK_GROUP])).x
-                    : 0.f;
-      b[t][c] = in && n0 + c < n ? to_f32(dy[(t0 + t) * n + n0 + c]) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < 16; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += a[t][ty + 16 * i] * b[t][tx + 16 * j];
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int c = c0 + ty + 16 * i, k = n0 + tx + 16 * j;
-      if (c < d && k < n) dw[(long long)c * n + k] = acc[i][j] * (gamma ? gamma[c] : 1.f);
-    }
-}
-
 int warp_grid(int rows, int d) {
   const long long w = (long long)rows * (ck_cols(d) / CK_GROUP);
   return (int)std::min<long long>((w + 7) / 8, 152 * 8);
@@ -129,21 +91,6 @@ cudaError_t launch_ckpt_unpack(int rows, int d, bool fp32, const void* ck, void*
   else
     ckpt_unpack_kernel<__nv_bfloat16><<<warp_grid(rows, d), 256, 0, st>>>(
         static_cast<const uint8_t*>(ck), static_cast<__nv_bfloat16*>(x), rows, d);
-  return cudaGetLastError();
-}
-
-size_t ckpt_dw_ws_bytes(int, int, int, bool) { return 0; }
-
-cudaError_t launch_ckpt_dw(int rows, int d, int n, bool fp32, const void* ck, const void* dy,
-                           const float* gamma, float* dw, unsigned char*, int*, cudaStream_t st) {
-  LaunchScope ls_("ckpt_dw", st);
-  const dim3 grid((d + 63) / 64, (n + 63) / 64);
-  if (fp32)
-    ckpt_dw_kernel<float><<<grid, 256, 0, st>>>(static_cast<const uint8_t*>(ck),
-                                                static_cast<const float*>(dy), gamma, dw, rows, d, n);
-  else
-    ckpt_dw_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(
-        static_cast<const uint8_t*>(ck), static_cast<const __nv_bfloat16*>(dy), gamma, dw, rows, d, n);
   return cudaGetLastError();
 }
 

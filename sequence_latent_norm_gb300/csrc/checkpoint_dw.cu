@@ -1,0 +1,550 @@
+// Weight gradient from an 8-bit checkpoint (include/laga.h: laga_ckpt_dw):
+//   dw[c, j] = gamma[c] sum_t v[t, c] dy[t, j],   v = code * 2^e,
+// M = channels, N = columns of dy, K = tokens, on the tensor cores.  v is a
+// bf16 number exactly, so the codes are turned into bf16 operand tiles on the
+// way through shared memory and never exist in 16 bits in HBM: 1 byte per
+// element is read instead of 2, and no separate unpacking pass (3 bytes per
+// element) runs.  An fp32 dy enters as three bf16 pieces, dy = p0 + p1 + p2
+// with every piece the rounded rest (24 significand bits in all), one after
+// the other against the same v tile: three products instead of one, and
+// nothing of dy is lost.
+//
+// Pairs of CTAs (two-CTA clusters, cta_group::2, M256 pair MMAs): CTA rank r
+// holds one group of 128 channels and half of the tile's BN columns.  16 warps:
+//   0       TMA producer of dy tiles      (ring of NB stages, 64 tokens each)
+//   1       TMA producer of code and scale tiles                 (NC stages)
+//   2       MMA issuer (rank 0)
+//   3       TMEM allocator
+//   4-7     epilogue: TMEM -> registers -> times gamma -> swizzled 32 x 32
+//           boxes -> TMA stores, one accumulator while the other is filled
+//   8-15    decoders: code tile -> bf16 tile, MN-major, 128-byte swizzled
+//           (ring of NA stages)
+// A decoder thread turns 32 codes per 64-token step into bf16 with ~3
+// integer and multiply instructions each; the pair's MMAs of that step take
+// 2 BN clocks, so the decoders set the pace below BN = 128 and stay hidden
+// above.
+//
+// Work split: tile counts rarely fill the 76 pairs evenly, so whole rounds of
+// one tile per pair run first, and the token steps of the tiles that are left
+// are dealt out evenly over all pairs, at least MIN_STEPS in a row each.  A
+// pair's part of such a tile is a fragment in the workspace; dw_join adds a
+// tile's fragments in token order.  Which pair takes what depends on the
+// sizes alone, so every run adds in the same order.
+#include <algorithm>
+
+#include "ckpt8.cuh"
+#include "common.cuh"
+#include "kernels.h"
+#include "ops.h"
+#include "sm100.cuh"
+#include "tmap.h"
+
+namespace laga {
+namespace {
+using namespace sm100;
+
+constexpr int KT = 64;                       // tokens per step
+constexpr int NA = 4, NB = 6, NC = 3;        // ring stages: v tiles, dy tiles, codes
+constexpr int BOX8K = 64 * 64 * 2;           // a 64 x 64 bf16 box
+constexpr int A_BYTES = 2 * BOX8K;           // 64 tokens x 128 channels
+constexpr int B_BYTES = 2 * BOX8K;           // 64 tokens x up to 128 columns
+constexpr int CODE_BYTES = KT * CK_GROUP;
+constexpr int SCALE_BYTES = KT * 16;         // 16 groups' scale bytes of each token
+constexpr int C_BYTES = CODE_BYTES + SCALE_BYTES;
+constexpr int EPI_BOX = 32 * 128, EPI_BUFS = 2;
+constexpr int A_OFF = 0, B_OFF = NA * A_BYTES, E_OFF = B_OFF + NB * B_BYTES;
+constexpr int C_OFF = E_OFF + 4 * EPI_BUFS * EPI_BOX;
+constexpr int SMEM_BYTES = C_OFF + NC * C_BYTES + 1024;
+constexpr int THREADS = 512, N_DEC = 8;
+constexpr int TMEM_COLS = 512, ACC_COLS = 256;
+constexpr int PAIRS = 76;                    // one pair per two SMs
+constexpr int MIN_STEPS = 8;
+
+struct DwMaps {
+  CUtensorMap codes, scales, dy, out, frag;
+};
+struct DwParams {
+  int groups, cols, d, n;
+  int n_tiles, tiles;
+  int steps, pieces;       // token steps of a tile; bf16 pieces of dy
+  int rounds;              // whole rounds: one tile per pair each
+  long long chunk;         // steps of the left-over tiles that each pair takes
+  int max_frags;           // fragments per pair
+  const float* gamma;
+  int* err;
+};
+
+// One piece of a pair's work: steps [k0, k0 + kn) of tile t; frag < 0: the
+// whole tile, stored to the output.
+struct Piece {
+  int t, k0, kn, frag;
+};
+// The i-th piece of pair p; false past the last one.
+LAGA_DEVINL bool piece_of(const DwParams& p, int pair, int i, Piece& w) {
+  if (i < p.rounds) {
+    w = {i * PAIRS + pair, 0, p.steps, -1};
+    return true;
+  }
+  i -= p.rounds;
+  const int first_tile = p.rounds * PAIRS;
+  const long long total = (long long)(p.tiles - first_tile) * p.steps;
+  const long long u0 = min(pair * p.chunk, total);
+  const long long u1 = min(u0 + p.chunk, total);
+  if (u0 >= u1) return false;
+  const long long ta = u0 / p.steps, tb = (u1 - 1) / p.steps;   // its first and last tile
+  if (ta + i > tb) return false;
+  const long long lo = max(u0, (ta + i) * p.steps), hi = min(u1, (ta + i + 1) * p.steps);
+  w = {first_tile + (int)(ta + i), (int)(lo - (ta + i) * p.steps), (int)(hi - lo),
+       pair * p.max_frags + i};
+  return true;
+}
+
+// Two codes (bytes b0, b1 of the selected halves) as bf16: sign, exponent and
+// significand moved into place stand for the code's value times 2^-120
+// (e4m3's bias is 7, bf16's 127), subnormal codes included; m1 brings that and
+// the group's 2^e back, exactly.
+LAGA_DEVINL uint32_t bf16_pair(uint32_t w, uint32_t sel, uint32_t m1) {
+  const uint32_t t = __byte_perm(w, 0u, sel);
+  const uint32_t r = ((t >> 4) & 0x07f007f0u) | (t & 0x80008000u);
+  uint32_t o;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(r), "r"(m1));
+  return o;
+}
+LAGA_DEVINL uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t o;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(a), "r"(b));
+  return o;
+}
+
+// 16 codes as two 16-byte chunks of bf16 values
+LAGA_DEVINL void decode16(const uint4& q, uint32_t byte, uint4& lo, uint4& hi) {
+  // 2^(e + 120) has the exponent field byte + 120; what does not fit in one
+  // bf16 factor goes into a second one
+  const uint32_t f1 = min(byte + 120u, 254u), f2 = byte + 247u - f1;
+  uint32_t m1 = byte == CK_NAN ? 0x7fc0u : f1 << 7;
+  m1 |= m1 << 16;
+  lo = make_uint4(bf16_pair(q.x, 0x1404, m1), bf16_pair(q.x, 0x3424, m1),
+                  bf16_pair(q.y, 0x1404, m1), bf16_pair(q.y, 0x3424, m1));
+  hi = make_uint4(bf16_pair(q.z, 0x1404, m1), bf16_pair(q.z, 0x3424, m1),
+                  bf16_pair(q.w, 0x1404, m1), bf16_pair(q.w, 0x3424, m1));
+  if (f2 != 127u) {
+    const uint32_t m2 = f2 << 7 | f2 << 23;
+    lo = make_uint4(mul_bf16x2(lo.x, m2), mul_bf16x2(lo.y, m2), mul_bf16x2(lo.z, m2),
+                    mul_bf16x2(lo.w, m2));
+    hi = make_uint4(mul_bf16x2(hi.x, m2), mul_bf16x2(hi.y, m2), mul_bf16x2(hi.z, m2),
+                    mul_bf16x2(hi.w, m2));
+  }
+}
+
+template <int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    ckpt_dw_kernel(const __grid_constant__ DwMaps tm, const __grid_constant__ DwParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  // Each CTA's: c_full/c_empty (codes), a_empty, b_empty, acc_full (the pair
+  // MMAs' commits arrive in both).  Rank 0's: a_full (a decoder warp of either
+  // CTA each), b_full (both CTAs' bytes), acc_empty (epilogue warps of both).
+  __shared__ uint64_t c_full[NC], c_empty[NC], a_full[NA], a_empty[NA], b_full[NB], b_empty[NB];
+  __shared__ uint64_t acc_full[2], acc_empty[2];
+  __shared__ uint32_t tmem_sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1;
+  constexpr int HALF = BN / 2;               // this CTA's columns of a tile
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NC; ++i) {
+      mbar_init(&c_full[i], 1);
+      mbar_init(&c_empty[i], N_DEC);
+    }
+    for (int i = 0; i < NA; ++i) {
+      mbar_init(&a_full[i], 2 * N_DEC);
+      mbar_init(&a_empty[i], 1);
+    }
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(&b_full[i], 1);
+      mbar_init(&b_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 8);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 3) {
+    tmem_alloc_pair(&tmem_sh, TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // both CTAs' barriers exist before anything signals them
+  tc_fence_after();
+  const uint32_t tmem = tmem_sh;
+  Piece w;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tm.dy);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int i = 0; ok && piece_of(p, pair, i, w); ++i) {
+        const int n0 = (w.t % p.n_tiles) * BN + (int)rank * HALF;
+        for (int k = w.k0; ok && k < w.k0 + w.kn; ++k)
+          for (int s = 0; s < p.pieces; ++s, ++it) {
+            const int st = it % NB;
+            if (it >= NB && !mbar_wait(&b_empty[st], (it / NB - 1) & 1, p.err)) {
+              ok = false;
+              break;
+            }
+            uint8_t* dst = sm + B_OFF + st * B_BYTES;
+            const uint32_t bar = smem_cluster_addr(&b_full[st], 0);
+            constexpr int BOXES = (HALF + 63) / 64;
+            if (rank == 0) mbar_arrive_expect_tx(&b_full[st], 2 * BOXES * BOX8K);
+#pragma unroll
+            for (int b = 0; b < BOXES; ++b)
+              tma_load_3d_pair(dst + b * BOX8K, &tm.dy, bar, n0 + b * 64, k * KT, s);
+          }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tm.codes);
+      tma_prefetch_desc(&tm.scales);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int i = 0; ok && piece_of(p, pair, i, w); ++i) {
+        const int g = (w.t / p.n_tiles) * 2 + (int)rank;
+        for (int k = w.k0; k < w.k0 + w.kn; ++k, ++it) {
+          const int st = it % NC;
+          if (it >= NC && !mbar_wait(&c_empty[st], (it / NC - 1) & 1, p.err)) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = sm + C_OFF + st * C_BYTES;
+          mbar_arrive_expect_tx(&c_full[st], C_BYTES);
+          tma_load_2d(dst, &tm.codes, &c_full[st], g * CK_GROUP, k * KT);
+          tma_load_2d(dst + CODE_BYTES, &tm.scales, &c_full[st], p.cols + (g & ~15), k * KT);
+        }
+      }
+    }
+  } else if (warp == 2) {
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = idesc_bf16(256, BN, 1, 1);
+      uint32_t ia = 0, ib = 0;
+      bool ok = true;
+      for (int i = 0; ok && piece_of(p, pair, i, w); ++i) {
+        const int buf = i & 1;
+        if (i >= 2 && !mbar_wait_cluster(&acc_empty[buf], ((i >> 1) - 1) & 1, p.err)) break;
+        tc_fence_after();
+        const uint32_t dst = tmem + (uint32_t)(buf * ACC_COLS);
+        for (int k = 0; ok && k < w.kn; ++k, ++ia) {
+          const int sa = ia % NA;
+          if (!mbar_wait_cluster(&a_full[sa], (ia / NA) & 1, p.err)) {
+            ok = false;
+            break;
+          }
+          const uint32_t alo = sdesc_lo(smem_u32(sm + A_OFF + sa * A_BYTES), BOX8K);
+          for (int s = 0; s < p.pieces; ++s, ++ib) {
+            const int sb = ib % NB;
+            if (!mbar_wait(&b_full[sb], (ib / NB) & 1, p.err)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t blo = sdesc_lo(smem_u32(sm + B_OFF + sb * B_BYTES), BOX8K);
+#pragma unroll
+            for (int kk = 0; kk < KT / 16; ++kk)
+              mma_ss_pair(dst, sdesc_make(alo + kk * (2048 >> 4)),
+                          sdesc_make(blo + kk * (2048 >> 4)), idesc,
+                          (k > 0 || s > 0 || kk > 0) ? 1u : 0u);
+            mma_commit_pair(&b_empty[sb]);
+          }
+          mma_commit_pair(&a_empty[sa]);
+        }
+        mma_commit_pair(&acc_full[buf]);
+      }
+    }
+  } else if (warp >= 4 && warp < 8) {
+    const int q = warp & 3;
+    uint8_t* stg = sm + E_OFF + q * (EPI_BUFS * EPI_BOX);
+    int nbox = 0;
+    for (int i = 0; piece_of(p, pair, i, w); ++i) {
+      const int buf = i & 1;
+      if (!mbar_wait(&acc_full[buf], (i >> 1) & 1, p.err)) break;
+      tc_fence_after();
+      const int n0 = (w.t % p.n_tiles) * BN;
+      const int row0 = ((w.t / p.n_tiles) * 2 + (int)rank) * CK_GROUP + q * 32;
+      const float gain = p.gamma && row0 + lane < p.d ? p.gamma[row0 + lane] : 1.f;
+      const uint32_t src = tmem + (uint32_t)(buf * ACC_COLS);
+#pragma unroll 1
+      for (int bx = 0; bx < BN / 32; ++bx, ++nbox) {
+        uint32_t u[32];
+        tmem_ld32(tmem_addr(src, q, bx * 32), u);
+        uint8_t* slot = stg + (nbox % EPI_BUFS) * EPI_BOX;
+        if (lane == 0) bulk_wait_read<EPI_BUFS - 1>();   // the slot's last store has been read
+        __syncwarp();
+        uint8_t* row = slot + lane * 128;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          float4 o;
+          o.x = __uint_as_float(u[4 * g]) * gain;
+          o.y = __uint_as_float(u[4 * g + 1]) * gain;
+          o.z = __uint_as_float(u[4 * g + 2]) * gain;
+          o.w = __uint_as_float(u[4 * g + 3]) * gain;
+          *reinterpret_cast<float4*>(row + ((g ^ (lane & 7)) << 4)) = o;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (w.frag >= 0)
+            tma_store_3d(&tm.frag, slot, bx * 32, (int)rank * CK_GROUP + q * 32, w.frag);
+          else if (row0 < p.d && n0 + bx * 32 < p.n)   // what a box has past the output is clipped
+            tma_store_3d(&tm.out, slot, n0 + bx * 32, row0, 0);
+          bulk_commit();
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(smem_cluster_addr(&acc_empty[buf], 0));
+    }
+    if (lane == 0) bulk_wait0();
+    __syncwarp();
+  } else if (warp >= 8) {
+    // thread: 16-byte chunk c of tokens t and t + 32 of a step
+    const int t = (warp - 8) * 4 + (lane >> 3), c = lane & 7;
+    uint32_t it = 0;
+    bool ok = true;
+    for (int i = 0; ok && piece_of(p, pair, i, w); ++i) {
+      const int g = (w.t / p.n_tiles) * 2 + (int)rank;
+      for (int k = 0; k < w.kn; ++k, ++it) {
+        const int sc = it % NC, sa = it % NA;
+        if (!mbar_wait(&c_full[sc], (it / NC) & 1, p.err)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* src = sm + C_OFF + sc * C_BYTES;
+        uint4 q[2];
+        uint32_t byte[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          q[h] = *reinterpret_cast<const uint4*>(src + (t + 32 * h) * CK_GROUP + c * 16);
+          byte[h] = src[CODE_BYTES + (t + 32 * h) * 16 + (g & 15)];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c_empty[sc]);
+        if (it >= NA && !mbar_wait(&a_empty[sa], (it / NA - 1) & 1, p.err)) {
+          ok = false;
+          break;
+        }
+        // token row, 64-channel box c / 4, chunks 2 (c % 4) and the next one.
+        // Lanes of chunks 4-7 store the second one first: the eight lanes of
+        // a token then hit all eight 16-byte banks at once.
+        uint8_t* dst = sm + A_OFF + sa * A_BYTES + (c >> 2) * BOX8K;
+        const int flip = c >> 2;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint4 o[2];
+          decode16(q[h], byte[h], o[0], o[1]);
+          const int r = t + 32 * h, j = 2 * (c & 3);
+          uint8_t* row = dst + r * 128;
+          *reinterpret_cast<uint4*>(row + (((j + flip) ^ (r & 7)) << 4)) = flip ? o[1] : o[0];
+          *reinterpret_cast<uint4*>(row + (((j + 1 - flip) ^ (r & 7)) << 4)) = flip ? o[0] : o[1];
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(smem_cluster_addr(&a_full[sa], 0));
+      }
+    }
+  }
+  // neither CTA leaves while the pair's MMAs or the other CTA's arrivals may
+  // still touch its shared memory or TMEM
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, TMEM_COLS);
+  }
+  cluster_sync();
+}
+
+// Sums of the left-over tiles' fragments, in token order.  A block takes 8
+// rows of a tile, a warp one row.
+__global__ void __launch_bounds__(256) dw_join_kernel(const float* __restrict__ frag, float* dw,
+                                                      const DwParams p, int bn) {
+  const int first_tile = p.rounds * PAIRS;
+  const int tile = blockIdx.x / 32, r = (blockIdx.x % 32) * 8 + (threadIdx.x >> 5);
+  const int t = first_tile + tile;
+  const int row = (t / p.n_tiles) * 256 + r, n0 = (t % p.n_tiles) * bn;
+  if (row >= p.d) return;
+  const long long u0 = (long long)tile * p.steps, u1 = u0 + p.steps;
+  const int pa = (int)(u0 / p.chunk), pb = (int)((u1 - 1) / p.chunk);
+  for (int c = threadIdx.x & 31; c < bn && n0 + c < p.n; c += 32) {
+    float s = 0.f;
+    for (int q = pa; q <= pb; ++q) {
+      const int i = tile - (int)(q * p.chunk / p.steps);   // its place among q's pieces
+      s += frag[((long long)(q * p.max_frags + i) * 256 + r) * bn + c];
+    }
+    dw[(long long)row * p.n + n0 + c] = s;
+  }
+}
+
+// dy in bf16 with rows of np = 8 ceil(n / 8) columns: a copy (bf16) or the
+// three pieces of an fp32 value.
+template <typename T>
+__global__ void __launch_bounds__(256) dy_pieces_kernel(const T* __restrict__ dy,
+                                                        __nv_bfloat16* __restrict__ out,
+                                                        long long rows, int n, int np) {
+  const long long total = rows * np;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
+    const long long r = i / np;
+    const int c = (int)(i % np);
+    const float v = c < n ? to_f32(dy[r * n + c]) : 0.f;
+    const __nv_bfloat16 p0 = __float2bfloat16_rz(v);   // towards zero: never past the largest bf16
+    out[i] = p0;
+    if (sizeof(T) == 4) {
+      const float rest = fabsf(v) <= 3.402823466e38f ? v - __bfloat162float(p0) : 0.f;
+      const __nv_bfloat16 p1 = __float2bfloat16_rn(rest);
+      out[total + i] = p1;
+      out[2 * total + i] = __float2bfloat16_rn(rest - __bfloat162float(p1));
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host side
+struct DwPlan {
+  int bn = 0, pieces = 1, np = 0;
+  bool convert = false;
+  DwParams p{};
+  size_t dy_bytes = 0, frag_bytes = 0;
+  int frag_slots = 0;
+};
+
+size_t up1k(size_t x) { return (x + 1023) / 1024 * 1024; }
+
+DwPlan dw_plan(int rows, int d, int n, bool fp32) {
+  DwPlan pl;
+  // Columns per tile: a step costs 2 BN clocks of MMA time, and no less than
+  // the decoders' ~256; ties go to the wider tile.
+  long long best = -1;
+  for (const int bn : {256, 192, 128}) {
+    const long long cost = (long long)((n + bn - 1) / bn) * std::max(2 * bn, 256);
+    if (best < 0 || cost < best) {
+      best = cost;
+      pl.bn = bn;
+    }
+  }
+  pl.pieces = fp32 ? 3 : 1;
+  pl.np = (n + 7) / 8 * 8;
+  pl.convert = fp32 || pl.np != n;
+  DwParams& p = pl.p;
+  p.d = d;
+  p.n = n;
+  p.cols = ck_cols(d);
+  p.groups = p.cols / CK_GROUP;
+  p.n_tiles = (n + pl.bn - 1) / pl.bn;
+  p.tiles = (p.groups + 1) / 2 * p.n_tiles;
+  p.steps = (rows + KT - 1) / KT;
+  p.pieces = pl.pieces;
+  // whole tiles are stored by TMA, whose rows start on 16 bytes
+  p.rounds = n % 4 == 0 ? p.tiles / PAIRS : 0;
+  const long long left = (long long)(p.tiles - p.rounds * PAIRS) * p.steps;
+  p.chunk = std::max<long long>((left + PAIRS - 1) / PAIRS, std::min(p.steps, MIN_STEPS));
+  p.max_frags = p.steps ? (int)((p.chunk + p.steps - 2) / p.steps) + 1 : 0;
+  pl.frag_slots = left > 0 ? (int)((left + p.chunk - 1) / p.chunk) * p.max_frags : 0;
+  if (pl.convert) pl.dy_bytes = up1k((size_t)pl.pieces * rows * pl.np * 2);
+  pl.frag_bytes = up1k((size_t)pl.frag_slots * 256 * pl.bn * 4);
+  return pl;
+}
+
+// Byte tensor of the checkpoint rows, without swizzling.
+cudaError_t byte_map(CUtensorMap* out, const void* base, uint64_t width, uint64_t rows,
+                     uint64_t pitch, uint32_t box_w) {
+  auto enc = tmap_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {width, rows}, str[1] = {pitch};
+  const cuuint32_t box[2] = {box_w, KT}, one[2] = {1, 1};
+  const CUresult r =
+      enc(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, str, box, one,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+size_t ckpt_dw_ws_bytes(int rows, int d, int n, bool fp32) {
+  if (rows == 0) return 0;
+  const DwPlan pl = dw_plan(rows, d, n, fp32);
+  return pl.dy_bytes + pl.frag_bytes;
+}
+
+cudaError_t launch_ckpt_dw(int rows, int d, int n, bool fp32, const void* ck, const void* dy,
+                           const float* gamma, float* dw, unsigned char* ws, int* err,
+                           cudaStream_t st) {
+  if (rows == 0) return cudaMemsetAsync(dw, 0, (size_t)d * n * 4, st);
+  DwPlan pl = dw_plan(rows, d, n, fp32);
+  DwParams& p = pl.p;
+  p.gamma = gamma;
+  p.err = err;
+  cudaError_t e;
+  const void* dyb = dy;
+  if (pl.convert) {
+    dyb = ws;
+    const int grid = (int)std::min<long long>(((long long)rows * pl.np + 255) / 256, 152 * 16);
+    LaunchScope ls_("ckpt_dw_pieces", st);
+    if (fp32)
+      dy_pieces_kernel<float><<<grid, 256, 0, st>>>(static_cast<const float*>(dy),
+                                                    reinterpret_cast<__nv_bfloat16*>(ws), rows, n,
+                                                    pl.np);
+    else
+      dy_pieces_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(
+          static_cast<const __nv_bfloat16*>(dy), reinterpret_cast<__nv_bfloat16*>(ws), rows, n,
+          pl.np);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  float* frag = reinterpret_cast<float*>(ws + pl.dy_bytes);
+  DwMaps tm{};
+  const uint64_t pitch = ck_pitch(d);
+  if ((e = byte_map(&tm.codes, ck, p.cols, rows, pitch, CK_GROUP)) != cudaSuccess) return e;
+  if ((e = byte_map(&tm.scales, ck, pitch, rows, pitch, 16)) != cudaSuccess) return e;
+  {
+    const uint64_t ld = (uint64_t)pl.np * 2;
+    uint64_t dims[3] = {(uint64_t)pl.np, (uint64_t)rows, (uint64_t)pl.pieces};
+    uint64_t str[2] = {ld, ld * rows};
+    uint32_t box[3] = {64, KT, 1};
+    if ((e = make_tmap_bf16(&tm.dy, dyb, 3, dims, str, box)) != cudaSuccess) return e;
+  }
+  if (p.rounds > 0) {
+    uint64_t dims[3] = {(uint64_t)n, (uint64_t)d, 1};
+    uint64_t str[2] = {(uint64_t)n * 4, (uint64_t)n * 4 * d};
+    uint32_t box[3] = {32, 32, 1};
+    if ((e = make_tmap_f32(&tm.out, dw, 3, dims, str, box, true)) != cudaSuccess) return e;
+  }
+  if (pl.frag_slots > 0) {
+    uint64_t dims[3] = {(uint64_t)pl.bn, 256, (uint64_t)pl.frag_slots};
+    uint64_t str[2] = {(uint64_t)pl.bn * 4, (uint64_t)pl.bn * 4 * 256};
+    uint32_t box[3] = {32, 32, 1};
+    if ((e = make_tmap_f32(&tm.frag, frag, 3, dims, str, box, true)) != cudaSuccess) return e;
+  }
+  auto k = pl.bn == 256 ? ckpt_dw_kernel<256> : pl.bn == 192 ? ckpt_dw_kernel<192>
+                                                             : ckpt_dw_kernel<128>;
+  if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES)) !=
+      cudaSuccess)
+    return e;
+  const int left = p.tiles - p.rounds * PAIRS;
+  const int pairs = p.rounds > 0 ? PAIRS : pl.frag_slots / p.max_frags;
+  {
+    LaunchScope ls_("ckpt_dw", st);
+    k<<<2 * pairs, THREADS, SMEM_BYTES, st>>>(tm, p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (left > 0) {
+    LaunchScope ls_("ckpt_dw_join", st);
+    dw_join_kernel<<<left * 32, 256, 0, st>>>(frag, dw, p, pl.bn);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace laga
