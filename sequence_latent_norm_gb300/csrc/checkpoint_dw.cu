@@ -10,19 +10,26 @@
 // nothing of dy is lost.
 //
 // Pairs of CTAs (two-CTA clusters, cta_group::2, M256 pair MMAs): CTA rank r
-// holds one group of 128 channels and half of the tile's BN columns.  16 warps:
+// holds one group of 128 channels and half of the tile's BN columns.  20 warps:
 //   0       TMA producer of dy tiles      (ring of NB stages, 64 tokens each)
 //   1       TMA producer of code and scale tiles                 (NC stages)
 //   2       MMA issuer (rank 0)
 //   3       TMEM allocator
-//   4-7     epilogue: TMEM -> registers -> times gamma -> swizzled 32 x 32
-//           boxes -> TMA stores, one accumulator while the other is filled
-//   8-15    decoders: code tile -> bf16 tile, MN-major, 128-byte swizzled
-//           (ring of NA stages)
-// A decoder thread turns 32 codes per 64-token step into bf16 with ~3
-// integer and multiply instructions each; the pair's MMAs of that step take
-// 2 BN clocks, so the decoders set the pace below BN = 128 and stay hidden
-// above.
+//   4-11    decoders: code tile -> bf16 tile, MN-major, 128-byte swizzled
+//           (ring of NA stages); two warps take a step, so that four steps
+//           are under way at a time: making a tile's generic stores visible to
+//           the tensor core takes longer than writing them
+//   12-19   epilogue: adds up the accumulators of a tile in registers, then
+//           multiplies by gamma and stores
+// A decoder turns 16 codes into bf16 with ~45 integer and multiply
+// instructions; the pair's MMAs of a step take 2 BN clocks.
+//
+// The tensor core's fp32 accumulation drops what does not fit below the
+// accumulator's last place instead of rounding it: a chain of 1024 MMAs
+// (16384 tokens) came out 8.4e-6 of its value short, 50 times the error of
+// rounded fp32 sums.  So a chain is CHAIN MMA stages at most (32 MMAs); the
+// epilogue warps add the chains in registers, rounding to nearest, while the
+// next one fills the other accumulator.
 //
 // Work split: tile counts rarely fill the 76 pairs evenly, so whole rounds of
 // one tile per pair run first, and the token steps of the tiles that are left
@@ -44,33 +51,36 @@ namespace {
 using namespace sm100;
 
 constexpr int KT = 64;                       // tokens per step
-constexpr int NA = 4, NB = 6, NC = 3;        // ring stages: v tiles, dy tiles, codes
+constexpr int NA = 6, NB = 5, NC = 4;        // ring stages: v tiles, dy tiles, codes
 constexpr int BOX8K = 64 * 64 * 2;           // a 64 x 64 bf16 box
 constexpr int A_BYTES = 2 * BOX8K;           // 64 tokens x 128 channels
 constexpr int B_BYTES = 2 * BOX8K;           // 64 tokens x up to 128 columns
 constexpr int CODE_BYTES = KT * CK_GROUP;
 constexpr int SCALE_BYTES = KT * 16;         // 16 groups' scale bytes of each token
 constexpr int C_BYTES = CODE_BYTES + SCALE_BYTES;
-constexpr int EPI_BOX = 32 * 128, EPI_BUFS = 2;
-constexpr int A_OFF = 0, B_OFF = NA * A_BYTES, E_OFF = B_OFF + NB * B_BYTES;
-constexpr int C_OFF = E_OFF + 4 * EPI_BUFS * EPI_BOX;
+constexpr int A_OFF = 0, B_OFF = NA * A_BYTES, C_OFF = B_OFF + NB * B_BYTES;
 constexpr int SMEM_BYTES = C_OFF + NC * C_BYTES + 1024;
-constexpr int THREADS = 512, N_DEC = 8;
+constexpr int THREADS = 640;
+constexpr int W_DEC = 4, W_EPI = 12;         // first decoder and epilogue warp
+constexpr int DEC_GROUPS = 4, DEC_WARPS = 2; // steps under way, warps per step
+constexpr int CHAIN = 8;
 constexpr int TMEM_COLS = 512, ACC_COLS = 256;
 constexpr int PAIRS = 76;                    // one pair per two SMs
 constexpr int MIN_STEPS = 8;
 
 struct DwMaps {
-  CUtensorMap codes, scales, dy, out, frag;
+  CUtensorMap codes, scales, dy;
 };
 struct DwParams {
   int groups, cols, d, n;
   int n_tiles, tiles;
   int steps, pieces;       // token steps of a tile; bf16 pieces of dy
+  int chain;               // token steps of one accumulation
   int rounds;              // whole rounds: one tile per pair each
   long long chunk;         // steps of the left-over tiles that each pair takes
   int max_frags;           // fragments per pair
   const float* gamma;
+  float *dw, *frag;
   int* err;
 };
 
@@ -156,10 +166,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NC; ++i) {
       mbar_init(&c_full[i], 1);
-      mbar_init(&c_empty[i], N_DEC);
+      mbar_init(&c_empty[i], DEC_WARPS);
     }
     for (int i = 0; i < NA; ++i) {
-      mbar_init(&a_full[i], 2 * N_DEC);
+      mbar_init(&a_full[i], 2 * DEC_WARPS);
       mbar_init(&a_empty[i], 1);
     }
     for (int i = 0; i < NB; ++i) {
@@ -168,7 +178,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 8);
+      mbar_init(&acc_empty[i], 16);
     }
     fence_barrier_init();
   }
@@ -182,6 +192,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_sh;
   Piece w;
+  // Registers: 96 a thread at launch; 32 + 2 * 64 + 2 * 160 = 5 * 96 over the
+  // five warpgroups (warps 0-3, the decoders', the epilogue's).
+  if (warp < W_DEC) reg_shrink<32>();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -231,126 +244,150 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   } else if (warp == 2) {
     if (lane == 0 && rank == 0) {
       const uint32_t idesc = idesc_bf16(256, BN, 1, 1);
-      uint32_t ia = 0, ib = 0;
+      uint32_t ia = 0, ib = 0, ic = 0;   // v tiles, dy tiles, chains
       bool ok = true;
       for (int i = 0; ok && piece_of(p, pair, i, w); ++i) {
-        const int buf = i & 1;
-        if (i >= 2 && !mbar_wait_cluster(&acc_empty[buf], ((i >> 1) - 1) & 1, p.err)) break;
-        tc_fence_after();
-        const uint32_t dst = tmem + (uint32_t)(buf * ACC_COLS);
-        for (int k = 0; ok && k < w.kn; ++k, ++ia) {
-          const int sa = ia % NA;
-          if (!mbar_wait_cluster(&a_full[sa], (ia / NA) & 1, p.err)) {
+        for (int k0 = 0; ok && k0 < w.kn; k0 += p.chain, ++ic) {
+          const int buf = ic & 1;
+          if (ic >= 2 && !mbar_wait_cluster(&acc_empty[buf], ((ic >> 1) - 1) & 1, p.err)) {
             ok = false;
             break;
           }
-          const uint32_t alo = sdesc_lo(smem_u32(sm + A_OFF + sa * A_BYTES), BOX8K);
-          for (int s = 0; s < p.pieces; ++s, ++ib) {
-            const int sb = ib % NB;
-            if (!mbar_wait(&b_full[sb], (ib / NB) & 1, p.err)) {
+          tc_fence_after();
+          const uint32_t dst = tmem + (uint32_t)(buf * ACC_COLS);
+          for (int k = k0; ok && k < min(k0 + p.chain, w.kn); ++k, ++ia) {
+            const int sa = ia % NA;
+            if (!mbar_wait_cluster(&a_full[sa], (ia / NA) & 1, p.err)) {
               ok = false;
               break;
             }
-            tc_fence_after();
-            const uint32_t blo = sdesc_lo(smem_u32(sm + B_OFF + sb * B_BYTES), BOX8K);
+            const uint32_t alo = sdesc_lo(smem_u32(sm + A_OFF + sa * A_BYTES), BOX8K);
+            for (int s = 0; s < p.pieces; ++s, ++ib) {
+              const int sb = ib % NB;
+              if (!mbar_wait(&b_full[sb], (ib / NB) & 1, p.err)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t blo = sdesc_lo(smem_u32(sm + B_OFF + sb * B_BYTES), BOX8K);
 #pragma unroll
-            for (int kk = 0; kk < KT / 16; ++kk)
-              mma_ss_pair(dst, sdesc_make(alo + kk * (2048 >> 4)),
-                          sdesc_make(blo + kk * (2048 >> 4)), idesc,
-                          (k > 0 || s > 0 || kk > 0) ? 1u : 0u);
-            mma_commit_pair(&b_empty[sb]);
+              for (int kk = 0; kk < KT / 16; ++kk)
+                mma_ss_pair(dst, sdesc_make(alo + kk * (2048 >> 4)),
+                            sdesc_make(blo + kk * (2048 >> 4)), idesc,
+                            (k > k0 || s > 0 || kk > 0) ? 1u : 0u);
+              mma_commit_pair(&b_empty[sb]);
+            }
+            mma_commit_pair(&a_empty[sa]);
           }
-          mma_commit_pair(&a_empty[sa]);
+          mma_commit_pair(&acc_full[buf]);
         }
-        mma_commit_pair(&acc_full[buf]);
       }
     }
-  } else if (warp >= 4 && warp < 8) {
-    const int q = warp & 3;
-    uint8_t* stg = sm + E_OFF + q * (EPI_BUFS * EPI_BOX);
-    int nbox = 0;
-    for (int i = 0; piece_of(p, pair, i, w); ++i) {
-      const int buf = i & 1;
-      if (!mbar_wait(&acc_full[buf], (i >> 1) & 1, p.err)) break;
-      tc_fence_after();
-      const int n0 = (w.t % p.n_tiles) * BN;
-      const int row0 = ((w.t / p.n_tiles) * 2 + (int)rank) * CK_GROUP + q * 32;
-      const float gain = p.gamma && row0 + lane < p.d ? p.gamma[row0 + lane] : 1.f;
-      const uint32_t src = tmem + (uint32_t)(buf * ACC_COLS);
-#pragma unroll 1
-      for (int bx = 0; bx < BN / 32; ++bx, ++nbox) {
-        uint32_t u[32];
-        tmem_ld32(tmem_addr(src, q, bx * 32), u);
-        uint8_t* slot = stg + (nbox % EPI_BUFS) * EPI_BOX;
-        if (lane == 0) bulk_wait_read<EPI_BUFS - 1>();   // the slot's last store has been read
-        __syncwarp();
-        uint8_t* row = slot + lane * 128;
+  } else if (warp >= W_EPI) {
+    reg_grow<160>();
+    // this warp: 32 channels (TMEM lanes) and half of the tile's columns
+    const int q = warp & 3, c0 = ((warp - W_EPI) >> 2) * HALF;
+    uint32_t ic = 0;
+    bool ok = true;
+    for (int i = 0; ok && piece_of(p, pair, i, w); ++i) {
+      float2 acc[HALF / 2];
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          float4 o;
-          o.x = __uint_as_float(u[4 * g]) * gain;
-          o.y = __uint_as_float(u[4 * g + 1]) * gain;
-          o.z = __uint_as_float(u[4 * g + 2]) * gain;
-          o.w = __uint_as_float(u[4 * g + 3]) * gain;
-          *reinterpret_cast<float4*>(row + ((g ^ (lane & 7)) << 4)) = o;
+      for (int j = 0; j < HALF / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+      for (int k0 = 0; k0 < w.kn; k0 += p.chain, ++ic) {
+        const int buf = ic & 1;
+        if (!mbar_wait(&acc_full[buf], (ic >> 1) & 1, p.err)) {
+          ok = false;
+          break;
         }
-        fence_proxy_async_smem();
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < HALF / 16; ++j) {
+          uint32_t u[16];
+          tmem_ld16(tmem_addr(tmem, q, buf * ACC_COLS + c0 + j * 16), u);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            acc[8 * j + e] = __fadd2_rn(acc[8 * j + e], make_float2(__uint_as_float(u[2 * e]),
+                                                                    __uint_as_float(u[2 * e + 1])));
+        }
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if (w.frag >= 0)
-            tma_store_3d(&tm.frag, slot, bx * 32, (int)rank * CK_GROUP + q * 32, w.frag);
-          else if (row0 < p.d && n0 + bx * 32 < p.n)   // what a box has past the output is clipped
-            tma_store_3d(&tm.out, slot, n0 + bx * 32, row0, 0);
-          bulk_commit();
+        if (lane == 0) mbar_arrive_cluster(smem_cluster_addr(&acc_empty[buf], 0));
+      }
+      if (!ok) break;
+      const int r = (int)rank * CK_GROUP + q * 32 + lane;       // row of the pair's tile
+      const int row = (w.t / p.n_tiles) * 256 + r, n0 = (w.t % p.n_tiles) * BN + c0;
+      if (row < p.d) {
+        const float gain = p.gamma ? p.gamma[row] : 1.f;
+        float* dst = w.frag >= 0 ? p.frag + ((long long)w.frag * 256 + r) * BN + c0
+                                 : p.dw + (long long)row * p.n + n0;
+        const int lim = w.frag >= 0 ? HALF : p.n - n0;           // columns that exist
+        if (w.frag >= 0 || p.n % 4 == 0) {
+#pragma unroll
+          for (int j = 0; j < HALF / 4; ++j)
+            if (4 * j < lim)
+              reinterpret_cast<float4*>(dst)[j] =
+                  make_float4(acc[2 * j].x * gain, acc[2 * j].y * gain, acc[2 * j + 1].x * gain,
+                              acc[2 * j + 1].y * gain);
+        } else {
+#pragma unroll
+          for (int j = 0; j < HALF / 2; ++j) {
+            if (2 * j < lim) dst[2 * j] = acc[j].x * gain;
+            if (2 * j + 1 < lim) dst[2 * j + 1] = acc[j].y * gain;
+          }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(smem_cluster_addr(&acc_empty[buf], 0));
     }
-    if (lane == 0) bulk_wait0();
-    __syncwarp();
-  } else if (warp >= 8) {
-    // thread: 16-byte chunk c of tokens t and t + 32 of a step
-    const int t = (warp - 8) * 4 + (lane >> 3), c = lane & 7;
+  } else if (warp >= W_DEC) {
+    reg_shrink<64>();
+    // group j takes the steps j, j + 4, ...; a thread the 16-byte chunk c of
+    // the tokens t, t + 8, ..., t + 56 of a step, four at a time
+    const int grp = (warp - W_DEC) / DEC_WARPS;
+    const int t = ((warp - W_DEC) % DEC_WARPS) * 4 + (lane >> 3), c = lane & 7;
     uint32_t it = 0;
     bool ok = true;
     for (int i = 0; ok && piece_of(p, pair, i, w); ++i) {
       const int g = (w.t / p.n_tiles) * 2 + (int)rank;
       for (int k = 0; k < w.kn; ++k, ++it) {
+        if ((int)(it % DEC_GROUPS) != grp) continue;
         const int sc = it % NC, sa = it % NA;
         if (!mbar_wait(&c_full[sc], (it / NC) & 1, p.err)) {
           ok = false;
           break;
         }
         const uint8_t* src = sm + C_OFF + sc * C_BYTES;
-        uint4 q[2];
-        uint32_t byte[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          q[h] = *reinterpret_cast<const uint4*>(src + (t + 32 * h) * CK_GROUP + c * 16);
-          byte[h] = src[CODE_BYTES + (t + 32 * h) * 16 + (g & 15)];
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c_empty[sc]);
-        if (it >= NA && !mbar_wait(&a_empty[sa], (it / NA - 1) & 1, p.err)) {
-          ok = false;
-          break;
-        }
         // token row, 64-channel box c / 4, chunks 2 (c % 4) and the next one.
         // Lanes of chunks 4-7 store the second one first: the eight lanes of
         // a token then hit all eight 16-byte banks at once.
         uint8_t* dst = sm + A_OFF + sa * A_BYTES + (c >> 2) * BOX8K;
-        const int flip = c >> 2;
+        const int flip = c >> 2, j = 2 * (c & 3);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint4 o[2];
-          decode16(q[h], byte[h], o[0], o[1]);
-          const int r = t + 32 * h, j = 2 * (c & 3);
-          uint8_t* row = dst + r * 128;
-          *reinterpret_cast<uint4*>(row + (((j + flip) ^ (r & 7)) << 4)) = flip ? o[1] : o[0];
-          *reinterpret_cast<uint4*>(row + (((j + 1 - flip) ^ (r & 7)) << 4)) = flip ? o[0] : o[1];
+        for (int half = 0; half < 2; ++half) {
+          uint4 v[4];
+          uint32_t byte[4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const int r = t + 8 * (4 * half + h);
+            v[h] = *reinterpret_cast<const uint4*>(src + r * CK_GROUP + c * 16);
+            byte[h] = src[CODE_BYTES + r * 16 + (g & 15)];
+          }
+          if (half == 0) {
+            if (it >= NA && !mbar_wait(&a_empty[sa], (it / NA - 1) & 1, p.err)) ok = false;
+          } else {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c_empty[sc]);
+          }
+          if (!ok) break;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint4 o[2];
+            decode16(v[h], byte[h], o[0], o[1]);
+            const int r = t + 8 * (4 * half + h);
+            uint8_t* row = dst + r * 128;
+            *reinterpret_cast<uint4*>(row + (((j + flip) ^ (r & 7)) << 4)) = flip ? o[1] : o[0];
+            *reinterpret_cast<uint4*>(row + (((j + 1 - flip) ^ (r & 7)) << 4)) = flip ? o[0] : o[1];
+          }
         }
+        if (!ok) break;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(smem_cluster_addr(&a_full[sa], 0));
@@ -371,8 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
 // Sums of the left-over tiles' fragments, in token order.  A block takes 8
 // rows of a tile, a warp one row.
-__global__ void __launch_bounds__(256) dw_join_kernel(const float* __restrict__ frag, float* dw,
-                                                      const DwParams p, int bn) {
+__global__ void __launch_bounds__(256) dw_join_kernel(const DwParams p, int bn) {
   const int first_tile = p.rounds * PAIRS;
   const int tile = blockIdx.x / 32, r = (blockIdx.x % 32) * 8 + (threadIdx.x >> 5);
   const int t = first_tile + tile;
@@ -384,9 +420,9 @@ __global__ void __launch_bounds__(256) dw_join_kernel(const float* __restrict__ 
     float s = 0.f;
     for (int q = pa; q <= pb; ++q) {
       const int i = tile - (int)(q * p.chunk / p.steps);   // its place among q's pieces
-      s += frag[((long long)(q * p.max_frags + i) * 256 + r) * bn + c];
+      s += p.frag[((long long)(q * p.max_frags + i) * 256 + r) * bn + c];
     }
-    dw[(long long)row * p.n + n0 + c] = s;
+    p.dw[(long long)row * p.n + n0 + c] = s;
   }
 }
 
@@ -447,8 +483,8 @@ DwPlan dw_plan(int rows, int d, int n, bool fp32) {
   p.tiles = (p.groups + 1) / 2 * p.n_tiles;
   p.steps = (rows + KT - 1) / KT;
   p.pieces = pl.pieces;
-  // whole tiles are stored by TMA, whose rows start on 16 bytes
-  p.rounds = n % 4 == 0 ? p.tiles / PAIRS : 0;
+  p.chain = std::max(1, CHAIN / pl.pieces);
+  p.rounds = p.tiles / PAIRS;
   const long long left = (long long)(p.tiles - p.rounds * PAIRS) * p.steps;
   p.chunk = std::max<long long>((left + PAIRS - 1) / PAIRS, std::min(p.steps, MIN_STEPS));
   p.max_frags = p.steps ? (int)((p.chunk + p.steps - 2) / p.steps) + 1 : 0;
@@ -504,7 +540,8 @@ cudaError_t launch_ckpt_dw(int rows, int d, int n, bool fp32, const void* ck, co
           pl.np);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  float* frag = reinterpret_cast<float*>(ws + pl.dy_bytes);
+  p.dw = dw;
+  p.frag = reinterpret_cast<float*>(ws + pl.dy_bytes);
   DwMaps tm{};
   const uint64_t pitch = ck_pitch(d);
   if ((e = byte_map(&tm.codes, ck, p.cols, rows, pitch, CK_GROUP)) != cudaSuccess) return e;
@@ -515,18 +552,6 @@ cudaError_t launch_ckpt_dw(int rows, int d, int n, bool fp32, const void* ck, co
     uint64_t str[2] = {ld, ld * rows};
     uint32_t box[3] = {64, KT, 1};
     if ((e = make_tmap_bf16(&tm.dy, dyb, 3, dims, str, box)) != cudaSuccess) return e;
-  }
-  if (p.rounds > 0) {
-    uint64_t dims[3] = {(uint64_t)n, (uint64_t)d, 1};
-    uint64_t str[2] = {(uint64_t)n * 4, (uint64_t)n * 4 * d};
-    uint32_t box[3] = {32, 32, 1};
-    if ((e = make_tmap_f32(&tm.out, dw, 3, dims, str, box, true)) != cudaSuccess) return e;
-  }
-  if (pl.frag_slots > 0) {
-    uint64_t dims[3] = {(uint64_t)pl.bn, 256, (uint64_t)pl.frag_slots};
-    uint64_t str[2] = {(uint64_t)pl.bn * 4, (uint64_t)pl.bn * 4 * 256};
-    uint32_t box[3] = {32, 32, 1};
-    if ((e = make_tmap_f32(&tm.frag, frag, 3, dims, str, box, true)) != cudaSuccess) return e;
   }
   auto k = pl.bn == 256 ? ckpt_dw_kernel<256> : pl.bn == 192 ? ckpt_dw_kernel<192>
                                                              : ckpt_dw_kernel<128>;
@@ -542,7 +567,7 @@ cudaError_t launch_ckpt_dw(int rows, int d, int n, bool fp32, const void* ck, co
   }
   if (left > 0) {
     LaunchScope ls_("ckpt_dw_join", st);
-    dw_join_kernel<<<left * 32, 256, 0, st>>>(frag, dw, p, pl.bn);
+    dw_join_kernel<<<left * 32, 256, 0, st>>>(p, pl.bn);
   }
   return cudaGetLastError();
 }
