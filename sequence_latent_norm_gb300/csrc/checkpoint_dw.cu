@@ -5,20 +5,18 @@
 // way through shared memory and never exist in 16 bits in HBM: 1 byte per
 // element is read instead of 2, and no separate unpacking pass (3 bytes per
 // element) runs.  An fp32 dy enters as three bf16 pieces, dy = p0 + p1 + p2
-// with every piece the rounded rest (24 significand bits in all), one after
+// with every piece the rest cut to 8 bits (24 significand bits in all), one after
 // the other against the same v tile: three products instead of one, and
 // nothing of dy is lost.
 //
 // Pairs of CTAs (two-CTA clusters, cta_group::2, M256 pair MMAs): CTA rank r
 // holds one group of 128 channels and half of the tile's BN columns.  20 warps:
-//   0       TMA producer of dy tiles      (ring of NB stages, 64 tokens each)
-//   1       TMA producer of code and scale tiles                 (NC stages)
+//   0       TMA producer of dy tiles       (ring of NS stages of 64 tokens)
+//   1       TMA producer of code and scale tiles               (NC stages)
 //   2       MMA issuer (rank 0)
 //   3       TMEM allocator
-//   4-11    decoders: code tile -> bf16 tile, MN-major, 128-byte swizzled
-//           (ring of NA stages); two warps take a step, so that four steps
-//           are under way at a time: making a tile's generic stores visible to
-//           the tensor core takes longer than writing them
+//   4-11    decoders: code tile -> bf16 tile of the stage, MN-major, 128-byte
+//           swizzled; two warps take a step, so four steps are under way
 //   12-19   epilogue: adds up the accumulators of a tile in registers, then
 //           multiplies by gamma and stores
 // A decoder turns 16 codes into bf16 with ~45 integer and multiply
@@ -27,7 +25,7 @@
 // The tensor core's fp32 accumulation drops what does not fit below the
 // accumulator's last place instead of rounding it: a chain of 1024 MMAs
 // (16384 tokens) came out 8.4e-6 of its value short, 50 times the error of
-// rounded fp32 sums.  So a chain is CHAIN MMA stages at most (32 MMAs); the
+// rounded fp32 sums.  So a chain is CHAIN steps at most (32 MMAs); the
 // epilogue warps add the chains in registers, rounding to nearest, while the
 // next one fills the other accumulator.
 //
@@ -51,18 +49,22 @@ namespace {
 using namespace sm100;
 
 constexpr int KT = 64;                       // tokens per step
-constexpr int NA = 6, NB = 5, NC = 4;        // ring stages: v tiles, dy tiles, codes
+constexpr int NS = 4, NC = 8;                // ring stages: v and dy tiles, codes
 constexpr int BOX8K = 64 * 64 * 2;           // a 64 x 64 bf16 box
 constexpr int A_BYTES = 2 * BOX8K;           // 64 tokens x 128 channels
 constexpr int B_BYTES = 2 * BOX8K;           // 64 tokens x up to 128 columns
 constexpr int CODE_BYTES = KT * CK_GROUP;
 constexpr int SCALE_BYTES = KT * 16;         // 16 groups' scale bytes of each token
 constexpr int C_BYTES = CODE_BYTES + SCALE_BYTES;
-constexpr int A_OFF = 0, B_OFF = NA * A_BYTES, C_OFF = B_OFF + NB * B_BYTES;
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int C_OFF = NS * STAGE_BYTES;
 constexpr int SMEM_BYTES = C_OFF + NC * C_BYTES + 1024;
 constexpr int THREADS = 640;
 constexpr int W_DEC = 4, W_EPI = 12;         // first decoder and epilogue warp
 constexpr int DEC_GROUPS = 4, DEC_WARPS = 2; // steps under way, warps per step
+// A decoder group waits on a parity, which only tells two neighbouring phases
+// apart: it has to see every phase of its stages' barriers.
+static_assert(NS % DEC_GROUPS == 0 && NC % DEC_GROUPS == 0, "a stage has one decoder group");
 constexpr int CHAIN = 8;
 constexpr int TMEM_COLS = 512, ACC_COLS = 256;
 constexpr int PAIRS = 76;                    // one pair per two SMs
@@ -74,8 +76,8 @@ struct DwMaps {
 struct DwParams {
   int groups, cols, d, n;
   int n_tiles, tiles;
-  int steps, pieces;       // token steps of a tile; bf16 pieces of dy
-  int chain;               // token steps of one accumulation
+  int pieces;              // bf16 pieces of dy
+  int steps;               // steps of a tile: step s is piece s % pieces of token step s / pieces
   int rounds;              // whole rounds: one tile per pair each
   long long chunk;         // steps of the left-over tiles that each pair takes
   int max_frags;           // fragments per pair
@@ -126,24 +128,34 @@ LAGA_DEVINL uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return o;
 }
 
-// 16 codes as two 16-byte chunks of bf16 values
-LAGA_DEVINL void decode16(const uint4& q, uint32_t byte, uint4& lo, uint4& hi) {
-  // 2^(e + 120) has the exponent field byte + 120; what does not fit in one
-  // bf16 factor goes into a second one
-  const uint32_t f1 = min(byte + 120u, 254u), f2 = byte + 247u - f1;
-  uint32_t m1 = byte == CK_NAN ? 0x7fc0u : f1 << 7;
-  m1 |= m1 << 16;
-  lo = make_uint4(bf16_pair(q.x, 0x1404, m1), bf16_pair(q.x, 0x3424, m1),
-                  bf16_pair(q.y, 0x1404, m1), bf16_pair(q.y, 0x3424, m1));
-  hi = make_uint4(bf16_pair(q.z, 0x1404, m1), bf16_pair(q.z, 0x3424, m1),
-                  bf16_pair(q.w, 0x1404, m1), bf16_pair(q.w, 0x3424, m1));
-  if (f2 != 127u) {
-    const uint32_t m2 = f2 << 7 | f2 << 23;
-    lo = make_uint4(mul_bf16x2(lo.x, m2), mul_bf16x2(lo.y, m2), mul_bf16x2(lo.z, m2),
-                    mul_bf16x2(lo.w, m2));
-    hi = make_uint4(mul_bf16x2(hi.x, m2), mul_bf16x2(hi.y, m2), mul_bf16x2(hi.z, m2),
-                    mul_bf16x2(hi.w, m2));
-  }
+// The factor 2^(e + 120) of a scale byte (e = byte - 127), or NaN, as a bf16
+// pair; what is past the largest power, 2^127, goes into a second factor.
+LAGA_DEVINL uint32_t factor1(uint32_t byte) {
+  const uint32_t m = byte == CK_NAN ? 0x7fc0u : min(byte + 120u, 254u) << 7;
+  return m | m << 16;
+}
+LAGA_DEVINL uint32_t factor2(uint32_t byte) {   // byte > 134
+  const uint32_t m = (byte - 7u) << 7;
+  return m | m << 16;
+}
+// 8 codes as one 16-byte chunk of bf16 values
+LAGA_DEVINL uint4 decode8(uint2 q, uint32_t m1) {
+  return make_uint4(bf16_pair(q.x, 0x1404, m1), bf16_pair(q.x, 0x3424, m1),
+                    bf16_pair(q.y, 0x1404, m1), bf16_pair(q.y, 0x3424, m1));
+}
+LAGA_DEVINL uint4 mul8(uint4 a, uint32_t m) {
+  return make_uint4(mul_bf16x2(a.x, m), mul_bf16x2(a.y, m), mul_bf16x2(a.z, m),
+                    mul_bf16x2(a.w, m));
+}
+
+// Arrive on rank 0's mbarrier (a cluster address), ordered after this thread's
+// work at CTA scope.  That is enough here: what the arrival announces is this
+// CTA's own shared memory, already made visible to the async proxy by its
+// fence, or its own TMEM, already read; nothing passes through rank 0's
+// threads.  (A cluster-scope release took ~1400 clocks on the decoders' path,
+// a cluster-scope acquire ~600 on the issuer's.)
+LAGA_DEVINL void mbar_arrive_pair(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 template <int BN>
@@ -152,11 +164,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
-  // Each CTA's: c_full/c_empty (codes), a_empty, b_empty, acc_full (the pair
-  // MMAs' commits arrive in both).  Rank 0's: a_full (a decoder warp of either
-  // CTA each), b_full (both CTAs' bytes), acc_empty (epilogue warps of both).
-  __shared__ uint64_t c_full[NC], c_empty[NC], a_full[NA], a_empty[NA], b_full[NB], b_empty[NB];
-  __shared__ uint64_t acc_full[2], acc_empty[2];
+  // Each CTA's: c_full, c_empty (codes), empty, acc_full (the pair MMAs' commits
+  // arrive in both).  Rank 0's: full (the bytes of both CTAs' dy tiles, and an
+  // arrival of every decoder warp that worked on the step in either CTA) and
+  // acc_empty (epilogue warps of both).
+  __shared__ uint64_t c_full[NC], c_empty[NC], full[NS], empty[NS], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -168,13 +180,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&c_full[i], 1);
       mbar_init(&c_empty[i], DEC_WARPS);
     }
-    for (int i = 0; i < NA; ++i) {
-      mbar_init(&a_full[i], 2 * DEC_WARPS);
-      mbar_init(&a_empty[i], 1);
-    }
-    for (int i = 0; i < NB; ++i) {
-      mbar_init(&b_full[i], 1);
-      mbar_init(&b_empty[i], 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1 + 2 * DEC_WARPS);
+      mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -203,21 +211,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       bool ok = true;
       for (int i = 0; ok && piece_of(p, pair, i, w); ++i) {
         const int n0 = (w.t % p.n_tiles) * BN + (int)rank * HALF;
-        for (int k = w.k0; ok && k < w.k0 + w.kn; ++k)
-          for (int s = 0; s < p.pieces; ++s, ++it) {
-            const int st = it % NB;
-            if (it >= NB && !mbar_wait(&b_empty[st], (it / NB - 1) & 1, p.err)) {
-              ok = false;
-              break;
-            }
-            uint8_t* dst = sm + B_OFF + st * B_BYTES;
-            const uint32_t bar = smem_cluster_addr(&b_full[st], 0);
-            constexpr int BOXES = (HALF + 63) / 64;
-            if (rank == 0) mbar_arrive_expect_tx(&b_full[st], 2 * BOXES * BOX8K);
-#pragma unroll
-            for (int b = 0; b < BOXES; ++b)
-              tma_load_3d_pair(dst + b * BOX8K, &tm.dy, bar, n0 + b * 64, k * KT, s);
+        for (int k = w.k0; k < w.k0 + w.kn; ++k, ++it) {
+          const int st = it % NS;
+          if (it >= NS && !mbar_wait(&empty[st], (it / NS - 1) & 1, p.err)) {
+            ok = false;
+            break;
           }
+          uint8_t* dst = sm + st * STAGE_BYTES + A_BYTES;
+          const uint32_t bar = smem_cluster_addr(&full[st], 0);
+          constexpr int BOXES = (HALF + 63) / 64;
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * BOXES * BOX8K);
+#pragma unroll
+          for (int b = 0; b < BOXES; ++b)
+            tma_load_3d_pair(dst + b * BOX8K, &tm.dy, bar, n0 + b * 64, k / p.pieces * KT,
+                             k % p.pieces);
+        }
       }
     }
   } else if (warp == 1) {
@@ -236,48 +244,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           uint8_t* dst = sm + C_OFF + st * C_BYTES;
           mbar_arrive_expect_tx(&c_full[st], C_BYTES);
-          tma_load_2d(dst, &tm.codes, &c_full[st], g * CK_GROUP, k * KT);
-          tma_load_2d(dst + CODE_BYTES, &tm.scales, &c_full[st], p.cols + (g & ~15), k * KT);
+          tma_load_2d(dst, &tm.codes, &c_full[st], g * CK_GROUP, k / p.pieces * KT);
+          tma_load_2d(dst + CODE_BYTES, &tm.scales, &c_full[st], p.cols + (g & ~15),
+                      k / p.pieces * KT);
         }
       }
     }
   } else if (warp == 2) {
     if (lane == 0 && rank == 0) {
       const uint32_t idesc = idesc_bf16(256, BN, 1, 1);
-      uint32_t ia = 0, ib = 0, ic = 0;   // v tiles, dy tiles, chains
+      uint32_t it = 0, ic = 0;   // steps, chains
       bool ok = true;
       for (int i = 0; ok && piece_of(p, pair, i, w); ++i) {
-        for (int k0 = 0; ok && k0 < w.kn; k0 += p.chain, ++ic) {
+        for (int k0 = 0; ok && k0 < w.kn; k0 += CHAIN, ++ic) {
           const int buf = ic & 1;
-          if (ic >= 2 && !mbar_wait_cluster(&acc_empty[buf], ((ic >> 1) - 1) & 1, p.err)) {
+          if (ic >= 2 && !mbar_wait(&acc_empty[buf], ((ic >> 1) - 1) & 1, p.err)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t dst = tmem + (uint32_t)(buf * ACC_COLS);
-          for (int k = k0; ok && k < min(k0 + p.chain, w.kn); ++k, ++ia) {
-            const int sa = ia % NA;
-            if (!mbar_wait_cluster(&a_full[sa], (ia / NA) & 1, p.err)) {
+          const int k1 = min(k0 + CHAIN, w.kn);
+          for (int k = k0; k < k1; ++k, ++it) {
+            const int st = it % NS;
+            if (!mbar_wait(&full[st], (it / NS) & 1, p.err)) {
               ok = false;
               break;
             }
-            const uint32_t alo = sdesc_lo(smem_u32(sm + A_OFF + sa * A_BYTES), BOX8K);
-            for (int s = 0; s < p.pieces; ++s, ++ib) {
-              const int sb = ib % NB;
-              if (!mbar_wait(&b_full[sb], (ib / NB) & 1, p.err)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const uint32_t blo = sdesc_lo(smem_u32(sm + B_OFF + sb * B_BYTES), BOX8K);
+            tc_fence_after();
+            const uint32_t alo = sdesc_lo(smem_u32(sm + st * STAGE_BYTES), BOX8K);
+            const uint32_t blo = alo + (A_BYTES >> 4);
 #pragma unroll
-              for (int kk = 0; kk < KT / 16; ++kk)
-                mma_ss_pair(dst, sdesc_make(alo + kk * (2048 >> 4)),
-                            sdesc_make(blo + kk * (2048 >> 4)), idesc,
-                            (k > k0 || s > 0 || kk > 0) ? 1u : 0u);
-              mma_commit_pair(&b_empty[sb]);
-            }
-            mma_commit_pair(&a_empty[sa]);
+            for (int kk = 0; kk < KT / 16; ++kk)
+              mma_ss_pair(dst, sdesc_make(alo + kk * (2048 >> 4)),
+                          sdesc_make(blo + kk * (2048 >> 4)), idesc,
+                          (k > k0 || kk > 0) ? 1u : 0u);
+            mma_commit_pair(&empty[st]);
           }
           mma_commit_pair(&acc_full[buf]);
         }
@@ -293,7 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       float2 acc[HALF / 2];
 #pragma unroll
       for (int j = 0; j < HALF / 2; ++j) acc[j] = make_float2(0.f, 0.f);
-      for (int k0 = 0; k0 < w.kn; k0 += p.chain, ++ic) {
+      for (int k0 = 0; k0 < w.kn; k0 += CHAIN, ++ic) {
         const int buf = ic & 1;
         if (!mbar_wait(&acc_full[buf], (ic >> 1) & 1, p.err)) {
           ok = false;
@@ -311,7 +313,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(smem_cluster_addr(&acc_empty[buf], 0));
+        if (lane == 0) mbar_arrive_pair(smem_cluster_addr(&acc_empty[buf], 0));
       }
       if (!ok) break;
       const int r = (int)rank * CK_GROUP + q * 32 + lane;       // row of the pair's tile
@@ -339,8 +341,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else if (warp >= W_DEC) {
     reg_shrink<64>();
-    // group j takes the steps j, j + 4, ...; a thread the 16-byte chunk c of
-    // the tokens t, t + 8, ..., t + 56 of a step, four at a time
+    // group j takes the steps j, j + DEC_GROUPS, ...; a thread the 16-byte
+    // chunk c of every TR-th token from t on, four at a time
+    constexpr int TR = 4 * DEC_WARPS, PASSES = KT / TR / 4;
     const int grp = (warp - W_DEC) / DEC_WARPS;
     const int t = ((warp - W_DEC) % DEC_WARPS) * 4 + (lane >> 3), c = lane & 7;
     uint32_t it = 0;
@@ -349,48 +352,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int g = (w.t / p.n_tiles) * 2 + (int)rank;
       for (int k = 0; k < w.kn; ++k, ++it) {
         if ((int)(it % DEC_GROUPS) != grp) continue;
-        const int sc = it % NC, sa = it % NA;
+        const int sc = it % NC, st = it % NS;
         if (!mbar_wait(&c_full[sc], (it / NC) & 1, p.err)) {
           ok = false;
           break;
         }
         const uint8_t* src = sm + C_OFF + sc * C_BYTES;
         // token row, 64-channel box c / 4, chunks 2 (c % 4) and the next one.
-        // Lanes of chunks 4-7 store the second one first: the eight lanes of
-        // a token then hit all eight 16-byte banks at once.
-        uint8_t* dst = sm + A_OFF + sa * A_BYTES + (c >> 2) * BOX8K;
+        // Lanes of chunks 4-7 decode and store the second one first: the eight
+        // lanes of a token then hit all eight 16-byte banks at once.
+        uint8_t* dst = sm + st * STAGE_BYTES + (c >> 2) * BOX8K;
         const int flip = c >> 2, j = 2 * (c & 3);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int half = 0; half < PASSES; ++half) {
           uint4 v[4];
           uint32_t byte[4];
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            const int r = t + 8 * (4 * half + h);
+            const int r = t + TR * (4 * half + h);
             v[h] = *reinterpret_cast<const uint4*>(src + r * CK_GROUP + c * 16);
             byte[h] = src[CODE_BYTES + r * 16 + (g & 15)];
           }
-          if (half == 0) {
-            if (it >= NA && !mbar_wait(&a_empty[sa], (it / NA - 1) & 1, p.err)) ok = false;
-          } else {
+          if (half == PASSES - 1) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&c_empty[sc]);
+          }
+          if (half == 0) {
+            if (it >= NS && !mbar_wait(&empty[st], (it / NS - 1) & 1, p.err)) ok = false;
           }
           if (!ok) break;
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            uint4 o[2];
-            decode16(v[h], byte[h], o[0], o[1]);
-            const int r = t + 8 * (4 * half + h);
+            const int r = t + TR * (4 * half + h);
             uint8_t* row = dst + r * 128;
-            *reinterpret_cast<uint4*>(row + (((j + flip) ^ (r & 7)) << 4)) = flip ? o[1] : o[0];
-            *reinterpret_cast<uint4*>(row + (((j + 1 - flip) ^ (r & 7)) << 4)) = flip ? o[0] : o[1];
+            const uint2 u0 = flip ? make_uint2(v[h].z, v[h].w) : make_uint2(v[h].x, v[h].y);
+            const uint2 u1 = flip ? make_uint2(v[h].x, v[h].y) : make_uint2(v[h].z, v[h].w);
+            const uint32_t m1 = factor1(byte[h]);
+            uint4 o0 = decode8(u0, m1), o1 = decode8(u1, m1);
+            if (byte[h] > 134u) {   // 2^(e + 120) is past bf16's largest power
+              o0 = mul8(o0, factor2(byte[h]));
+              o1 = mul8(o1, factor2(byte[h]));
+            }
+            *reinterpret_cast<uint4*>(row + (((j + flip) ^ (r & 7)) << 4)) = o0;
+            *reinterpret_cast<uint4*>(row + (((j + 1 - flip) ^ (r & 7)) << 4)) = o1;
           }
         }
         if (!ok) break;
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(smem_cluster_addr(&a_full[sa], 0));
+        if (lane == 0) mbar_arrive_pair(smem_cluster_addr(&full[st], 0));
       }
     }
   }
@@ -406,44 +416,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync();
 }
 
-// Sums of the left-over tiles' fragments, in token order.  A block takes 8
-// rows of a tile, a warp one row.
+// Sums of the left-over tiles' fragments, in token order: a thread four
+// columns of a row, four fragments' loads at a time.
 __global__ void __launch_bounds__(256) dw_join_kernel(const DwParams p, int bn) {
-  const int first_tile = p.rounds * PAIRS;
-  const int tile = blockIdx.x / 32, r = (blockIdx.x % 32) * 8 + (threadIdx.x >> 5);
-  const int t = first_tile + tile;
-  const int row = (t / p.n_tiles) * 256 + r, n0 = (t % p.n_tiles) * bn;
-  if (row >= p.d) return;
+  const int vecs = bn / 4;
+  const int tile = blockIdx.x / vecs;                    // vecs blocks of 256 x 4 values a tile
+  const int i = (blockIdx.x % vecs) * 256 + threadIdx.x;
+  const int r = i / vecs, c = (i % vecs) * 4;
+  const int t = p.rounds * PAIRS + tile;
+  const int row = (t / p.n_tiles) * 256 + r, n0 = (t % p.n_tiles) * bn + c;
+  if (row >= p.d || n0 >= p.n) return;
   const long long u0 = (long long)tile * p.steps, u1 = u0 + p.steps;
   const int pa = (int)(u0 / p.chunk), pb = (int)((u1 - 1) / p.chunk);
-  for (int c = threadIdx.x & 31; c < bn && n0 + c < p.n; c += 32) {
-    float s = 0.f;
-    for (int q = pa; q <= pb; ++q) {
-      const int i = tile - (int)(q * p.chunk / p.steps);   // its place among q's pieces
-      s += p.frag[((long long)(q * p.max_frags + i) * 256 + r) * bn + c];
+  // the tile is the first piece of every pair after pa
+  const int ia = tile - (int)(pa * p.chunk / p.steps);
+  const float* src = p.frag + (long long)r * bn + c;
+  const long long slot = 256LL * bn;
+  float4 s = *reinterpret_cast<const float4*>(src + (pa * p.max_frags + ia) * slot);
+  for (int q = pa + 1; q <= pb; q += 4) {
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      v[k] = q + k <= pb ? *reinterpret_cast<const float4*>(src + (q + k) * p.max_frags * slot)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      s.x += v[k].x; s.y += v[k].y; s.z += v[k].z; s.w += v[k].w;
     }
-    p.dw[(long long)row * p.n + n0 + c] = s;
+  }
+  float* dst = p.dw + (long long)row * p.n + n0;
+  if (p.n % 4 == 0) {
+    *reinterpret_cast<float4*>(dst) = s;
+  } else {
+    const float v[4] = {s.x, s.y, s.z, s.w};
+    for (int k = 0; k < 4 && n0 + k < p.n; ++k) dst[k] = v[k];
   }
 }
 
 // dy in bf16 with rows of np = 8 ceil(n / 8) columns: a copy (bf16) or the
-// three pieces of an fp32 value.
+// three pieces of an fp32 value, each the rest cut to bf16's 8 significand
+// bits, so that the three hold all 24.
+// A thread takes 8 columns; whole rows of 16-byte loads where n allows it.
 template <typename T>
 __global__ void __launch_bounds__(256) dy_pieces_kernel(const T* __restrict__ dy,
                                                         __nv_bfloat16* __restrict__ out,
                                                         long long rows, int n, int np) {
-  const long long total = rows * np;
+  const int vecs = np / 8;
+  const long long total = rows * vecs;
   for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
-    const long long r = i / np;
-    const int c = (int)(i % np);
-    const float v = c < n ? to_f32(dy[r * n + c]) : 0.f;
-    const __nv_bfloat16 p0 = __float2bfloat16_rz(v);   // towards zero: never past the largest bf16
-    out[i] = p0;
-    if (sizeof(T) == 4) {
-      const float rest = fabsf(v) <= 3.402823466e38f ? v - __bfloat162float(p0) : 0.f;
-      const __nv_bfloat16 p1 = __float2bfloat16_rn(rest);
-      out[total + i] = p1;
-      out[2 * total + i] = __float2bfloat16_rn(rest - __bfloat162float(p1));
+    const long long r = total <= 0x7fffffff ? (long long)((int)i / vecs) : i / vecs;
+    const int c = (int)(i - r * vecs) * 8;
+    float v[8];
+    if (sizeof(T) == 4 && n % 4 == 0 && c + 8 <= n) {
+      const float4* src = reinterpret_cast<const float4*>(dy + r * n + c);
+      const float4 a = src[0], b = src[1];
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = c + k < n ? to_f32(dy[r * n + c + k]) : 0.f;
+    }
+    // towards zero: never past the largest bf16
+#pragma unroll
+    for (int s = 0; s < (sizeof(T) == 4 ? 3 : 1); ++s) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const __nv_bfloat16 a = __float2bfloat16_rz(v[2 * k]), b = __float2bfloat16_rz(v[2 * k + 1]);
+        w[k] = (uint32_t)__bfloat16_as_ushort(a) | (uint32_t)__bfloat16_as_ushort(b) << 16;
+        v[2 * k] = fabsf(v[2 * k]) <= 3.402823466e38f ? v[2 * k] - __bfloat162float(a) : 0.f;
+        v[2 * k + 1] =
+            fabsf(v[2 * k + 1]) <= 3.402823466e38f ? v[2 * k + 1] - __bfloat162float(b) : 0.f;
+      }
+      reinterpret_cast<uint4*>(out)[s * total + i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
@@ -481,9 +526,8 @@ DwPlan dw_plan(int rows, int d, int n, bool fp32) {
   p.groups = p.cols / CK_GROUP;
   p.n_tiles = (n + pl.bn - 1) / pl.bn;
   p.tiles = (p.groups + 1) / 2 * p.n_tiles;
-  p.steps = (rows + KT - 1) / KT;
+  p.steps = (rows + KT - 1) / KT * pl.pieces;
   p.pieces = pl.pieces;
-  p.chain = std::max(1, CHAIN / pl.pieces);
   p.rounds = p.tiles / PAIRS;
   const long long left = (long long)(p.tiles - p.rounds * PAIRS) * p.steps;
   p.chunk = std::max<long long>((left + PAIRS - 1) / PAIRS, std::min(p.steps, MIN_STEPS));
@@ -528,7 +572,7 @@ cudaError_t launch_ckpt_dw(int rows, int d, int n, bool fp32, const void* ck, co
   const void* dyb = dy;
   if (pl.convert) {
     dyb = ws;
-    const int grid = (int)std::min<long long>(((long long)rows * pl.np + 255) / 256, 152 * 16);
+    const int grid = (int)std::min<long long>(((long long)rows * (pl.np / 8) + 255) / 256, 152 * 8);
     LaunchScope ls_("ckpt_dw_pieces", st);
     if (fp32)
       dy_pieces_kernel<float><<<grid, 256, 0, st>>>(static_cast<const float*>(dy),
@@ -567,7 +611,7 @@ cudaError_t launch_ckpt_dw(int rows, int d, int n, bool fp32, const void* ck, co
   }
   if (left > 0) {
     LaunchScope ls_("ckpt_dw_join", st);
-    dw_join_kernel<<<left * 32, 256, 0, st>>>(p, pl.bn);
+    dw_join_kernel<<<left * (pl.bn / 4), 256, 0, st>>>(p, pl.bn);
   }
   return cudaGetLastError();
 }
