@@ -462,7 +462,8 @@ laga_status laga_ckpt_unpack(int rows, int d, laga_dtype dtype, const void* ck, 
 }
 
 static bool dw_sizes_ok(int rows, int d, int n, laga_dtype dy_dtype) {
-  return rows >= 0 && d >= 1 && d <= CK_MAX_D && n >= 1 && n <= CK_MAX_N && dtype_ok(dy_dtype);
+  return rows >= 0 && d >= 1 && d <= CK_MAX_D && n >= 1 && n <= CK_MAX_N && dtype_ok(dy_dtype) &&
+         ckpt_dw_fits(rows, d, n, dy_dtype == LAGA_FP32);
 }
 
 size_t laga_ckpt_dw_workspace_bytes(int rows, int d, int n, laga_dtype dy_dtype) {

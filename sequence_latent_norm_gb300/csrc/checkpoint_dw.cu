@@ -14,18 +14,19 @@
 //   0       TMA producer of dy tiles       (ring of NS stages of 64 tokens)
 //   1       TMA producer of code and scale tiles               (NC stages)
 //   2       MMA issuer (rank 0)
+//   2, 3    in rank 1: pass the decoders' arrivals on to rank 0
 //   3       TMEM allocator
 //   4-11    decoders: code tile -> bf16 tile of the stage, MN-major, 128-byte
-//           swizzled; two warps take a step, so four steps are under way
+//           swizzled
 //   12-19   epilogue: adds up the accumulators of a tile in registers, then
 //           multiplies by gamma and stores
-// A decoder turns 16 codes into bf16 with ~45 integer and multiply
-// instructions; the pair's MMAs of a step take 2 BN clocks.
+// A decoder turns 4 codes into bf16 with 9 integer and multiply instructions;
+// the pair's MMAs of a step take 2 BN clocks.
 //
 // The tensor core's fp32 accumulation drops what does not fit below the
 // accumulator's last place instead of rounding it: a chain of 1024 MMAs
 // (16384 tokens) came out 8.4e-6 of its value short, 50 times the error of
-// rounded fp32 sums.  So a chain is CHAIN steps at most (32 MMAs); the
+// rounded fp32 sums.  So a chain is CHAIN steps at most (64 MMAs); the
 // epilogue warps add the chains in registers, rounding to nearest, while the
 // next one fills the other accumulator.
 //
@@ -35,6 +36,8 @@
 // pair's part of such a tile is a fragment in the workspace; dw_join adds a
 // tile's fragments in token order.  Which pair takes what depends on the
 // sizes alone, so every run adds in the same order.
+#include <limits.h>
+
 #include <algorithm>
 
 #include "ckpt8.cuh"
@@ -49,7 +52,7 @@ namespace {
 using namespace sm100;
 
 constexpr int KT = 64;                       // tokens per step
-constexpr int NS = 4, NC = 8;                // ring stages: v and dy tiles, codes
+constexpr int NS = 6, NC = 3;                // ring stages: v and dy tiles, codes
 constexpr int BOX8K = 64 * 64 * 2;           // a 64 x 64 bf16 box
 constexpr int A_BYTES = 2 * BOX8K;           // 64 tokens x 128 channels
 constexpr int B_BYTES = 2 * BOX8K;           // 64 tokens x up to 128 columns
@@ -61,11 +64,16 @@ constexpr int C_OFF = NS * STAGE_BYTES;
 constexpr int SMEM_BYTES = C_OFF + NC * C_BYTES + 1024;
 constexpr int THREADS = 640;
 constexpr int W_DEC = 4, W_EPI = 12;         // first decoder and epilogue warp
-constexpr int DEC_GROUPS = 4, DEC_WARPS = 2; // steps under way, warps per step
-// A decoder group waits on a parity, which only tells two neighbouring phases
-// apart: it has to see every phase of its stages' barriers.
-static_assert(NS % DEC_GROUPS == 0 && NC % DEC_GROUPS == 0, "a stage has one decoder group");
-constexpr int CHAIN = 8;
+constexpr int DEC_WARPS = W_EPI - W_DEC;
+// Registers a thread: at launch (the most that THREADS threads can have, in
+// steps of 8), and after each warpgroup's setmaxnreg.
+constexpr int REG_LAUNCH = 65536 / THREADS / 8 * 8;
+constexpr int REG_MISC = 32, REG_DEC = 64, REG_EPI = 160;
+static_assert(W_DEC % 4 == 0 && W_EPI % 4 == 0 && THREADS % 128 == 0, "whole warpgroups");
+static_assert(W_DEC * REG_MISC + (W_EPI - W_DEC) * REG_DEC + (THREADS / 32 - W_EPI) * REG_EPI <=
+                  THREADS / 32 * REG_LAUNCH,
+              "the epilogue's warps grow on what the others give back");
+constexpr int CHAIN = 16;
 constexpr int TMEM_COLS = 512, ACC_COLS = 256;
 constexpr int PAIRS = 76;                    // one pair per two SMs
 constexpr int MIN_STEPS = 8;
@@ -79,83 +87,94 @@ struct DwParams {
   int pieces;              // bf16 pieces of dy
   int steps;               // steps of a tile: step s is piece s % pieces of token step s / pieces
   int rounds;              // whole rounds: one tile per pair each
-  long long chunk;         // steps of the left-over tiles that each pair takes
+  int chunk;               // steps of the left-over tiles that each pair takes
   int max_frags;           // fragments per pair
   const float* gamma;
   float *dw, *frag;
   int* err;
 };
 
-// One piece of a pair's work: steps [k0, k0 + kn) of tile t; frag < 0: the
+// A pair's work, piece by piece: kn steps from k0 on of tile t.  frag < 0: a
 // whole tile, stored to the output.
-struct Piece {
+struct Walk {
   int t, k0, kn, frag;
-};
-// The i-th piece of pair p; false past the last one.
-LAGA_DEVINL bool piece_of(const DwParams& p, int pair, int i, Piece& w) {
-  if (i < p.rounds) {
-    w = {i * PAIRS + pair, 0, p.steps, -1};
+  int i, next_t, next_k, left;   // of the pair's share of the left-over tiles
+
+  LAGA_DEVINL Walk(const DwParams& p, int pair) {
+    const long long total = (long long)(p.tiles - p.rounds * PAIRS) * p.steps;
+    const long long u = min((long long)pair * p.chunk, total);
+    left = (int)min((long long)p.chunk, total - u);
+    next_t = p.rounds * PAIRS + (int)(u / p.steps);
+    next_k = (int)(u % p.steps);
+    i = 0;
+  }
+  LAGA_DEVINL bool next(const DwParams& p, int pair) {
+    if (i < p.rounds) {
+      t = i * PAIRS + pair;
+      k0 = 0;
+      kn = p.steps;
+      frag = -1;
+    } else if (left > 0) {
+      t = next_t++;
+      k0 = next_k;
+      kn = min(left, p.steps - k0);
+      frag = pair * p.max_frags + i - p.rounds;
+      next_k = 0;
+      left -= kn;
+    } else {
+      return false;
+    }
+    ++i;
     return true;
   }
-  i -= p.rounds;
-  const int first_tile = p.rounds * PAIRS;
-  const long long total = (long long)(p.tiles - first_tile) * p.steps;
-  const long long u0 = min(pair * p.chunk, total);
-  const long long u1 = min(u0 + p.chunk, total);
-  if (u0 >= u1) return false;
-  const long long ta = u0 / p.steps, tb = (u1 - 1) / p.steps;   // its first and last tile
-  if (ta + i > tb) return false;
-  const long long lo = max(u0, (ta + i) * p.steps), hi = min(u1, (ta + i + 1) * p.steps);
-  w = {first_tile + (int)(ta + i), (int)(lo - (ta + i) * p.steps), (int)(hi - lo),
-       pair * p.max_frags + i};
-  return true;
-}
+};
 
-// Two codes (bytes b0, b1 of the selected halves) as bf16: sign, exponent and
-// significand moved into place stand for the code's value times 2^-120
-// (e4m3's bias is 7, bf16's 127), subnormal codes included; m1 brings that and
-// the group's 2^e back, exactly.
-LAGA_DEVINL uint32_t bf16_pair(uint32_t w, uint32_t sel, uint32_t m1) {
-  const uint32_t t = __byte_perm(w, 0u, sel);
-  const uint32_t r = ((t >> 4) & 0x07f007f0u) | (t & 0x80008000u);
-  uint32_t o;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(r), "r"(m1));
-  return o;
-}
 LAGA_DEVINL uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t o;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(a), "r"(b));
   return o;
 }
 
-// The factor 2^(e + 120) of a scale byte (e = byte - 127), or NaN, as a bf16
-// pair; what is past the largest power, 2^127, goes into a second factor.
-LAGA_DEVINL uint32_t factor1(uint32_t byte) {
-  const uint32_t m = byte == CK_NAN ? 0x7fc0u : min(byte + 120u, 254u) << 7;
-  return m | m << 16;
+// Four codes (bytes 0-3) as bf16 pairs: lo of codes 0 and 2, hi of codes 1
+// and 3.  Sign, exponent and significand moved into bf16's places stand for
+// the code's value times 2^-120 (e4m3's bias is 7, bf16's 127), subnormal
+// codes included; m = 2^(e + 120) makes it the value, exactly.  The pairs
+// leave the channels of a word in the order 0, 2, 1, 3: channel_of undoes
+// that where the accumulator's rows are stored.
+LAGA_DEVINL void decode4(uint32_t w, uint32_t m, uint32_t& lo, uint32_t& hi) {
+  lo = mul_bf16x2(((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u), m);
+  hi = mul_bf16x2(((w >> 4) & 0x07f007f0u) | (w & 0x80008000u), m);
 }
-LAGA_DEVINL uint32_t factor2(uint32_t byte) {   // byte > 134
-  const uint32_t m = (byte - 7u) << 7;
-  return m | m << 16;
-}
-// 8 codes as one 16-byte chunk of bf16 values
-LAGA_DEVINL uint4 decode8(uint2 q, uint32_t m1) {
-  return make_uint4(bf16_pair(q.x, 0x1404, m1), bf16_pair(q.x, 0x3424, m1),
-                    bf16_pair(q.y, 0x1404, m1), bf16_pair(q.y, 0x3424, m1));
-}
-LAGA_DEVINL uint4 mul8(uint4 a, uint32_t m) {
-  return make_uint4(mul_bf16x2(a.x, m), mul_bf16x2(a.y, m), mul_bf16x2(a.z, m),
-                    mul_bf16x2(a.w, m));
+LAGA_DEVINL int channel_of(int m) { return (m & ~3) | (m & 1) << 1 | (m >> 1 & 1); }
+
+// 16 codes under one scale byte as two 16-byte chunks of bf16 values.  The
+// factor 2^(e + 120), e = byte - 127, has the exponent field byte + 120; past
+// byte 134 (e = 7) it takes two factors, and byte 255 is a NaN.
+LAGA_DEVINL void decode16(const uint4& q, uint32_t byte, uint4& a, uint4& b) {
+  const bool far = byte > 134u;
+  const uint32_t m = far ? 0x7f007f00u : byte * 0x00800080u + 120u * 0x00800080u;
+  decode4(q.x, m, a.x, a.y);
+  decode4(q.y, m, a.z, a.w);
+  decode4(q.z, m, b.x, b.y);
+  decode4(q.w, m, b.z, b.w);
+  if (far) {
+    const uint32_t n = byte == CK_NAN ? 0x7fc07fc0u : (byte - 7u) * 0x00800080u;
+    a = make_uint4(mul_bf16x2(a.x, n), mul_bf16x2(a.y, n), mul_bf16x2(a.z, n), mul_bf16x2(a.w, n));
+    b = make_uint4(mul_bf16x2(b.x, n), mul_bf16x2(b.y, n), mul_bf16x2(b.z, n), mul_bf16x2(b.w, n));
+  }
 }
 
-// Arrive on rank 0's mbarrier (a cluster address), ordered after this thread's
-// work at CTA scope.  That is enough here: what the arrival announces is this
-// CTA's own shared memory, already made visible to the async proxy by its
-// fence, or its own TMEM, already read; nothing passes through rank 0's
-// threads.  (A cluster-scope release took ~1400 clocks on the decoders' path,
-// a cluster-scope acquire ~600 on the issuer's.)
-LAGA_DEVINL void mbar_arrive_pair(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Whether a phase has completed, without waiting for it.
+LAGA_DEVINL bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 template <int BN>
@@ -165,9 +184,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
   // Each CTA's: c_full, c_empty (codes), empty, acc_full (the pair MMAs' commits
-  // arrive in both).  Rank 0's: full (the bytes of both CTAs' dy tiles, and an
-  // arrival of every decoder warp that worked on the step in either CTA) and
-  // acc_empty (epilogue warps of both).
+  // arrive in both).  full: in rank 1 an arrival of every decoder warp; in rank
+  // 0 the same, the bytes of both CTAs' dy tiles, and an arrival that says
+  // that rank 1's is complete.  Rank 0's acc_empty: epilogue warps of both.
   __shared__ uint64_t c_full[NC], c_empty[NC], full[NS], empty[NS], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -181,7 +200,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&c_empty[i], DEC_WARPS);
     }
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&full[i], 1 + 2 * DEC_WARPS);
+      mbar_init(&full[i], rank == 0 ? DEC_WARPS + 2 : DEC_WARPS);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -199,17 +218,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync();   // both CTAs' barriers exist before anything signals them
   tc_fence_after();
   const uint32_t tmem = tmem_sh;
-  Piece w;
-  // Registers: 96 a thread at launch; 32 + 2 * 64 + 2 * 160 = 5 * 96 over the
-  // five warpgroups (warps 0-3, the decoders', the epilogue's).
-  if (warp < W_DEC) reg_shrink<32>();
+  Walk w(p, pair);
+  if (warp < W_DEC) reg_shrink<REG_MISC>();
 
   if (warp == 0) {
     if (lane == 0) {
       tma_prefetch_desc(&tm.dy);
       uint32_t it = 0;
       bool ok = true;
-      for (int i = 0; ok && piece_of(p, pair, i, w); ++i) {
+      while (ok && w.next(p, pair)) {
         const int n0 = (w.t % p.n_tiles) * BN + (int)rank * HALF;
         for (int k = w.k0; k < w.k0 + w.kn; ++k, ++it) {
           const int st = it % NS;
@@ -234,7 +251,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       tma_prefetch_desc(&tm.scales);
       uint32_t it = 0;
       bool ok = true;
-      for (int i = 0; ok && piece_of(p, pair, i, w); ++i) {
+      while (ok && w.next(p, pair)) {
         const int g = (w.t / p.n_tiles) * 2 + (int)rank;
         for (int k = w.k0; k < w.k0 + w.kn; ++k, ++it) {
           const int st = it % NC;
@@ -250,15 +267,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
       }
     }
-  } else if (warp == 2) {
-    if (lane == 0 && rank == 0) {
+  } else if (warp == 2 && rank == 0) {
+    if (lane == 0) {
       const uint32_t idesc = idesc_bf16(256, BN, 1, 1);
       uint32_t it = 0, ic = 0;   // steps, chains
+      bool ready = false;        // step it's stage has been seen full
       bool ok = true;
-      for (int i = 0; ok && piece_of(p, pair, i, w); ++i) {
+      while (ok && w.next(p, pair)) {
         for (int k0 = 0; ok && k0 < w.kn; k0 += CHAIN, ++ic) {
           const int buf = ic & 1;
-          if (ic >= 2 && !mbar_wait(&acc_empty[buf], ((ic >> 1) - 1) & 1, p.err)) {
+          if (ic >= 2 && !mbar_wait_cluster(&acc_empty[buf], ((ic >> 1) - 1) & 1, p.err)) {
             ok = false;
             break;
           }
@@ -267,11 +285,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           const int k1 = min(k0 + CHAIN, w.kn);
           for (int k = k0; k < k1; ++k, ++it) {
             const int st = it % NS;
-            if (!mbar_wait(&full[st], (it / NS) & 1, p.err)) {
+            if (!ready && !mbar_wait(&full[st], (it / NS) & 1, p.err)) {
               ok = false;
               break;
             }
             tc_fence_after();
+            // ask for the next stage now: the answer arrives while this one's
+            // MMAs are issued
+            ready = mbar_test(&full[(it + 1) % NS], ((it + 1) / NS) & 1);
             const uint32_t alo = sdesc_lo(smem_u32(sm + st * STAGE_BYTES), BOX8K);
             const uint32_t blo = alo + (A_BYTES >> 4);
 #pragma unroll
@@ -285,13 +306,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
       }
     }
+  } else if (warp < W_DEC) {
+    // Rank 1's warps 2 and 3, a step each in turn: announce its decoded tile to
+    // rank 0.  The decoders' stores are complete for this CTA; the cluster-
+    // scope release that makes them so for the pair takes hundreds of clocks,
+    // which the decoders would wait for and these two do not mind.
+    if (lane == 0 && rank == 1) {
+      uint32_t base = 0;
+      bool ok = true;
+      while (ok && w.next(p, pair)) {
+        for (uint32_t it = base + ((base ^ warp) & 1); it < base + w.kn; it += 2) {
+          const int st = it % NS;
+          if (!mbar_wait(&full[st], (it / NS) & 1, p.err)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_cluster(smem_cluster_addr(&full[st], 0));
+        }
+        base += w.kn;
+      }
+    }
   } else if (warp >= W_EPI) {
-    reg_grow<160>();
+    reg_grow<REG_EPI>();
     // this warp: 32 channels (TMEM lanes) and half of the tile's columns
     const int q = warp & 3, c0 = ((warp - W_EPI) >> 2) * HALF;
     uint32_t ic = 0;
     bool ok = true;
-    for (int i = 0; ok && piece_of(p, pair, i, w); ++i) {
+    while (ok && w.next(p, pair)) {
       float2 acc[HALF / 2];
 #pragma unroll
       for (int j = 0; j < HALF / 2; ++j) acc[j] = make_float2(0.f, 0.f);
@@ -313,10 +354,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_pair(smem_cluster_addr(&acc_empty[buf], 0));
+        if (lane == 0) mbar_arrive_cluster(smem_cluster_addr(&acc_empty[buf], 0));
       }
       if (!ok) break;
-      const int r = (int)rank * CK_GROUP + q * 32 + lane;       // row of the pair's tile
+      const int r = (int)rank * CK_GROUP + channel_of(q * 32 + lane);   // row of the pair's tile
       const int row = (w.t / p.n_tiles) * 256 + r, n0 = (w.t % p.n_tiles) * BN + c0;
       if (row < p.d) {
         const float gain = p.gamma ? p.gamma[row] : 1.f;
@@ -340,67 +381,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
     }
   } else if (warp >= W_DEC) {
-    reg_shrink<64>();
-    // group j takes the steps j, j + DEC_GROUPS, ...; a thread the 16-byte
-    // chunk c of every TR-th token from t on, four at a time
-    constexpr int TR = 4 * DEC_WARPS, PASSES = KT / TR / 4;
-    const int grp = (warp - W_DEC) / DEC_WARPS;
-    const int t = ((warp - W_DEC) % DEC_WARPS) * 4 + (lane >> 3), c = lane & 7;
+    reg_shrink<REG_DEC>();
+    // A warp takes TOK tokens of every step, a thread 16 codes (chunk c of a
+    // 64-channel box) of N of them.  Eight lanes work on the tokens r and r ^ 5
+    // of an 8-token swizzle atom and four chunks of one box: their 16-byte
+    // accesses hit all eight 16-byte banks, in the code tile (chunk c of token
+    // r sits at c ^ r) as in the bf16 tile (chunks 2c and 2c + 1 at their own
+    // index ^ r).  The next step's codes are read before this one's are
+    // decoded.
+    constexpr int TOK = KT / DEC_WARPS, N = TOK / 4;
+    static_assert(TOK == 4 || TOK == 8, "tokens of a warp");
+    const int dw = warp - W_DEC, c = lane & 3, box = lane >> 3 & 1;
+    uint32_t src_off[N], dst_off[N], row_off[N];
+#pragma unroll
+    for (int h = 0; h < N; ++h) {
+      // the atom's token pairs (0, 5), (1, 4), (2, 7), (3, 6), two per 4-token part
+      const int part = TOK == 4 ? dw & 1 : h;
+      const int r = (2 * part + (lane >> 4)) ^ (lane & 4 ? 5 : 0);
+      const int t = (dw * TOK & ~7) + r;
+      row_off[h] = CODE_BYTES + t * 16;
+      src_off[h] = t * CK_GROUP + (((box * 4 + c) ^ r) << 4);
+      dst_off[h] = box * BOX8K + t * 128 + (((2 * c) ^ r) << 4);
+    }
+    uint4 v[N];
+    uint32_t byte[N];
     uint32_t it = 0;
     bool ok = true;
-    for (int i = 0; ok && piece_of(p, pair, i, w); ++i) {
-      const int g = (w.t / p.n_tiles) * 2 + (int)rank;
-      for (int k = 0; k < w.kn; ++k, ++it) {
-        if ((int)(it % DEC_GROUPS) != grp) continue;
-        const int sc = it % NC, st = it % NS;
-        if (!mbar_wait(&c_full[sc], (it / NC) & 1, p.err)) {
+    while (ok && w.next(p, pair)) {
+      const int g = ((w.t / p.n_tiles) * 2 + (int)rank) & 15;
+      auto fetch = [&](uint32_t i) {
+        const int sc = i % NC;
+        if (!mbar_wait(&c_full[sc], (i / NC) & 1, p.err)) return false;
+        const uint8_t* src = sm + C_OFF + sc * C_BYTES;
+#pragma unroll
+        for (int h = 0; h < N; ++h) {
+          v[h] = *reinterpret_cast<const uint4*>(src + src_off[h]);
+          byte[h] = src[row_off[h] + g];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c_empty[sc]);
+        return true;
+      };
+      ok = fetch(it);
+      for (int k = 0; ok && k < w.kn; ++k, ++it) {
+        const int st = it % NS;
+        uint4 q[N];
+        uint32_t e[N];
+#pragma unroll
+        for (int h = 0; h < N; ++h) {
+          q[h] = v[h];
+          e[h] = byte[h];
+        }
+        if (k + 1 < w.kn && !fetch(it + 1)) {
           ok = false;
           break;
         }
-        const uint8_t* src = sm + C_OFF + sc * C_BYTES;
-        // token row, 64-channel box c / 4, chunks 2 (c % 4) and the next one.
-        // Lanes of chunks 4-7 decode and store the second one first: the eight
-        // lanes of a token then hit all eight 16-byte banks at once.
-        uint8_t* dst = sm + st * STAGE_BYTES + (c >> 2) * BOX8K;
-        const int flip = c >> 2, j = 2 * (c & 3);
-#pragma unroll
-        for (int half = 0; half < PASSES; ++half) {
-          uint4 v[4];
-          uint32_t byte[4];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const int r = t + TR * (4 * half + h);
-            v[h] = *reinterpret_cast<const uint4*>(src + r * CK_GROUP + c * 16);
-            byte[h] = src[CODE_BYTES + r * 16 + (g & 15)];
-          }
-          if (half == PASSES - 1) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c_empty[sc]);
-          }
-          if (half == 0) {
-            if (it >= NS && !mbar_wait(&empty[st], (it / NS - 1) & 1, p.err)) ok = false;
-          }
-          if (!ok) break;
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const int r = t + TR * (4 * half + h);
-            uint8_t* row = dst + r * 128;
-            const uint2 u0 = flip ? make_uint2(v[h].z, v[h].w) : make_uint2(v[h].x, v[h].y);
-            const uint2 u1 = flip ? make_uint2(v[h].x, v[h].y) : make_uint2(v[h].z, v[h].w);
-            const uint32_t m1 = factor1(byte[h]);
-            uint4 o0 = decode8(u0, m1), o1 = decode8(u1, m1);
-            if (byte[h] > 134u) {   // 2^(e + 120) is past bf16's largest power
-              o0 = mul8(o0, factor2(byte[h]));
-              o1 = mul8(o1, factor2(byte[h]));
-            }
-            *reinterpret_cast<uint4*>(row + (((j + flip) ^ (r & 7)) << 4)) = o0;
-            *reinterpret_cast<uint4*>(row + (((j + 1 - flip) ^ (r & 7)) << 4)) = o1;
-          }
+        if (it >= NS && !mbar_wait(&empty[st], (it / NS - 1) & 1, p.err)) {
+          ok = false;
+          break;
         }
-        if (!ok) break;
+        uint8_t* dst = sm + st * STAGE_BYTES;
+#pragma unroll
+        for (int h = 0; h < N; ++h) {
+          uint4 a, b;
+          decode16(q[h], e[h], a, b);
+          *reinterpret_cast<uint4*>(dst + dst_off[h]) = a;
+          *reinterpret_cast<uint4*>(dst + (dst_off[h] ^ 16)) = b;
+        }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_pair(smem_cluster_addr(&full[st], 0));
+        if (lane == 0) mbar_arrive(&full[st]);
       }
     }
   }
@@ -429,7 +479,7 @@ __global__ void __launch_bounds__(256) dw_join_kernel(const DwParams p, int bn) 
   const long long u0 = (long long)tile * p.steps, u1 = u0 + p.steps;
   const int pa = (int)(u0 / p.chunk), pb = (int)((u1 - 1) / p.chunk);
   // the tile is the first piece of every pair after pa
-  const int ia = tile - (int)(pa * p.chunk / p.steps);
+  const int ia = tile - (int)((long long)pa * p.chunk / p.steps);
   const float* src = p.frag + (long long)r * bn + c;
   const long long slot = 256LL * bn;
   float4 s = *reinterpret_cast<const float4*>(src + (pa * p.max_frags + ia) * slot);
@@ -496,7 +546,7 @@ __global__ void __launch_bounds__(256) dy_pieces_kernel(const T* __restrict__ dy
 // ---------------------------------------------------------------- host side
 struct DwPlan {
   int bn = 0, pieces = 1, np = 0;
-  bool convert = false;
+  bool convert = false, fits = false;   // fits: the step counts stay in 32 bits
   DwParams p{};
   size_t dy_bytes = 0, frag_bytes = 0;
   int frag_slots = 0;
@@ -530,7 +580,11 @@ DwPlan dw_plan(int rows, int d, int n, bool fp32) {
   p.pieces = pl.pieces;
   p.rounds = p.tiles / PAIRS;
   const long long left = (long long)(p.tiles - p.rounds * PAIRS) * p.steps;
-  p.chunk = std::max<long long>((left + PAIRS - 1) / PAIRS, std::min(p.steps, MIN_STEPS));
+  const long long chunk =
+      std::max<long long>((left + PAIRS - 1) / PAIRS, std::min(p.steps, MIN_STEPS));
+  pl.fits = chunk <= INT_MAX - p.steps;
+  if (!pl.fits) return pl;
+  p.chunk = (int)chunk;
   p.max_frags = p.steps ? (int)((p.chunk + p.steps - 2) / p.steps) + 1 : 0;
   pl.frag_slots = left > 0 ? (int)((left + p.chunk - 1) / p.chunk) * p.max_frags : 0;
   if (pl.convert) pl.dy_bytes = up1k((size_t)pl.pieces * rows * pl.np * 2);
@@ -538,7 +592,7 @@ DwPlan dw_plan(int rows, int d, int n, bool fp32) {
   return pl;
 }
 
-// Byte tensor of the checkpoint rows, without swizzling.
+// Byte tensor of the checkpoint rows; boxes of 128 bytes a row are swizzled.
 cudaError_t byte_map(CUtensorMap* out, const void* base, uint64_t width, uint64_t rows,
                      uint64_t pitch, uint32_t box_w) {
   auto enc = tmap_encoder();
@@ -547,12 +601,15 @@ cudaError_t byte_map(CUtensorMap* out, const void* base, uint64_t width, uint64_
   const cuuint32_t box[2] = {box_w, KT}, one[2] = {1, 1};
   const CUresult r =
       enc(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, str, box, one,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+          CU_TENSOR_MAP_INTERLEAVE_NONE,
+          box_w == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
           CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 }  // namespace
+
+bool ckpt_dw_fits(int rows, int d, int n, bool fp32) { return dw_plan(rows, d, n, fp32).fits; }
 
 size_t ckpt_dw_ws_bytes(int rows, int d, int n, bool fp32) {
   if (rows == 0) return 0;
@@ -617,3 +674,4 @@ cudaError_t launch_ckpt_dw(int rows, int d, int n, bool fp32, const void* ck, co
 }
 
 }  // namespace laga
+

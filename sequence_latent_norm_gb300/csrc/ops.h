@@ -32,6 +32,8 @@ cudaError_t launch_ckpt_pack(int rows, int d, bool fp32, const void* x, void* ck
 cudaError_t launch_ckpt_unpack(int rows, int d, bool fp32, const void* ck, void* x,
                                cudaStream_t st);
 
+// Whether the sizes stay inside the kernel's 32-bit step counts.
+bool ckpt_dw_fits(int rows, int d, int n, bool fp32);
 size_t ckpt_dw_ws_bytes(int rows, int d, int n, bool fp32);
 cudaError_t launch_ckpt_dw(int rows, int d, int n, bool fp32, const void* ck, const void* dy,
                            const float* gamma, float* dw, unsigned char* ws, int* err,
