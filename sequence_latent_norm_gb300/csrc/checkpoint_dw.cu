@@ -10,15 +10,15 @@
 // nothing of dy is lost.
 //
 // Pairs of CTAs (two-CTA clusters, cta_group::2, M256 pair MMAs): CTA rank r
-// holds one group of 128 channels and half of the tile's BN columns.  20 warps:
-//   0       TMA producer of dy tiles       (ring of NS stages of 64 tokens)
+// holds one group of 128 channels and half of the tile's BN columns.  28 warps:
+//   0       TMA producer of dy tiles       (ring of NB stages of 64 tokens)
 //   1       TMA producer of code and scale tiles               (NC stages)
 //   2       MMA issuer (rank 0)
 //   2, 3    in rank 1: pass the decoders' arrivals on to rank 0
 //   3       TMEM allocator
-//   4-11    decoders: code tile -> bf16 tile of the stage, MN-major, 128-byte
-//           swizzled
-//   12-19   epilogue: adds up the accumulators of a tile in registers, then
+//   4-19    decoders: code tile -> bf16 tile (NA stages), MN-major, 128-byte
+//           swizzled; eight warps take a step, so two steps are under way
+//   20-27   epilogue: adds up the accumulators of a tile in registers, then
 //           multiplies by gamma and stores
 // A decoder turns 4 codes into bf16 with 9 integer and multiply instructions;
 // the pair's MMAs of a step take 2 BN clocks.
@@ -52,23 +52,31 @@ namespace {
 using namespace sm100;
 
 constexpr int KT = 64;                       // tokens per step
-constexpr int NS = 6, NC = 3;                // ring stages: v and dy tiles, codes
+constexpr int NA = 6, NB = 5, NC = 4;        // ring stages: v tiles, dy tiles, codes
+constexpr int NE = 12;                       // step barriers (full, empty)
 constexpr int BOX8K = 64 * 64 * 2;           // a 64 x 64 bf16 box
 constexpr int A_BYTES = 2 * BOX8K;           // 64 tokens x 128 channels
 constexpr int B_BYTES = 2 * BOX8K;           // 64 tokens x up to 128 columns
 constexpr int CODE_BYTES = KT * CK_GROUP;
 constexpr int SCALE_BYTES = KT * 16;         // 16 groups' scale bytes of each token
 constexpr int C_BYTES = CODE_BYTES + SCALE_BYTES;
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int C_OFF = NS * STAGE_BYTES;
+constexpr int B_OFF = NA * A_BYTES, C_OFF = B_OFF + NB * B_BYTES;
 constexpr int SMEM_BYTES = C_OFF + NC * C_BYTES + 1024;
-constexpr int THREADS = 640;
-constexpr int W_DEC = 4, W_EPI = 12;         // first decoder and epilogue warp
-constexpr int DEC_WARPS = W_EPI - W_DEC;
+constexpr int THREADS = 896;
+constexpr int W_DEC = 4, W_EPI = 20;         // first decoder and epilogue warp
+constexpr int DEC_GROUPS = 2;               // steps under way, one per group of decoders
+constexpr int DEC_WARPS = (W_EPI - W_DEC) / DEC_GROUPS;
+// A waiter that does not wait for every phase of a barrier must see every
+// phase of those it waits on (a parity tells only neighbouring phases apart).
+// Decoder group j sees the steps j, j + DEC_GROUPS, ..., a relay every other
+// pair of steps.
+static_assert(NE % DEC_GROUPS == 0 && NA % DEC_GROUPS == 0 && NC % DEC_GROUPS == 0 && NE % 4 == 0,
+              "a barrier belongs to one group");
+static_assert(NE > NA && NE > NB, "a step's barrier outlives its tiles");
 // Registers a thread: at launch (the most that THREADS threads can have, in
 // steps of 8), and after each warpgroup's setmaxnreg.
 constexpr int REG_LAUNCH = 65536 / THREADS / 8 * 8;
-constexpr int REG_MISC = 32, REG_DEC = 64, REG_EPI = 160;
+constexpr int REG_MISC = 32, REG_DEC = 40, REG_EPI = 152;
 static_assert(W_DEC % 4 == 0 && W_EPI % 4 == 0 && THREADS % 128 == 0, "whole warpgroups");
 static_assert(W_DEC * REG_MISC + (W_EPI - W_DEC) * REG_DEC + (THREADS / 32 - W_EPI) * REG_EPI <=
                   THREADS / 32 * REG_LAUNCH,
@@ -187,7 +195,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   // arrive in both).  full: in rank 1 an arrival of every decoder warp; in rank
   // 0 the same, the bytes of both CTAs' dy tiles, and an arrival that says
   // that rank 1's is complete.  Rank 0's acc_empty: epilogue warps of both.
-  __shared__ uint64_t c_full[NC], c_empty[NC], full[NS], empty[NS], acc_full[2], acc_empty[2];
+  __shared__ uint64_t c_full[NC], c_empty[NC], full[NE], empty[NE], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -199,7 +207,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&c_full[i], 1);
       mbar_init(&c_empty[i], DEC_WARPS);
     }
-    for (int i = 0; i < NS; ++i) {
+    for (int i = 0; i < NE; ++i) {
       mbar_init(&full[i], rank == 0 ? DEC_WARPS + 2 : DEC_WARPS);
       mbar_init(&empty[i], 1);
     }
@@ -229,12 +237,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       while (ok && w.next(p, pair)) {
         const int n0 = (w.t % p.n_tiles) * BN + (int)rank * HALF;
         for (int k = w.k0; k < w.k0 + w.kn; ++k, ++it) {
-          const int st = it % NS;
-          if (it >= NS && !mbar_wait(&empty[st], (it / NS - 1) & 1, p.err)) {
+          // the stage's last tile was step it - NB's
+          if (it >= NB && !mbar_wait(&empty[(it - NB) % NE], ((it - NB) / NE) & 1, p.err)) {
             ok = false;
             break;
           }
-          uint8_t* dst = sm + st * STAGE_BYTES + A_BYTES;
+          const int st = it % NE;
+          uint8_t* dst = sm + B_OFF + it % NB * B_BYTES;
           const uint32_t bar = smem_cluster_addr(&full[st], 0);
           constexpr int BOXES = (HALF + 63) / 64;
           if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * BOXES * BOX8K);
@@ -284,17 +293,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           const uint32_t dst = tmem + (uint32_t)(buf * ACC_COLS);
           const int k1 = min(k0 + CHAIN, w.kn);
           for (int k = k0; k < k1; ++k, ++it) {
-            const int st = it % NS;
-            if (!ready && !mbar_wait(&full[st], (it / NS) & 1, p.err)) {
+            const int st = it % NE;
+            if (!ready && !mbar_wait(&full[st], (it / NE) & 1, p.err)) {
               ok = false;
               break;
             }
             tc_fence_after();
             // ask for the next stage now: the answer arrives while this one's
             // MMAs are issued
-            ready = mbar_test(&full[(it + 1) % NS], ((it + 1) / NS) & 1);
-            const uint32_t alo = sdesc_lo(smem_u32(sm + st * STAGE_BYTES), BOX8K);
-            const uint32_t blo = alo + (A_BYTES >> 4);
+            ready = mbar_test(&full[(it + 1) % NE], ((it + 1) / NE) & 1);
+            const uint32_t alo = sdesc_lo(smem_u32(sm + it % NA * A_BYTES), BOX8K);
+            const uint32_t blo = sdesc_lo(smem_u32(sm + B_OFF + it % NB * B_BYTES), BOX8K);
 #pragma unroll
             for (int kk = 0; kk < KT / 16; ++kk)
               mma_ss_pair(dst, sdesc_make(alo + kk * (2048 >> 4)),
@@ -307,23 +316,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
     }
   } else if (warp < W_DEC) {
-    // Rank 1's warps 2 and 3, a step each in turn: announce its decoded tile to
-    // rank 0.  The decoders' stores are complete for this CTA; the cluster-
-    // scope release that makes them so for the pair takes hundreds of clocks,
+    // Rank 1's warps 2 and 3, two steps each in turn: announce the decoded
+    // tiles to rank 0.  The decoders' stores are complete for this CTA; the
+    // cluster-scope fence that makes them so for the pair takes ~1000 clocks,
     // which the decoders would wait for and these two do not mind.
     if (lane == 0 && rank == 1) {
-      uint32_t base = 0;
-      bool ok = true;
-      while (ok && w.next(p, pair)) {
-        for (uint32_t it = base + ((base ^ warp) & 1); it < base + w.kn; it += 2) {
-          const int st = it % NS;
-          if (!mbar_wait(&full[st], (it / NS) & 1, p.err)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_cluster(smem_cluster_addr(&full[st], 0));
-        }
-        base += w.kn;
+      const uint32_t total = (uint32_t)(p.rounds * p.steps + w.left);
+      for (uint32_t it = 2 * (warp & 1); it < total; it += 4) {
+        const uint32_t last = min(it + 1, total - 1);
+        if (!mbar_wait(&full[it % NE], (it / NE) & 1, p.err)) break;
+        if (last != it && !mbar_wait(&full[last % NE], (last / NE) & 1, p.err)) break;
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        for (uint32_t k = it; k <= last; ++k)
+          asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                           smem_cluster_addr(&full[k % NE], 0))
+                       : "memory");
       }
     }
   } else if (warp >= W_EPI) {
@@ -382,16 +389,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else if (warp >= W_DEC) {
     reg_shrink<REG_DEC>();
-    // A warp takes TOK tokens of every step, a thread 16 codes (chunk c of a
+    // Group j takes the steps j, j + DEC_GROUPS, ...; a warp TOK tokens of a step, a thread 16 codes (chunk c of a
     // 64-channel box) of N of them.  Eight lanes work on the tokens r and r ^ 5
     // of an 8-token swizzle atom and four chunks of one box: their 16-byte
     // accesses hit all eight 16-byte banks, in the code tile (chunk c of token
     // r sits at c ^ r) as in the bf16 tile (chunks 2c and 2c + 1 at their own
-    // index ^ r).  The next step's codes are read before this one's are
-    // decoded.
+    // index ^ r).  The group's next codes are read before these are decoded.
     constexpr int TOK = KT / DEC_WARPS, N = TOK / 4;
     static_assert(TOK == 4 || TOK == 8, "tokens of a warp");
-    const int dw = warp - W_DEC, c = lane & 3, box = lane >> 3 & 1;
+    const int grp = (warp - W_DEC) / DEC_WARPS, dw = (warp - W_DEC) % DEC_WARPS;
+    const int c = lane & 3, box = lane >> 3 & 1;
     uint32_t src_off[N], dst_off[N], row_off[N];
 #pragma unroll
     for (int h = 0; h < N; ++h) {
@@ -405,13 +412,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     uint4 v[N];
     uint32_t byte[N];
-    uint32_t it = 0;
+    uint32_t base = 0;   // steps before this piece
     bool ok = true;
     while (ok && w.next(p, pair)) {
       const int g = ((w.t / p.n_tiles) * 2 + (int)rank) & 15;
-      auto fetch = [&](uint32_t i) {
-        const int sc = i % NC;
-        if (!mbar_wait(&c_full[sc], (i / NC) & 1, p.err)) return false;
+      const uint32_t end = base + w.kn;
+      auto fetch = [&](uint32_t it) {
+        const int sc = it % NC;
+        if (!mbar_wait(&c_full[sc], (it / NC) & 1, p.err)) return false;
         const uint8_t* src = sm + C_OFF + sc * C_BYTES;
 #pragma unroll
         for (int h = 0; h < N; ++h) {
@@ -422,9 +430,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (lane == 0) mbar_arrive(&c_empty[sc]);
         return true;
       };
-      ok = fetch(it);
-      for (int k = 0; ok && k < w.kn; ++k, ++it) {
-        const int st = it % NS;
+      uint32_t it = base + (grp + DEC_GROUPS - base % DEC_GROUPS) % DEC_GROUPS;
+      if (it < end) ok = fetch(it);
+      for (; ok && it < end; it += DEC_GROUPS) {
         uint4 q[N];
         uint32_t e[N];
 #pragma unroll
@@ -432,15 +440,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           q[h] = v[h];
           e[h] = byte[h];
         }
-        if (k + 1 < w.kn && !fetch(it + 1)) {
+        if (it + DEC_GROUPS < end && !fetch(it + DEC_GROUPS)) {
           ok = false;
           break;
         }
-        if (it >= NS && !mbar_wait(&empty[st], (it / NS - 1) & 1, p.err)) {
+        if (it >= NA && !mbar_wait(&empty[(it - NA) % NE], ((it - NA) / NE) & 1, p.err)) {
           ok = false;
           break;
         }
-        uint8_t* dst = sm + st * STAGE_BYTES;
+        uint8_t* dst = sm + it % NA * A_BYTES;
 #pragma unroll
         for (int h = 0; h < N; ++h) {
           uint4 a, b;
@@ -450,8 +458,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[st]);
+        if (lane == 0) mbar_arrive(&full[it % NE]);
       }
+      base = end;
     }
   }
   // neither CTA leaves while the pair's MMAs or the other CTA's arrivals may
