@@ -10,16 +10,20 @@
 // nothing of dy is lost.
 //
 // Pairs of CTAs (two-CTA clusters, cta_group::2, M256 pair MMAs): CTA rank r
-// holds one group of 128 channels and half of the tile's BN columns.  28 warps:
-//   0       TMA producer of dy tiles       (ring of NB stages of 64 tokens)
-//   1       TMA producer of code and scale tiles               (NC stages)
+// holds one group of 128 channels and half of the tile's BN columns.  20 warps:
+//   0       TMA producer of dy tiles        (ring of NB stages)
+//   1       TMA producer of code and scale tiles (NC stages)
 //   2       MMA issuer (rank 0)
 //   2, 3    in rank 1: pass the decoders' arrivals on to rank 0
 //   3       TMEM allocator
-//   4-19    decoders: code tile -> bf16 tile (NA stages), MN-major, 128-byte
-//           swizzled; eight warps take a step, so two steps are under way
-//   20-27   epilogue: adds up the accumulators of a tile in registers, then
+//   4-11    decoders: code tile -> bf16 tile (NA stages), MN-major, 128-byte
+//           swizzled
+//   12-19   epilogue: adds up the accumulators of a tile in registers, then
 //           multiplies by gamma and stores
+// A step is 128 tokens.  Every hand-over between warps costs a few hundred
+// clocks, whatever the step's size, and the issuer's wait, commit and MMAs of
+// a 64-token step took longer than the MMAs ran: with 64 tokens (NA = 6, NB =
+// 5) the kernel took 319 us for 16384 x 7168 x 1536, with 128 it takes 293.
 // A decoder turns 4 codes into bf16 with 9 integer and multiply instructions;
 // the pair's MMAs of a step take 2 BN clocks.
 //
@@ -51,40 +55,37 @@ namespace laga {
 namespace {
 using namespace sm100;
 
-constexpr int KT = 64;                       // tokens per step
-constexpr int NA = 6, NB = 5, NC = 4;        // ring stages: v tiles, dy tiles, codes
-constexpr int NE = 12;                       // step barriers (full, empty)
-constexpr int BOX8K = 64 * 64 * 2;           // a 64 x 64 bf16 box
-constexpr int A_BYTES = 2 * BOX8K;           // 64 tokens x 128 channels
-constexpr int B_BYTES = 2 * BOX8K;           // 64 tokens x up to 128 columns
+constexpr int KT = 128;                      // tokens per step
+constexpr int NA = 3, NB = 2, NC = 3;        // ring stages: v tiles, dy tiles, codes
+constexpr int NE = 4;                        // step barriers (full, empty)
+constexpr int BOX = KT * 64 * 2;             // KT tokens x 64 bf16
+constexpr int A_BYTES = 2 * BOX;             // KT tokens x 128 channels
+constexpr int B_BYTES = 2 * BOX;             // KT tokens x up to 128 columns
 constexpr int CODE_BYTES = KT * CK_GROUP;
 constexpr int SCALE_BYTES = KT * 16;         // 16 groups' scale bytes of each token
 constexpr int C_BYTES = CODE_BYTES + SCALE_BYTES;
 constexpr int B_OFF = NA * A_BYTES, C_OFF = B_OFF + NB * B_BYTES;
 constexpr int SMEM_BYTES = C_OFF + NC * C_BYTES + 1024;
-constexpr int THREADS = 896;
-constexpr int W_DEC = 4, W_EPI = 20;         // first decoder and epilogue warp
-constexpr int DEC_GROUPS = 2;               // steps under way, one per group of decoders
-constexpr int DEC_WARPS = (W_EPI - W_DEC) / DEC_GROUPS;
-// A waiter that does not wait for every phase of a barrier must see every
-// phase of those it waits on (a parity tells only neighbouring phases apart).
-// Decoder group j sees the steps j, j + DEC_GROUPS, ..., a relay every other
-// pair of steps.
-static_assert(NE % DEC_GROUPS == 0 && NA % DEC_GROUPS == 0 && NC % DEC_GROUPS == 0 && NE % 4 == 0,
-              "a barrier belongs to one group");
+constexpr int THREADS = 640;
+constexpr int W_DEC = 4, W_EPI = 12;         // first decoder and epilogue warp
+constexpr int DEC_WARPS = W_EPI - W_DEC;
+// A parity tells only neighbouring phases of a barrier apart, so a waiter has
+// to see every phase of the barriers that it waits on.  Everyone does but the
+// two relays, which take every other step.
+static_assert(NE % 2 == 0, "a step barrier belongs to one relay");
 static_assert(NE > NA && NE > NB, "a step's barrier outlives its tiles");
 // Registers a thread: at launch (the most that THREADS threads can have, in
 // steps of 8), and after each warpgroup's setmaxnreg.
 constexpr int REG_LAUNCH = 65536 / THREADS / 8 * 8;
-constexpr int REG_MISC = 32, REG_DEC = 40, REG_EPI = 152;
+constexpr int REG_MISC = 32, REG_DEC = 64, REG_EPI = 160;
 static_assert(W_DEC % 4 == 0 && W_EPI % 4 == 0 && THREADS % 128 == 0, "whole warpgroups");
 static_assert(W_DEC * REG_MISC + (W_EPI - W_DEC) * REG_DEC + (THREADS / 32 - W_EPI) * REG_EPI <=
                   THREADS / 32 * REG_LAUNCH,
               "the epilogue's warps grow on what the others give back");
-constexpr int CHAIN = 16;
+constexpr int CHAIN = 8;
 constexpr int TMEM_COLS = 512, ACC_COLS = 256;
 constexpr int PAIRS = 76;                    // one pair per two SMs
-constexpr int MIN_STEPS = 8;
+constexpr int MIN_STEPS = 4;
 
 struct DwMaps {
   CUtensorMap codes, scales, dy;
@@ -246,10 +247,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           uint8_t* dst = sm + B_OFF + it % NB * B_BYTES;
           const uint32_t bar = smem_cluster_addr(&full[st], 0);
           constexpr int BOXES = (HALF + 63) / 64;
-          if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * BOXES * BOX8K);
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * BOXES * BOX);
 #pragma unroll
           for (int b = 0; b < BOXES; ++b)
-            tma_load_3d_pair(dst + b * BOX8K, &tm.dy, bar, n0 + b * 64, k / p.pieces * KT,
+            tma_load_3d_pair(dst + b * BOX, &tm.dy, bar, n0 + b * 64, k / p.pieces * KT,
                              k % p.pieces);
         }
       }
@@ -302,8 +303,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             // ask for the next stage now: the answer arrives while this one's
             // MMAs are issued
             ready = mbar_test(&full[(it + 1) % NE], ((it + 1) / NE) & 1);
-            const uint32_t alo = sdesc_lo(smem_u32(sm + it % NA * A_BYTES), BOX8K);
-            const uint32_t blo = sdesc_lo(smem_u32(sm + B_OFF + it % NB * B_BYTES), BOX8K);
+            const uint32_t alo = sdesc_lo(smem_u32(sm + it % NA * A_BYTES), BOX);
+            const uint32_t blo = sdesc_lo(smem_u32(sm + B_OFF + it % NB * B_BYTES), BOX);
 #pragma unroll
             for (int kk = 0; kk < KT / 16; ++kk)
               mma_ss_pair(dst, sdesc_make(alo + kk * (2048 >> 4)),
@@ -316,21 +317,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
     }
   } else if (warp < W_DEC) {
-    // Rank 1's warps 2 and 3, two steps each in turn: announce the decoded
-    // tiles to rank 0.  The decoders' stores are complete for this CTA; the
-    // cluster-scope fence that makes them so for the pair takes ~1000 clocks,
-    // which the decoders would wait for and these two do not mind.
+    // Rank 1's warps 2 and 3, a step each in turn: announce the decoded tile
+    // to rank 0.  The decoders' stores are complete for this CTA; the cluster-
+    // scope release that makes them so for the pair takes ~1000 clocks, which
+    // the decoders would wait for and these two do not mind.
     if (lane == 0 && rank == 1) {
       const uint32_t total = (uint32_t)(p.rounds * p.steps + w.left);
-      for (uint32_t it = 2 * (warp & 1); it < total; it += 4) {
-        const uint32_t last = min(it + 1, total - 1);
+      for (uint32_t it = warp & 1; it < total; it += 2) {
         if (!mbar_wait(&full[it % NE], (it / NE) & 1, p.err)) break;
-        if (last != it && !mbar_wait(&full[last % NE], (last / NE) & 1, p.err)) break;
-        asm volatile("fence.acq_rel.cluster;" ::: "memory");
-        for (uint32_t k = it; k <= last; ++k)
-          asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                           smem_cluster_addr(&full[k % NE], 0))
-                       : "memory");
+        mbar_arrive_cluster(smem_cluster_addr(&full[it % NE], 0));
       }
     }
   } else if (warp >= W_EPI) {
@@ -389,26 +384,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else if (warp >= W_DEC) {
     reg_shrink<REG_DEC>();
-    // Group j takes the steps j, j + DEC_GROUPS, ...; a warp TOK tokens of a step, a thread 16 codes (chunk c of a
-    // 64-channel box) of N of them.  Eight lanes work on the tokens r and r ^ 5
-    // of an 8-token swizzle atom and four chunks of one box: their 16-byte
-    // accesses hit all eight 16-byte banks, in the code tile (chunk c of token
-    // r sits at c ^ r) as in the bf16 tile (chunks 2c and 2c + 1 at their own
-    // index ^ r).  The group's next codes are read before these are decoded.
+    // A warp takes TOK tokens of a step, a thread 16 codes (chunk c of a
+    // 64-channel box) of N of them.  Eight lanes work on the tokens r and
+    // r ^ 5 of an 8-token swizzle atom and four chunks of one box: their
+    // 16-byte accesses hit all eight 16-byte banks, in the code tile (chunk c
+    // of token r sits at c ^ r) as in the bf16 tile (chunks 2c and 2c + 1 at
+    // their own index ^ r).  The next step's codes are read before this one's
+    // are decoded.
     constexpr int TOK = KT / DEC_WARPS, N = TOK / 4;
-    static_assert(TOK == 4 || TOK == 8, "tokens of a warp");
-    const int grp = (warp - W_DEC) / DEC_WARPS, dw = (warp - W_DEC) % DEC_WARPS;
-    const int c = lane & 3, box = lane >> 3 & 1;
-    uint32_t src_off[N], dst_off[N], row_off[N];
+    static_assert(TOK % 8 == 0, "whole swizzle atoms");
+    const int dw = warp - W_DEC, c = lane & 3, box = lane >> 3 & 1;
+    uint32_t src_off[2], dst_off[2], row_off[2];   // of an atom's two token pairs of this lane
 #pragma unroll
-    for (int h = 0; h < N; ++h) {
-      // the atom's token pairs (0, 5), (1, 4), (2, 7), (3, 6), two per 4-token part
-      const int part = TOK == 4 ? dw & 1 : h;
-      const int r = (2 * part + (lane >> 4)) ^ (lane & 4 ? 5 : 0);
-      const int t = (dw * TOK & ~7) + r;
+    for (int h = 0; h < 2; ++h) {
+      const int r = (2 * h + (lane >> 4)) ^ (lane & 4 ? 5 : 0);   // (0, 5), (1, 4), (2, 7), (3, 6)
+      const int t = dw * TOK + r;
       row_off[h] = CODE_BYTES + t * 16;
       src_off[h] = t * CK_GROUP + (((box * 4 + c) ^ r) << 4);
-      dst_off[h] = box * BOX8K + t * 128 + (((2 * c) ^ r) << 4);
+      dst_off[h] = box * BOX + t * 128 + (((2 * c) ^ r) << 4);
     }
     uint4 v[N];
     uint32_t byte[N];
@@ -423,16 +416,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const uint8_t* src = sm + C_OFF + sc * C_BYTES;
 #pragma unroll
         for (int h = 0; h < N; ++h) {
-          v[h] = *reinterpret_cast<const uint4*>(src + src_off[h]);
-          byte[h] = src[row_off[h] + g];
+          v[h] = *reinterpret_cast<const uint4*>(src + src_off[h & 1] + (h >> 1) * 8 * CK_GROUP);
+          byte[h] = src[row_off[h & 1] + (h >> 1) * 8 * 16 + g];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&c_empty[sc]);
         return true;
       };
-      uint32_t it = base + (grp + DEC_GROUPS - base % DEC_GROUPS) % DEC_GROUPS;
-      if (it < end) ok = fetch(it);
-      for (; ok && it < end; it += DEC_GROUPS) {
+      ok = fetch(base);
+      for (uint32_t it = base; ok && it < end; ++it) {
         uint4 q[N];
         uint32_t e[N];
 #pragma unroll
@@ -440,7 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           q[h] = v[h];
           e[h] = byte[h];
         }
-        if (it + DEC_GROUPS < end && !fetch(it + DEC_GROUPS)) {
+        if (it + 1 < end && !fetch(it + 1)) {
           ok = false;
           break;
         }
@@ -453,8 +445,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         for (int h = 0; h < N; ++h) {
           uint4 a, b;
           decode16(q[h], e[h], a, b);
-          *reinterpret_cast<uint4*>(dst + dst_off[h]) = a;
-          *reinterpret_cast<uint4*>(dst + (dst_off[h] ^ 16)) = b;
+          const uint32_t o = dst_off[h & 1] + (h >> 1) * 8 * 128;
+          *reinterpret_cast<uint4*>(dst + o) = a;
+          *reinterpret_cast<uint4*>(dst + (o ^ 16)) = b;
         }
         fence_proxy_async_smem();
         __syncwarp();
