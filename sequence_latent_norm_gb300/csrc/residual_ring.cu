@@ -417,6 +417,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint8_t *bd = buf + q.src[B_D].off, *bh = buf + q.src[B_DH].off;
     const uint8_t *bx = buf + q.src[B_X].off, *by = buf + q.src[B_Y].off, *bg = buf + q.src[B_G].off;
     float m0 = 0.f, m1 = 0.f;
+    // Teams up to 256 threads keep x^ and y^ from one pass over the row to the
+    // next (16384 x 2048 from checkpoints: 97 us, 102 us decoding in every
+    // pass); for the one large team of a CTA the registers do not reach
+    // (16384 x 7168: 410 us decoding again, 498 us keeping them).
+    constexpr bool KEEP = TEAM < 512;
+    V8 hat[KEEP ? NV : 1];
     if (p.pre) {
       float2 t0 = both(0.f), t1 = both(0.f);
 #pragma unroll
@@ -434,6 +440,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             t0 = add2(t0, e);
             t1 = fma2(e, xh.v[k], t1);
           }
+          if (KEEP) hat[i] = xh;
         }
       }
       float s[2] = {t0.x + t0.y, t1.x + t1.y};
@@ -458,7 +465,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (p.pre) {
           V8 dh, xh, g;
           load8(bh, v, dh, T());
-          kept8<T>(bx, p.ckpt, cols, v, st_pre, xh);
+          if (KEEP)
+            xh = hat[i];
+          else
+            kept8<T>(bx, p.ckpt, cols, v, st_pre, xh);
           g_pre.load(v, g);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -470,6 +480,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (p.post) {
           V8 y, g, a;
           kept8<T>(by, p.ckpt, cols, v, st_post, y);
+          if (KEEP) hat[i] = y;
           if (gain) {
             g_post.load(v, g);
           } else {
@@ -512,7 +523,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (v < nvec) {
           if (gain) {
             V8 y;
-            kept8<T>(by, p.ckpt, cols, v, st_post, y);
+            if (KEEP)
+              y = hat[i];
+            else
+              kept8<T>(by, p.ckpt, cols, v, st_post, y);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               f[i].v[k] = mul2(both(st_post.y),
