@@ -9,7 +9,6 @@ exact in bf16.  :func:`pack8` makes one, ``unpack`` reads it back and
 
 from __future__ import annotations
 
-import contextlib
 import math
 
 import torch
@@ -19,30 +18,41 @@ from . import _lib
 IO_NAME = {torch.bfloat16: "bf16", torch.float32: "fp32"}
 
 
-@contextlib.contextmanager
-def on_stream(device, stream):
+class on_stream:
     """Run on ``device`` and ``stream`` (None: the device's current stream);
-    yields the stream's handle.  What is allocated inside belongs to that
-    stream, so its memory is reused in that stream's order."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream().cuda_stream
-        else:
-            if stream.device != device:
-                raise ValueError(f"stream on {stream.device}, tensors on {device}")
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+    entering gives the stream's handle.  What is allocated inside belongs to
+    that stream, so its memory is reused in that stream's order."""
+
+    __slots__ = ("device", "stream", "inner")
+
+    def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream on {stream.device}, tensors on {device}")
+        self.device, self.stream, self.inner = device, stream, None
+
+    def __enter__(self):
+        if self.stream is not None:
+            self.inner = torch.cuda.stream(self.stream)   # its device, too
+        elif torch.cuda.current_device() != self.device.index:
+            self.inner = torch.cuda.device(self.device)
+        if self.inner is not None:
+            self.inner.__enter__()
+        return (self.stream or torch.cuda.current_stream(self.device)).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.inner is not None:
+            self.inner.__exit__(*exc)
 
 
 def need(t, name, dtype, device=None, shape=None):
     """Check one CUDA tensor argument and return its address."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype} != {dtype}")
-    if t.device.type != "cuda" or (device is not None and t.device != device):
+    if not t.is_cuda or (device is not None and t.device != device):
         raise ValueError(f"{name}: on {t.device}, expected {device if device else 'a CUDA device'}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")

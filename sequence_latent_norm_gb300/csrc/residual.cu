@@ -28,13 +28,12 @@ LAGA_DEVINL void st1(void* p, long long i, float v) { static_cast<T*>(p)[i] = fr
 
 // ---------------------------------------------------- rows of any width
 // One CTA per row, one element per access, the row's fp32 values in shared
-// memory between the passes.  Warp w owns the 128-channel groups w, w + 8,
-// ..., lane l the channels l, l + 32, l + 64, l + 96 of a group, in every
-// pass, so a thread only ever reads what it wrote itself.
-constexpr int GT = 256;
-
-template <int K>
-LAGA_DEVINL void block_sum(float (&v)[K], float* red) {   // red [8][K]
+// memory between the passes, and the backward's column sums beside them over
+// all rows of a CTA.  Warp w owns the 128-channel groups w, w + GT / 32, ...,
+// lane l the channels l, l + 32, l + 64, l + 96 of a group, in every pass, so
+// a thread only ever reads what it wrote itself.
+template <int GT, int K>
+LAGA_DEVINL void block_sum(float (&v)[K], float* red) {   // red [GT / 32][K]
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
   __syncthreads();   // the previous reduction has been read
@@ -49,7 +48,7 @@ LAGA_DEVINL void block_sum(float (&v)[K], float* red) {   // red [8][K]
   }
 }
 
-template <typename F>
+template <int GT, typename F>
 LAGA_DEVINL void for_cols(int d, F f) {
   for (int g = threadIdx.x >> 5; g * CK_GROUP < d; g += GT / 32)
 #pragma unroll
@@ -60,7 +59,7 @@ LAGA_DEVINL void for_cols(int d, F f) {
 }
 
 // A row's values v(c) as codes and scales
-template <typename F>
+template <int GT, typename F>
 LAGA_DEVINL void quantise_row(int d, uint8_t* row, F v) {
   const int cols = ck_cols(d), lane = threadIdx.x & 31;
   for (int g = threadIdx.x >> 5; g < cols / CK_GROUP; g += GT / 32) {
@@ -85,36 +84,36 @@ LAGA_DEVINL void quantise_row(int d, uint8_t* row, F v) {
 }
 
 // mean and 1/std of a row's values v(c)
-template <typename F>
+template <int GT, typename F>
 LAGA_DEVINL float2 row_stat(int d, float inv_d, int norm, float eps, float* red, F v) {
   if (norm == LAGA_NORM_NONE) return make_float2(0.f, 1.f);
   float mean = 0.f;
   if (norm == LAGA_NORM_LAYER) {
     float s[1] = {0.f};
-    for_cols(d, [&](int c) { s[0] += v(c); });
-    block_sum<1>(s, red);
+    for_cols<GT>(d, [&](int c) { s[0] += v(c); });
+    block_sum<GT, 1>(s, red);
     mean = s[0] * inv_d;
   }
   float q[1] = {0.f};
-  for_cols(d, [&](int c) { const float t = v(c) - mean; q[0] += t * t; });
-  block_sum<1>(q, red);
+  for_cols<GT>(d, [&](int c) { const float t = v(c) - mean; q[0] += t * t; });
+  block_sum<GT, 1>(q, red);
   return make_float2(mean, 1.f / sqrtf(q[0] * inv_d + eps));
 }
 
-template <typename T>
-__global__ void __launch_bounds__(GT) res_fwd_rows_kernel(const ResArgs p) {
+template <typename T, int GT>
+__global__ void __launch_bounds__(GT, 2048 / GT) res_fwd_rows_kernel(const ResArgs p) {
   extern __shared__ float xs[];   // [d]
   __shared__ float red[GT / 32];
   const int d = p.d, pitch = ck_pitch(d);
   for (long long r = blockIdx.x; r < p.rows; r += gridDim.x) {
     const long long o = r * d;
-    for_cols(d, [&](int c) { xs[c] = ld1<T>(p.x.x, o + c); });
+    for_cols<GT>(d, [&](int c) { xs[c] = ld1<T>(p.x.x, o + c); });
     if (p.post) {
       const float alpha = *p.x.alpha;
-      const float2 st = row_stat(d, p.inv_d, p.norm_post, p.eps, red,
+      const float2 st = row_stat<GT>(d, p.inv_d, p.norm_post, p.eps, red,
                                  [&](int c) { return ld1<T>(p.x.y, o + c); });
       auto hat = [&](int c) { return (ld1<T>(p.x.y, o + c) - st.x) * st.y; };
-      for_cols(d, [&](int c) {
+      for_cols<GT>(d, [&](int c) {
         float z = hat(c);
         if (p.norm_post != LAGA_NORM_NONE) z *= p.x.gamma_post[c];
         if (p.gate != LAGA_GATE_NONE)
@@ -122,14 +121,14 @@ __global__ void __launch_bounds__(GT) res_fwd_rows_kernel(const ResArgs p) {
         xs[c] += alpha * z;
         st1<T>(p.x.x_out, o + c, xs[c]);
       });
-      if (p.ckpt) quantise_row(d, static_cast<uint8_t*>(p.x.ck_y) + r * pitch, hat);
+      if (p.ckpt) quantise_row<GT>(d, static_cast<uint8_t*>(p.x.ck_y) + r * pitch, hat);
       if (threadIdx.x == 0) reinterpret_cast<float2*>(p.x.stat_post)[r] = st;
     }
     if (p.pre) {
-      const float2 st = row_stat(d, p.inv_d, p.norm_pre, p.eps, red, [&](int c) { return xs[c]; });
+      const float2 st = row_stat<GT>(d, p.inv_d, p.norm_pre, p.eps, red, [&](int c) { return xs[c]; });
       auto hat = [&](int c) { return (xs[c] - st.x) * st.y; };
-      for_cols(d, [&](int c) { st1<T>(p.x.h, o + c, hat(c) * p.x.gamma_pre[c]); });
-      if (p.ckpt) quantise_row(d, static_cast<uint8_t*>(p.x.ck_x) + r * pitch, hat);
+      for_cols<GT>(d, [&](int c) { st1<T>(p.x.h, o + c, hat(c) * p.x.gamma_pre[c]); });
+      if (p.ckpt) quantise_row<GT>(d, static_cast<uint8_t*>(p.x.ck_x) + r * pitch, hat);
       if (threadIdx.x == 0) reinterpret_cast<float2*>(p.x.stat_pre)[r] = st;
     }
   }
@@ -143,44 +142,42 @@ LAGA_DEVINL float kept_hat(const void* kept, int ckpt, int d, long long r, int c
   return ck_value2(row[c], ck_unit(row[ck_cols(d) + c / CK_GROUP])).x;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(GT) res_bwd_rows_kernel(const ResArgs p) {
-  extern __shared__ float ds[];   // [d]: dx, then f
+template <typename T, int GT>
+__global__ void __launch_bounds__(GT, 2048 / GT) res_bwd_rows_kernel(const ResArgs p) {
+  extern __shared__ float ds[];   // [3][d]: dx, then f; the column sums
   __shared__ float red[4 * GT / 32];
   const int d = p.d;
   float d_alpha = 0.f;
-  // this CTA's rows of the column partials; a thread adds to its own columns
-  float* const pp = p.part_post + (long long)blockIdx.x * d;
-  float* const pq = p.part_pre + (long long)blockIdx.x * d;
+  float *const pp = ds + d, *const pq = ds + 2 * d;
+  for_cols<GT>(d, [&](int c) { pp[c] = pq[c] = 0.f; });
   for (long long r = blockIdx.x; r < p.rows; r += gridDim.x) {
     const long long o = r * d;
-    const bool first = r == blockIdx.x;
     if (p.pre) {
       const float2 st = reinterpret_cast<const float2*>(p.x.stat_pre)[r];
       auto hat = [&](int c) { return kept_hat<T>(p.x.kept_x, p.ckpt, d, r, c, st); };
       float s[2] = {0.f, 0.f};
-      for_cols(d, [&](int c) {
+      for_cols<GT>(d, [&](int c) {
         const float dh = ld1<T>(p.x.dh, o + c), x = hat(c), e = dh * p.x.gamma_pre[c];
-        pq[c] = (first ? 0.f : pq[c]) + dh * x;
+        pq[c] += dh * x;
         s[0] += e;
         s[1] += e * x;
       });
-      block_sum<2>(s, red);
+      block_sum<GT, 2>(s, red);
       const float m0 = p.norm_pre == LAGA_NORM_LAYER ? s[0] * p.inv_d : 0.f, m1 = s[1] * p.inv_d;
-      for_cols(d, [&](int c) {
+      for_cols<GT>(d, [&](int c) {
         const float e = ld1<T>(p.x.dh, o + c) * p.x.gamma_pre[c];
         const float D = p.x.dx_out ? ld1<T>(p.x.dx_out, o + c) : 0.f;
         ds[c] = D + st.y * (e - m0 - hat(c) * m1);
         st1<T>(p.x.dx, o + c, ds[c]);
       });
     } else {
-      for_cols(d, [&](int c) { ds[c] = ld1<T>(p.x.dx_out, o + c); });
+      for_cols<GT>(d, [&](int c) { ds[c] = ld1<T>(p.x.dx_out, o + c); });
     }
     if (p.post) {
       const float alpha = *p.x.alpha;
       const float2 st = reinterpret_cast<const float2*>(p.x.stat_post)[r];
       float s[4] = {0.f, 0.f, 0.f, 0.f};   // f, f y^, dx s z, token gate
-      for_cols(d, [&](int c) {
+      for_cols<GT>(d, [&](int c) {
         const float y = kept_hat<T>(p.x.kept_y, p.ckpt, d, r, c, st);
         const float g = p.norm_post != LAGA_NORM_NONE ? p.x.gamma_post[c] : 1.f;
         float2 sg = make_float2(1.f, 0.f);
@@ -191,23 +188,28 @@ __global__ void __launch_bounds__(GT) res_bwd_rows_kernel(const ResArgs p) {
         const float da = dz * sg.y * z;
         if (p.gate == LAGA_GATE_FULL) st1<T>(p.x.dgate, o + c, da);
         s[3] += da;
-        if (p.norm_post != LAGA_NORM_NONE) pp[c] = (first ? 0.f : pp[c]) + dz * y;
+        if (p.norm_post != LAGA_NORM_NONE) pp[c] += dz * y;
         s[0] += f;
         s[1] += f * y;
         ds[c] = f;
       });
-      block_sum<4>(s, red);
+      block_sum<GT, 4>(s, red);
       d_alpha += s[2];
       if (p.gate == LAGA_GATE_TOKEN && threadIdx.x == 0) st1<T>(p.x.dgate, r, s[3]);
       const bool none = p.norm_post == LAGA_NORM_NONE;
       const float m0 = p.norm_post == LAGA_NORM_LAYER ? s[0] * p.inv_d : 0.f;
       const float m1 = none ? 0.f : s[1] * p.inv_d;
-      for_cols(d, [&](int c) {
+      for_cols<GT>(d, [&](int c) {
         const float y = none ? 0.f : kept_hat<T>(p.x.kept_y, p.ckpt, d, r, c, st);
         st1<T>(p.x.dy, o + c, (none ? 1.f : st.y) * (ds[c] - m0 - y * m1));
       });
     }
   }
+  const long long slot = (long long)blockIdx.x * d;
+  for_cols<GT>(d, [&](int c) {
+    if (p.post && p.norm_post != LAGA_NORM_NONE) p.part_post[slot + c] = pp[c];
+    if (p.pre) p.part_pre[slot + c] = pq[c];
+  });
   if (p.post && threadIdx.x == 0) p.part_alpha[blockIdx.x] = d_alpha;
 }
 
@@ -247,9 +249,20 @@ __global__ void __launch_bounds__(512) res_colsum_kernel(const float* part_post,
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Rows of any width: 2048 threads an SM (32 registers each), which hide the
+// latency of the scalar accesses, in CTAs of 256 threads, or of 1024 where
+// shared memory does not hold `arrays` fp32 rows for eight CTAs.  With 41
+// registers and so fewer threads the forward took 110 us instead of 86 (4096 x
+// 5001 bf16), and with 256 threads throughout, the sums in global memory, the
+// backward 443 us instead of 294.
+bool rows_wide(int d, int arrays) { return arrays * d * 4 + 2048 > 220 * 1024 / 8; }
+int rows_ctas(int d, int arrays) {
+  return std::max(1, std::min(rows_wide(d, arrays) ? 2 : 8, 220 * 1024 / (arrays * d * 4 + 2048)));
+}
+
 // Column partial slots of a backward launch
 int bwd_slots(const laga_res_dims& d) {
-  return ring_ok(d, true) ? ring_slots(d) : std::min(d.rows, 2 * kSms);
+  return ring_ok(d, true) ? ring_slots(d) : std::min(d.rows, kSms * rows_ctas(d.d, 3));
 }
 
 ResArgs make_args(const laga_res_dims& d, const ResPtrs& x) {
@@ -300,11 +313,13 @@ cudaError_t launch_res_fwd(const laga_res_dims& d, const ResPtrs& x, cudaStream_
   const ResArgs a = make_args(d, x);
   if (ring_ok(d, false)) return launch_ring_fwd(d, a, st);
   const size_t smem = (size_t)d.d * 4;
-  auto k = d.io_dtype == LAGA_FP32 ? res_fwd_rows_kernel<float> : res_fwd_rows_kernel<__nv_bfloat16>;
+  const bool f32 = d.io_dtype == LAGA_FP32, wide = rows_wide(d.d, 1);
+  auto k = wide ? (f32 ? res_fwd_rows_kernel<float, 1024> : res_fwd_rows_kernel<__nv_bfloat16, 1024>)
+                : (f32 ? res_fwd_rows_kernel<float, 256> : res_fwd_rows_kernel<__nv_bfloat16, 256>);
   cudaError_t e = allow_smem(k, smem);
   if (e != cudaSuccess) return e;
   LaunchScope ls_("res_fwd", st);
-  k<<<std::min(d.rows, 8 * kSms), GT, smem, st>>>(a);
+  k<<<std::min(d.rows, kSms * rows_ctas(d.d, 1)), wide ? 1024 : 256, smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -318,12 +333,14 @@ cudaError_t launch_res_bwd(const laga_res_dims& d, const ResPtrs& x, cudaStream_
   if (d.rows > 0 && ring_ok(d, true)) {
     if ((e = launch_ring_bwd(d, a, st)) != cudaSuccess) return e;
   } else if (d.rows > 0) {
-    const size_t smem = (size_t)d.d * 4;
-    auto k = d.io_dtype == LAGA_FP32 ? res_bwd_rows_kernel<float>
-                                     : res_bwd_rows_kernel<__nv_bfloat16>;
+    const size_t smem = (size_t)3 * d.d * 4;
+    const bool f32 = d.io_dtype == LAGA_FP32, wide = rows_wide(d.d, 3);
+    auto k = wide
+                 ? (f32 ? res_bwd_rows_kernel<float, 1024> : res_bwd_rows_kernel<__nv_bfloat16, 1024>)
+                 : (f32 ? res_bwd_rows_kernel<float, 256> : res_bwd_rows_kernel<__nv_bfloat16, 256>);
     if ((e = allow_smem(k, smem)) != cudaSuccess) return e;
     LaunchScope ls_("res_bwd", st);
-    k<<<slots, GT, smem, st>>>(a);
+    k<<<slots, wide ? 1024 : 256, smem, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   LaunchScope ls_("res_colsum", st);

@@ -570,6 +570,8 @@ struct RingPlan {
   uint32_t row_bytes[5] = {};
 };
 
+int ring_grid(const laga_res_dims& d) { return std::min(d.rows, kSms); }
+
 // The smallest team whose rings hold two rows each (one row buffer is worked
 // on, the other filled), else the smallest that holds one; team 0: none does.
 RingPlan ring_plan(const laga_res_dims& d, bool bwd) {
@@ -596,16 +598,17 @@ RingPlan ring_plan(const laga_res_dims& d, bool bwd) {
         if (depth < want) continue;
         best.team = sh[i].team;
         best.nv = sh[i].nv;
-        best.depth = depth;
-        best.gain_bytes = g;
+        // Rows of one team.  With one, the gains would be copied for a single
+        // use, and a short ring keeps a small call's shared memory small.
+        const int per = ring_grid(d) ? (d.rows - 1) / (ring_grid(d) * (THREADS / sh[i].team)) + 1 : 1;
+        best.depth = std::min(depth, per);
+        best.gain_bytes = per > 1 ? g : 0;
         for (int k = 0; k < 5; ++k) best.row_bytes[k] = bwd ? b[k] : f[k];
         return best;
       }
     }
   return best;
 }
-
-int ring_grid(const laga_res_dims& d) { return std::min(d.rows, kSms); }
 
 // dx_out may be missing: its place in the row buffer then stays unread
 RingArgs ring_args(const RingPlan& pl, const void* const (&base)[5]) {
@@ -643,8 +646,11 @@ Kernel bwd_kernel(int team, int nv) {
 cudaError_t launch(const char* name, Kernel k, const RingPlan& pl, const RingArgs& q,
                    const laga_res_dims& d, const ResArgs& a, cudaStream_t st) {
   const size_t smem = pl.gain_bytes + (size_t)(THREADS / pl.team) * pl.depth * q.stage_bytes;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  if (smem > 44 * 1024) {   // 48 KB with the static part need no opt-in
+    const cudaError_t e =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   LaunchScope ls_(name, st);
   k<<<ring_grid(d), THREADS, smem, st>>>(a, q);
   return cudaGetLastError();
