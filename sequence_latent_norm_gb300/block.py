@@ -24,6 +24,15 @@ sequence, so their gradients are summed over the ranks (all-reduce);
 ``attn`` already assembles dW_kv_b along the head axis and sums dgamma.
 The weight gradients come out of the GEMMs in the I/O dtype and are
 returned in (at least) fp32.
+
+What the block holds of h between the passes serves dW_q and dW_kv_a alone.
+``checkpoint="fp8"`` holds it in 8 bits (``checkpoint.py``) and takes both
+gradients, in fp32, straight from the codes.
+
+``LagaResidualStack`` puts blocks on a residual stream, each with its norm in
+front, and its norm, gate and residual scale behind (``residual.py``); between
+two blocks both run in one kernel.  The paper leaves this part of the
+transformer open.
 """
 
 from __future__ import annotations
@@ -34,6 +43,8 @@ import torch.distributed as dist
 
 from .sp import LibraryCompute, SequenceParallelLaga
 from .api import Shard
+from .checkpoint import Checkpoint8, pack8, weight_grad8
+from .residual import ResidualNorm
 
 
 def _wide(t):
@@ -46,9 +57,14 @@ class LagaAttentionBlock:
     c, w_kvb, gamma, cos, sin) -> (out, lse)`` on the rank's chunk,
     ``backward(d_out) -> (dq, dc, dw_kvb, dgamma)``); ``group`` is the
     process group whose ranks share the weights (None: one rank, no
-    collective)."""
+    collective); ``checkpoint`` how h is held between the passes ("none": as
+    given, "fp8": in 8 bits, on a CUDA device)."""
 
-    def __init__(self, attn, n_h: int, group=None, distributed: bool = False):
+    def __init__(self, attn, n_h: int, group=None, distributed: bool = False,
+                 checkpoint: str = "none"):
+        if checkpoint not in ("none", "fp8"):
+            raise ValueError(f"checkpoint={checkpoint!r}: one of none, fp8")
+        self.checkpoint = checkpoint
         self.attn = attn
         self.n_h = n_h
         self.group = group
@@ -57,33 +73,40 @@ class LagaAttentionBlock:
         self._saved = None
 
     @classmethod
-    def sequence_parallel(cls, n_h: int, S: int, *, group=None, device=None, **dims):
+    def sequence_parallel(cls, n_h: int, S: int, *, group=None, device=None,
+                          checkpoint: str = "none", **dims):
         """A rank of a sequence-parallel group (torch.distributed must be
         initialised): the library on its n_h/P heads behind sp.py's
         exchanges."""
         return cls(SequenceParallelLaga(n_h, S, group=group, device=device, **dims), n_h, group,
-                   distributed=True)
+                   distributed=True, checkpoint=checkpoint)
 
     @classmethod
-    def single(cls, n_h: int, S: int, *, device=None, B: int = 1, **dims):
+    def single(cls, n_h: int, S: int, *, device=None, B: int = 1, checkpoint: str = "none",
+               **dims):
         """All n_h heads and the whole sequence on one device, no process
         group: the library directly."""
         shard = Shard(S=S, H=n_h, n_h_total=n_h, B=B, **dims)
-        return cls(LibraryCompute(shard, device), n_h)
+        return cls(LibraryCompute(shard, device), n_h, checkpoint=checkpoint)
 
-    def forward(self, h, w_q, w_kva, gamma, w_kvb, w_o, cos, sin):
+    def forward(self, h, w_q, w_kva, gamma, w_kvb, w_o, cos, sin, *, kept=None, kept_gain=None):
         """h [B, S_r, d_model] (this rank's chunk); w_q [d_model, n_h (d_nope
         + d_rope)]; w_kva [d_model, d_kv + d_rope]; gamma [d_kv] fp32;
         w_kvb [d_kv, n_h (d_nope + d_v)]; w_o [n_h d_v, d_model]; cos/sin
         [S, d_rope/2] fp32 for the full sequence.  Returns y [B, S_r,
-        d_model] in h's dtype."""
+        d_model] in h's dtype.  ``kept``, a Checkpoint8 with h = kept *
+        kept_gain (fp32 [d_model] or None), is held instead of h."""
         B, S_r, d_model = h.shape
         h_flat = h.reshape(B * S_r, d_model)
         q = (h_flat @ w_q).reshape(B, S_r, self.n_h, -1)
         c = (h_flat @ w_kva).reshape(B, S_r, -1)
         out, _ = self.attn.forward(q, c, w_kvb, gamma, cos, sin)
         out_flat = out.reshape(B * S_r, -1)
-        self._saved = (h_flat, w_q, w_kva, w_o, out_flat, out.shape, h.shape)
+        if kept is None and self.checkpoint == "fp8":
+            kept = pack8(h_flat)
+        elif kept is None:
+            kept = h_flat
+        self._saved = (kept, kept_gain, w_q, w_kva, w_o, out_flat, out.shape, h.shape)
         return (out_flat @ w_o).reshape(B, S_r, d_model)
 
     def _all_reduce(self, t, what):
@@ -99,17 +122,96 @@ class LagaAttentionBlock:
         [B, S_r, d_model] in h's dtype; dw_q, dw_kva, dw_o (fp32, summed
         over the ranks); dw_kvb [d_kv, n_h (d_nope + d_v)] and dgamma
         [d_kv] (fp32, from ``attn``)."""
-        h_flat, w_q, w_kva, w_o, out_flat, out_shape, h_shape = self._saved
-        dy_flat = dy.reshape(h_flat.shape[0], -1)
+        kept, gain, w_q, w_kva, w_o, out_flat, out_shape, h_shape = self._saved
+        rows = out_flat.shape[0]
+        dy_flat = dy.reshape(rows, -1)
         dw_o = _wide(out_flat.t() @ dy_flat)
         d_out = (dy_flat @ w_o.t()).reshape(out_shape)
         dq, dc, dw_kvb, dgamma = self.attn.backward(d_out)
-        dq_flat = dq.reshape(h_flat.shape[0], -1)
-        dc_flat = dc.reshape(h_flat.shape[0], -1).to(dq.dtype)
-        dh = (dq_flat @ w_q.t() + dc_flat @ w_kva.t()).reshape(h_shape)
-        dw_q = _wide(h_flat.t() @ dq_flat)
-        dw_kva = _wide(h_flat.t() @ dc_flat)
+        dq_flat = dq.reshape(rows, -1)
+        dc_flat = dc.reshape(rows, -1)
+        dc_io = dc_flat.to(dq.dtype)
+        dh = (dq_flat @ w_q.t() + dc_io @ w_kva.t()).reshape(h_shape)
+        if isinstance(kept, Checkpoint8):
+            dw_q = weight_grad8(kept, dq_flat, gain)
+            dw_kva = weight_grad8(kept, dc_flat, gain)
+        else:
+            dw_q = _wide(kept.t() @ dq_flat)
+            dw_kva = _wide(kept.t() @ dc_io)
         return dict(dh=dh, dw_q=self._all_reduce(dw_q, "all_reduce_dw_q"),
                     dw_kva=self._all_reduce(dw_kva, "all_reduce_dw_kva"),
                     dw_o=self._all_reduce(dw_o, "all_reduce_dw_o"),
                     dw_kvb=dw_kvb, dgamma=dgamma)
+
+
+class LagaResidualStack:
+    """Attention blocks on a residual stream x [B, S_r, d_model]:
+
+        h_l = N_pre(x_l) gamma_pre,  y_l = block_l(h_l),
+        x_{l+1} = x_l + alpha s N_post(y_l) gamma_post
+
+    ``blocks``: one LagaAttentionBlock a layer.  norm_pre, norm_post ("none":
+    a plain gated residual add) and gate as for ResidualNorm.  ``ckpt`` holds
+    the normalised x and y of every layer as 8-bit checkpoints; the one of x
+    also serves the layer's dW_q and dW_kv_a, so neither x nor h is held in
+    the I/O type."""
+
+    def __init__(self, blocks, d_model: int, *, norm_pre: str = "rms", norm_post: str = "none",
+                 gate: str = "none", ckpt: bool = False, io_dtype: str = "bf16", eps: float = 1e-5,
+                 device="cuda"):
+        if not blocks:
+            raise ValueError("at least one block")
+        kw = dict(norm_pre=norm_pre, norm_post=norm_post, gate=gate, ckpt=ckpt, io_dtype=io_dtype,
+                  eps=eps, device=device)
+        self.blocks = list(blocks)
+        self.first = ResidualNorm(d_model, post=False, **kw)
+        self.between = ResidualNorm(d_model, **kw)
+        self.last = ResidualNorm(d_model, pre=False, **kw)
+        self._saved = None
+
+    def forward(self, x, layers, cos, sin):
+        """``layers``: per block a dict of w_q, w_kva, gamma, w_kvb, w_o (see
+        LagaAttentionBlock.forward), gamma_pre [d_model] and alpha [1] fp32,
+        and, where they apply, gamma_post [d_model] fp32 and gate logits [B,
+        S_r, d_model or 1].  Returns x behind the last block."""
+        if len(layers) != len(self.blocks):
+            raise ValueError(f"{len(layers)} layers for {len(self.blocks)} blocks")
+        r = self.first.forward(x, gamma_pre=layers[0]["gamma_pre"])
+        kept = [r.saved]                      # of the norm in front of block l
+        behind = []                           # of the residual half behind block l
+        for i, (block, w) in enumerate(zip(self.blocks, layers)):
+            in_bits = self.first.ckpt
+            y = block.forward(r.h, w["w_q"], w["w_kva"], w["gamma"], w["w_kvb"], w["w_o"], cos, sin,
+                              kept=kept[i].x if in_bits else None,
+                              kept_gain=w["gamma_pre"] if in_bits else None)
+            ends = i + 1 == len(layers)
+            step = self.last if ends else self.between
+            r = step.forward(r.x, y, gate=w.get("gate"), alpha=w["alpha"],
+                             gamma_post=w.get("gamma_post"),
+                             gamma_pre=None if ends else layers[i + 1]["gamma_pre"])
+            behind.append(r.saved)
+            kept.append(r.saved)
+        self._saved = (kept[0], behind)
+        return r.x
+
+    def backward(self, dx):
+        """dx of the stream behind the last block.  Returns (dx in front of the
+        first block, per block a dict: the block's weight gradients, and
+        dgamma_pre, dalpha, dgamma_post and dgate where they apply; those of
+        the shared parameters summed over the ranks)."""
+        first, behind = self._saved
+        grads = [None] * len(self.blocks)
+        g = self.last.backward(behind[-1], dx)
+        for i in reversed(range(len(self.blocks))):
+            block = self.blocks[i]
+            out = {k: block._all_reduce(v, "all_reduce_" + k) for k, v in
+                   (("dalpha", g.dalpha), ("dgamma_post", g.dgamma_post)) if v is not None}
+            if g.dgate is not None:
+                out["dgate"] = g.dgate
+            out.update(block.backward(g.dy))
+            dh = out.pop("dh")
+            g = (self.between.backward(behind[i - 1], g.dx, dh) if i else
+                 self.first.backward(first, g.dx, dh))
+            out["dgamma_pre"] = block._all_reduce(g.dgamma_pre, "all_reduce_dgamma_pre")
+            grads[i] = out
+        return g.dx, grads
