@@ -419,8 +419,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           v[h] = *reinterpret_cast<const uint4*>(src + src_off[h & 1] + (h >> 1) * 8 * CK_GROUP);
           byte[h] = src[row_off[h & 1] + (h >> 1) * 8 * 16 + g];
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c_empty[sc]);
         return true;
       };
       ok = fetch(base);
@@ -451,7 +449,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[it % NE]);
+        // The codes are given back only here, where what was made of them has
+        // been stored: an arrival can overtake loads that are still queued,
+        // and the next codes then come in under them.
+        if (lane == 0) {
+          mbar_arrive(&c_empty[it % NC]);
+          mbar_arrive(&full[it % NE]);
+        }
       }
       base = end;
     }

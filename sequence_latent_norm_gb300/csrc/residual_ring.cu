@@ -328,9 +328,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (v < nvec) load8(bx, v, x[i], T());
       }
     }
-    // the row buffer has been read by everyone: refill it
-    team_sync<TEAM>(ring.team);
-    if (tl == 0 && it + q.depth < n_it) ring.issue(q, stage, r + q.depth * G);
+    // The row buffer may be refilled once everyone has used what was read from
+    // it (a load can still be queued behind a barrier that its thread has
+    // passed): with a residual half x' has been stored by now, without one x
+    // is first used by the statistics below.
+    auto refill = [&] {
+      team_sync<TEAM>(ring.team);
+      if (tl == 0 && it + q.depth < n_it) ring.issue(q, stage, r + q.depth * G);
+    };
+    if (p.post) refill();
     if (p.pre) {
       float2 st = make_float2(0.f, 1.f);
       if (p.norm_pre == LAGA_NORM_LAYER) {
@@ -355,6 +361,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       float s[1] = {t.x + t.y};
       team_sum<TEAM, 1>(s, red, ring.team, slot);
       st.y = 1.f / sqrtf(s[0] * p.inv_d + p.eps);
+      if (!p.post) refill();
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = i * TEAM + tl;
@@ -536,6 +543,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
     }
+    // every value read from the row buffer has gone into a store by now
     team_sync<TEAM>(ring.team);
     if (tl == 0 && it + q.depth < n_it) ring.issue(q, stage, r + q.depth * G);
     if (++stage == q.depth) {

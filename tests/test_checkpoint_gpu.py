@@ -183,3 +183,40 @@ def test_refusals_on_the_gpu():
         ck.unpack(torch.float16)
     with pytest.raises(ValueError, match="shape"):
         laga.Checkpoint8(ck.data[:, :128].contiguous(), 64)
+
+
+@pytest.mark.parametrize("n", [512, 1536])
+def test_weight_grad_step_by_step_at_full_size(n):
+    """Several tiles for each pair of CTAs, as a 16384-token step has them.
+    Column j of dy picks the tokens of one 128-token step, whose values are a
+    number that tells neighbouring steps apart: every element is the exact
+    sum of its step, whichever tiles, chains and fragments it went through."""
+    laga = _laga()
+    T, d = 16384, 7168
+    step = torch.arange(T, device=DEV) // 128
+    ck = laga.pack8((1 + (step % 8) / 8.0)[:, None].expand(T, d).contiguous())
+    col = torch.arange(n, device=DEV)
+    dy = ((col % 128)[None, :] == step[:, None]).to(torch.bfloat16)
+    want = (128 * (1 + (col % 8) / 8.0)).expand(d, n)
+    for _ in range(3):
+        assert torch.equal(laga.weight_grad8(ck, dy), want)
+
+
+@pytest.mark.parametrize("rows,d,n,dtype", [(16384, 7168, 1536, "bf16"), (16384, 7168, 576, "fp32"),
+                                            (4096, 6000, 1000, "bf16"), (1000, 16384, 1026, "bf16"),
+                                            (9000, 5001, 1530, "fp32")])
+def test_weight_grad_at_full_size(rows, d, n, dtype):
+    """Against the product in 64 bits on the GPU, with the bound of the small
+    sizes; every run gives the same bits."""
+    laga = _laga()
+    g = torch.Generator(device=DEV).manual_seed(n)
+    ck = laga.pack8(torch.randn(rows, d, generator=g, device=DEV))
+    dy = torch.randn(rows, n, generator=g, device=DEV).to(DT[dtype])
+    gamma = 1 + 0.1 * torch.randn(d, generator=g, device=DEV)
+    got = laga.weight_grad8(ck, dy, gamma)
+    for _ in range(3):
+        assert torch.equal(got, laga.weight_grad8(ck, dy, gamma))
+    v = ck.unpack(torch.float32).double() * gamma.double()
+    ref, size = v.t() @ dy.double(), v.abs().t() @ dy.double().abs()
+    assert ((got.double() - ref).abs() <= (rows + 64) * 2.0 ** -23 * size).all()
+    _sync()
