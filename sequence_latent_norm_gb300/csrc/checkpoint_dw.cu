@@ -21,18 +21,20 @@
 //   12-19   epilogue: adds up the accumulators of a tile in registers, then
 //           multiplies by gamma and stores
 // A step is 128 tokens.  Every hand-over between warps costs a few hundred
-// clocks, whatever the step's size, and the issuer's wait, commit and MMAs of
-// a 64-token step took longer than the MMAs ran: with 64 tokens (NA = 6, NB =
-// 5) the kernel took 319 us for 16384 x 7168 x 1536, with 128 it takes 293.
-// A decoder turns 4 codes into bf16 with 9 integer and multiply instructions;
-// the pair's MMAs of a step take 2 BN clocks.
+// clocks, whatever the step's size: 16384 x 7168 x 1536 takes 309 us with steps
+// of 128 tokens and 377 us with 64 (the rings as deep in tokens).  What bounds
+// it is that chain of hand-overs (codes, decoded tile, MMAs, and back) over
+// the three v tiles that shared memory holds: without its decoding it takes
+// ~280 us, with one of eight MMAs ~260 us, and the MMAs alone would take 140
+// us.  With three pieces of dy per v tile the dy loads come on top.
+// A decoder turns 4 codes into bf16 with 9 integer and multiply instructions.
 //
 // The tensor core's fp32 accumulation drops what does not fit below the
 // accumulator's last place instead of rounding it: a chain of 1024 MMAs
 // (16384 tokens) came out 8.4e-6 of its value short, 50 times the error of
-// rounded fp32 sums.  So a chain is CHAIN steps at most (64 MMAs); the
-// epilogue warps add the chains in registers, rounding to nearest, while the
-// next one fills the other accumulator.
+// rounded fp32 sums.  So a chain is 64 MMAs at most, and the epilogue warps
+// add the chains in registers, rounding to nearest, while the next one fills
+// the other accumulator (1.7e-7).
 //
 // Work split: tile counts rarely fill the 76 pairs evenly, so whole rounds of
 // one tile per pair run first, and the token steps of the tiles that are left
@@ -57,7 +59,7 @@ using namespace sm100;
 
 constexpr int KT = 128;                      // tokens per step
 constexpr int NA = 3, NB = 2, NC = 3;        // ring stages: v tiles, dy tiles, codes
-constexpr int NE = 4;                        // step barriers (full, empty)
+constexpr int NE = 4;                        // barriers of the v tiles (a_full, a_empty)
 constexpr int BOX = KT * 64 * 2;             // KT tokens x 64 bf16
 constexpr int A_BYTES = 2 * BOX;             // KT tokens x 128 channels
 constexpr int B_BYTES = 2 * BOX;             // KT tokens x up to 128 columns
@@ -72,8 +74,8 @@ constexpr int DEC_WARPS = W_EPI - W_DEC;
 // A parity tells only neighbouring phases of a barrier apart, so a waiter has
 // to see every phase of the barriers that it waits on.  Everyone does but the
 // two relays, which take every other step.
-static_assert(NE % 2 == 0, "a step barrier belongs to one relay");
-static_assert(NE > NA && NE > NB, "a step's barrier outlives its tiles");
+static_assert(NE % 2 == 0, "a v tile's barrier belongs to one relay");
+static_assert(NE > NA, "a v tile's barrier outlives it");
 // Registers a thread: at launch (the most that THREADS threads can have, in
 // steps of 8), and after each warpgroup's setmaxnreg.
 constexpr int REG_LAUNCH = 65536 / THREADS / 8 * 8;
@@ -93,8 +95,9 @@ struct DwMaps {
 struct DwParams {
   int groups, cols, d, n;
   int n_tiles, tiles;
-  int pieces;              // bf16 pieces of dy
-  int steps;               // steps of a tile: step s is piece s % pieces of token step s / pieces
+  int pieces;              // bf16 pieces of dy, all multiplied with one v tile
+  int steps;               // steps of a tile
+  int chain;               // steps of one accumulation
   int rounds;              // whole rounds: one tile per pair each
   int chunk;               // steps of the left-over tiles that each pair takes
   int max_frags;           // fragments per pair
@@ -135,6 +138,13 @@ struct Walk {
     }
     ++i;
     return true;
+  }
+  // The j-th step of the piece.  Neighbouring pairs start up to seven steps
+  // apart and go round: the pairs that share a dy tile would otherwise all ask
+  // for the same lines at once (16384 x 7168 x 576 fp32: 368 us in step, 359 us
+  // apart).
+  LAGA_DEVINL int step(const DwParams& p, int j) const {
+    return k0 + (j + ((t / p.n_tiles) & 7)) % kn;
   }
 };
 
@@ -192,11 +202,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
-  // Each CTA's: c_full, c_empty (codes), empty, acc_full (the pair MMAs' commits
-  // arrive in both).  full: in rank 1 an arrival of every decoder warp; in rank
-  // 0 the same, the bytes of both CTAs' dy tiles, and an arrival that says
-  // that rank 1's is complete.  Rank 0's acc_empty: epilogue warps of both.
-  __shared__ uint64_t c_full[NC], c_empty[NC], full[NE], empty[NE], acc_full[2], acc_empty[2];
+  // Each CTA's: c_full, c_empty (codes), a_empty, b_empty, acc_full (the pair
+  // MMAs' commits arrive in both).  a_full: an arrival of every decoder warp,
+  // and in rank 0 one that says that rank 1's is complete.  Rank 0's: b_full
+  // (both CTAs' dy bytes), acc_empty (epilogue warps of both).
+  __shared__ uint64_t c_full[NC], c_empty[NC], a_full[NE], a_empty[NE], b_full[NB], b_empty[NB];
+  __shared__ uint64_t acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -209,8 +220,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&c_empty[i], DEC_WARPS);
     }
     for (int i = 0; i < NE; ++i) {
-      mbar_init(&full[i], rank == 0 ? DEC_WARPS + 2 : DEC_WARPS);
-      mbar_init(&empty[i], 1);
+      mbar_init(&a_full[i], rank == 0 ? DEC_WARPS + 1 : DEC_WARPS);
+      mbar_init(&a_empty[i], 1);
+    }
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(&b_full[i], 1);
+      mbar_init(&b_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -237,22 +252,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       bool ok = true;
       while (ok && w.next(p, pair)) {
         const int n0 = (w.t % p.n_tiles) * BN + (int)rank * HALF;
-        for (int k = w.k0; k < w.k0 + w.kn; ++k, ++it) {
-          // the stage's last tile was step it - NB's
-          if (it >= NB && !mbar_wait(&empty[(it - NB) % NE], ((it - NB) / NE) & 1, p.err)) {
-            ok = false;
-            break;
-          }
-          const int st = it % NE;
-          uint8_t* dst = sm + B_OFF + it % NB * B_BYTES;
-          const uint32_t bar = smem_cluster_addr(&full[st], 0);
-          constexpr int BOXES = (HALF + 63) / 64;
-          if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * BOXES * BOX);
+        for (int j = 0; ok && j < w.kn; ++j)
+          for (int s = 0; s < p.pieces; ++s, ++it) {
+            const int st = it % NB;
+            if (it >= NB && !mbar_wait(&b_empty[st], (it / NB - 1) & 1, p.err)) {
+              ok = false;
+              break;
+            }
+            uint8_t* dst = sm + B_OFF + st * B_BYTES;
+            const uint32_t bar = smem_cluster_addr(&b_full[st], 0);
+            constexpr int BOXES = (HALF + 63) / 64;
+            if (rank == 0) mbar_arrive_expect_tx(&b_full[st], 2 * BOXES * BOX);
 #pragma unroll
-          for (int b = 0; b < BOXES; ++b)
-            tma_load_3d_pair(dst + b * BOX, &tm.dy, bar, n0 + b * 64, k / p.pieces * KT,
-                             k % p.pieces);
-        }
+            for (int b = 0; b < BOXES; ++b)
+              tma_load_3d_pair(dst + b * BOX, &tm.dy, bar, n0 + b * 64, w.step(p, j) * KT, s);
+          }
       }
     }
   } else if (warp == 1) {
@@ -263,7 +277,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       bool ok = true;
       while (ok && w.next(p, pair)) {
         const int g = (w.t / p.n_tiles) * 2 + (int)rank;
-        for (int k = w.k0; k < w.k0 + w.kn; ++k, ++it) {
+        for (int j = 0; j < w.kn; ++j, ++it) {
+          const int t0 = w.step(p, j) * KT;
           const int st = it % NC;
           if (it >= NC && !mbar_wait(&c_empty[st], (it / NC - 1) & 1, p.err)) {
             ok = false;
@@ -271,20 +286,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           uint8_t* dst = sm + C_OFF + st * C_BYTES;
           mbar_arrive_expect_tx(&c_full[st], C_BYTES);
-          tma_load_2d(dst, &tm.codes, &c_full[st], g * CK_GROUP, k / p.pieces * KT);
-          tma_load_2d(dst + CODE_BYTES, &tm.scales, &c_full[st], p.cols + (g & ~15),
-                      k / p.pieces * KT);
+          tma_load_2d(dst, &tm.codes, &c_full[st], g * CK_GROUP, t0);
+          tma_load_2d(dst + CODE_BYTES, &tm.scales, &c_full[st], p.cols + (g & ~15), t0);
         }
       }
     }
   } else if (warp == 2 && rank == 0) {
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16(256, BN, 1, 1);
-      uint32_t it = 0, ic = 0;   // steps, chains
-      bool ready = false;        // step it's stage has been seen full
+      uint32_t ia = 0, ib = 0, ic = 0;   // v tiles, dy tiles, chains
+      bool a_ready = false, b_ready = false;   // the next ones have been seen full
       bool ok = true;
       while (ok && w.next(p, pair)) {
-        for (int k0 = 0; ok && k0 < w.kn; k0 += CHAIN, ++ic) {
+        for (int k0 = 0; ok && k0 < w.kn; k0 += p.chain, ++ic) {
           const int buf = ic & 1;
           if (ic >= 2 && !mbar_wait_cluster(&acc_empty[buf], ((ic >> 1) - 1) & 1, p.err)) {
             ok = false;
@@ -292,25 +306,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           tc_fence_after();
           const uint32_t dst = tmem + (uint32_t)(buf * ACC_COLS);
-          const int k1 = min(k0 + CHAIN, w.kn);
-          for (int k = k0; k < k1; ++k, ++it) {
-            const int st = it % NE;
-            if (!ready && !mbar_wait(&full[st], (it / NE) & 1, p.err)) {
+          const int k1 = min(k0 + p.chain, w.kn);
+          for (int k = k0; ok && k < k1; ++k, ++ia) {
+            if (!a_ready && !mbar_wait(&a_full[ia % NE], (ia / NE) & 1, p.err)) {
               ok = false;
               break;
             }
-            tc_fence_after();
-            // ask for the next stage now: the answer arrives while this one's
-            // MMAs are issued
-            ready = mbar_test(&full[(it + 1) % NE], ((it + 1) / NE) & 1);
-            const uint32_t alo = sdesc_lo(smem_u32(sm + it % NA * A_BYTES), BOX);
-            const uint32_t blo = sdesc_lo(smem_u32(sm + B_OFF + it % NB * B_BYTES), BOX);
+            const uint32_t alo = sdesc_lo(smem_u32(sm + ia % NA * A_BYTES), BOX);
+            for (int s = 0; s < p.pieces; ++s, ++ib) {
+              const int st = ib % NB;
+              if (!b_ready && !mbar_wait(&b_full[st], (ib / NB) & 1, p.err)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              // ask for the next tiles now: the answers arrive while these
+              // MMAs are issued
+              b_ready = mbar_test(&b_full[(ib + 1) % NB], ((ib + 1) / NB) & 1);
+              a_ready = mbar_test(&a_full[(ia + 1) % NE], ((ia + 1) / NE) & 1);
+              const uint32_t blo = sdesc_lo(smem_u32(sm + B_OFF + st * B_BYTES), BOX);
 #pragma unroll
-            for (int kk = 0; kk < KT / 16; ++kk)
-              mma_ss_pair(dst, sdesc_make(alo + kk * (2048 >> 4)),
-                          sdesc_make(blo + kk * (2048 >> 4)), idesc,
-                          (k > k0 || kk > 0) ? 1u : 0u);
-            mma_commit_pair(&empty[st]);
+              for (int kk = 0; kk < KT / 16; ++kk)
+                mma_ss_pair(dst, sdesc_make(alo + kk * (2048 >> 4)),
+                            sdesc_make(blo + kk * (2048 >> 4)), idesc,
+                            (k > k0 || s > 0 || kk > 0) ? 1u : 0u);
+              mma_commit_pair(&b_empty[st]);
+            }
+            mma_commit_pair(&a_empty[ia % NE]);
           }
           mma_commit_pair(&acc_full[buf]);
         }
@@ -324,8 +346,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (lane == 0 && rank == 1) {
       const uint32_t total = (uint32_t)(p.rounds * p.steps + w.left);
       for (uint32_t it = warp & 1; it < total; it += 2) {
-        if (!mbar_wait(&full[it % NE], (it / NE) & 1, p.err)) break;
-        mbar_arrive_cluster(smem_cluster_addr(&full[it % NE], 0));
+        if (!mbar_wait(&a_full[it % NE], (it / NE) & 1, p.err)) break;
+        mbar_arrive_cluster(smem_cluster_addr(&a_full[it % NE], 0));
       }
     }
   } else if (warp >= W_EPI) {
@@ -338,7 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       float2 acc[HALF / 2];
 #pragma unroll
       for (int j = 0; j < HALF / 2; ++j) acc[j] = make_float2(0.f, 0.f);
-      for (int k0 = 0; k0 < w.kn; k0 += CHAIN, ++ic) {
+      for (int k0 = 0; k0 < w.kn; k0 += p.chain, ++ic) {
         const int buf = ic & 1;
         if (!mbar_wait(&acc_full[buf], (ic >> 1) & 1, p.err)) {
           ok = false;
@@ -434,7 +456,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           ok = false;
           break;
         }
-        if (it >= NA && !mbar_wait(&empty[(it - NA) % NE], ((it - NA) / NE) & 1, p.err)) {
+        if (it >= NA && !mbar_wait(&a_empty[(it - NA) % NE], ((it - NA) / NE) & 1, p.err)) {
           ok = false;
           break;
         }
@@ -454,7 +476,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // and the next codes then come in under them.
         if (lane == 0) {
           mbar_arrive(&c_empty[it % NC]);
-          mbar_arrive(&full[it % NE]);
+          mbar_arrive(&a_full[it % NE]);
         }
       }
       base = end;
@@ -562,8 +584,10 @@ size_t up1k(size_t x) { return (x + 1023) / 1024 * 1024; }
 
 DwPlan dw_plan(int rows, int d, int n, bool fp32) {
   DwPlan pl;
-  // Columns per tile: a step costs 2 BN clocks of MMA time, and no less than
-  // the decoders' ~256; ties go to the wider tile.
+  // Columns per tile: a step costs MMA time in proportion to BN, and no less
+  // than a tile of 128 columns, which the decoders set the pace of; ties go to
+  // the wider tile (1536 columns: 309 us in tiles of 256, 374 us of 192; 576
+  // columns fit three tiles of 192).
   long long best = -1;
   for (const int bn : {256, 192, 128}) {
     const long long cost = (long long)((n + bn - 1) / bn) * std::max(2 * bn, 256);
@@ -582,13 +606,14 @@ DwPlan dw_plan(int rows, int d, int n, bool fp32) {
   p.groups = p.cols / CK_GROUP;
   p.n_tiles = (n + pl.bn - 1) / pl.bn;
   p.tiles = (p.groups + 1) / 2 * p.n_tiles;
-  p.steps = (rows + KT - 1) / KT * pl.pieces;
+  p.steps = (rows + KT - 1) / KT;
+  p.chain = std::max(1, CHAIN / pl.pieces);
   p.pieces = pl.pieces;
   p.rounds = p.tiles / PAIRS;
   const long long left = (long long)(p.tiles - p.rounds * PAIRS) * p.steps;
   const long long chunk =
       std::max<long long>((left + PAIRS - 1) / PAIRS, std::min(p.steps, MIN_STEPS));
-  pl.fits = chunk <= INT_MAX - p.steps;
+  pl.fits = (long long)p.rounds * p.steps + chunk + p.steps <= INT_MAX;
   if (!pl.fits) return pl;
   p.chunk = (int)chunk;
   p.max_frags = p.steps ? (int)((p.chunk + p.steps - 2) / p.steps) + 1 : 0;
