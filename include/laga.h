@@ -253,8 +253,9 @@ laga_status laga_diag_mma_rate(int form, int n, int n_acc, int run, int n_instr,
 /* Static text for a status code. */
 const char* laga_status_string(laga_status status);
 
-/* Number of kernel launches the last laga_fwd / laga_bwd call on this host
- * thread enqueued (0 after an error).  For launch accounting. */
+/* Number of kernel launches the last laga_fwd, laga_bwd, laga_res_* or
+ * laga_ckpt_* call on this host thread enqueued (0 after an error).  For
+ * launch accounting. */
 int laga_last_launch_count(void);
 
 /* LayerNorm + RoPE backward (the backward of steps a1-a2 alone) for callers

@@ -62,7 +62,7 @@ def _f64(t):
 def _close(got, ref, bound, what):
     got = as_f64(got).reshape(ref.shape)
     off = np.abs(got - ref)
-    worst = float((off / bound).max()) if off.size else 0.0
+    worst = float((off / np.maximum(bound, 1e-300)).max()) if off.size else 0.0
     assert np.isfinite(got).all() and (off <= bound).all(), f"{what}: {worst:.2f} of its bound"
 
 
@@ -218,6 +218,14 @@ def test_every_option(post, pre, norm_post, norm_pre, gate, d):
 def test_many_rows(rows, d):
     """More rows than a launch has places, so that every place walks several."""
     _check(rows, d, "bf16", True, True, "rms", "layer", "full", True)
+
+
+@pytest.mark.parametrize("rows,d,ckpt", [(400, 7168, False), (320, 16384, False), (320, 16384, True),
+                                         (1500, 4096, False), (2600, 1024, False)])
+def test_many_rows_of_fp32(rows, d, ckpt):
+    """fp32 rows: rings of one and two rows, and teams with several rows each."""
+    _check(rows, d, "fp32", True, True, "layer", "rms", "full", ckpt)
+    _check(rows, d, "fp32", False, True, "none", "layer", "none", ckpt)
 
 
 @pytest.mark.parametrize("d", [512, 333])

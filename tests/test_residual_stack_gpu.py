@@ -294,6 +294,35 @@ def test_weight_grad_many_times_over_ragged_sizes():
     laga._lib.sync_check()
 
 
+def test_more_than_two_to_the_31_elements():
+    """Rows behind the 2^31st element are as in a call of their own."""
+    laga = _laga()
+    rows, d, last = 301000, 7168, 160
+    g = torch.Generator(device=DEV).manual_seed(8)
+    tail = torch.randn(last, d, generator=g, device=DEV).to(torch.bfloat16)
+    x = torch.ones(rows, d, dtype=torch.bfloat16, device=DEV)
+    x[-last:] = tail
+    gamma = torch.rand(d, generator=g, device=DEV)
+    plan = laga.ResidualNorm(d, post=False, norm_pre="layer", ckpt=True, device=DEV)
+    big, small = plan.forward(x, gamma_pre=gamma), plan.forward(tail, gamma_pre=gamma)
+    assert torch.equal(big.h[-last:], small.h)
+    assert torch.equal(big.saved.x.data[-last:], small.saved.x.data)
+    gb, gs = plan.backward(big.saved, None, x), plan.backward(small.saved, None, tail)
+    assert torch.equal(gb.dx[-last:], gs.dx)
+    del gb, big
+    ck = laga.pack8(x)
+    assert torch.equal(ck.data[-last:], laga.pack8(tail).data)
+    assert torch.equal(ck.unpack()[-last:], laga.pack8(tail).unpack())
+    del x
+    dy = torch.zeros(rows, 16, dtype=torch.bfloat16, device=DEV)
+    dy[-last:] = tail[:, :16]
+    v = laga.pack8(tail).unpack(torch.float32).double()
+    ref, size = v.t() @ tail[:, :16].double(), v.abs().t() @ tail[:, :16].double().abs()
+    got = laga.weight_grad8(ck, dy)
+    assert ((got.double() - ref).abs() <= (last + 64) * 2.0 ** -23 * size).all()
+    laga._lib.sync_check()
+
+
 BAND, FILL = 4096, 0xA5
 
 
