@@ -10,10 +10,13 @@ namespace laga {
 namespace {
 
 // Widths of a multiple of 8, where rows start on 16 bytes: a thread takes 8
-// channels, 16 neighbouring threads a group, a block ROWS rows at a time; UNROLL
-// vectors' loads are issued before any is worked on, which is what hides the
-// HBM latency (both kernels move 3 bytes per bf16 element and do little else).
-constexpr int ROWS = 8, UNROLL = 4;
+// channels, 16 neighbouring threads a group, a block ROWS rows at a time, and
+// issues UNROLL vectors' loads before it works on any.  Both kernels move 3
+// bytes per bf16 element.  Unpacking does little else (16384 x 7168: 62 us with
+// 4, 72 us with 1; 0.84 of the HBM rate); packing, with the group's maximum
+// and the conversions, gains more from the warps that fewer registers allow
+// (80 us with 1, 88 us with 2, 102 us with 4).
+constexpr int ROWS = 8, PACK_UNROLL = 1, UNPACK_UNROLL = 4;
 
 LAGA_DEVINL void load8(const float* p, float2 (&f)[4]) {
   const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
@@ -50,10 +53,10 @@ __global__ void __launch_bounds__(256) ckpt_pack8_kernel(const T* __restrict__ x
   for (long long r0 = (long long)blockIdx.x * ROWS; r0 < rows; r0 += (long long)gridDim.x * ROWS) {
     const int n = (int)min((long long)ROWS, rows - r0) * vpr;
     // whole warps go round, so that every lane of a group is there
-    for (int i0 = threadIdx.x & ~31; i0 < n; i0 += 256 * UNROLL) {
-      float2 f[UNROLL][4];
+    for (int i0 = threadIdx.x & ~31; i0 < n; i0 += 256 * PACK_UNROLL) {
+      float2 f[PACK_UNROLL][4];
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
+      for (int u = 0; u < PACK_UNROLL; ++u) {
         const int i = i0 + u * 256 + (threadIdx.x & 31);
         const int r = i / vpr, v = i - r * vpr;
 #pragma unroll
@@ -61,7 +64,7 @@ __global__ void __launch_bounds__(256) ckpt_pack8_kernel(const T* __restrict__ x
         if (i < n && v * 8 < d) load8(x + (r0 + r) * d + v * 8, f[u]);
       }
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
+      for (int u = 0; u < PACK_UNROLL; ++u) {
         const int i = i0 + u * 256 + (threadIdx.x & 31);
         const int r = i / vpr, v = i - r * vpr;
         float m = 0.f;
@@ -89,11 +92,11 @@ __global__ void __launch_bounds__(256) ckpt_unpack8_kernel(const uint8_t* __rest
   const int cols = ck_cols(d), vpr = d / 8, pitch = ck_pitch(d);
   for (long long r0 = (long long)blockIdx.x * ROWS; r0 < rows; r0 += (long long)gridDim.x * ROWS) {
     const int n = (int)min((long long)ROWS, rows - r0) * vpr;
-    for (int i0 = threadIdx.x; i0 < n; i0 += 256 * UNROLL) {
-      uint2 q[UNROLL];
-      uint32_t s[UNROLL];
+    for (int i0 = threadIdx.x; i0 < n; i0 += 256 * UNPACK_UNROLL) {
+      uint2 q[UNPACK_UNROLL];
+      uint32_t s[UNPACK_UNROLL];
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
+      for (int u = 0; u < UNPACK_UNROLL; ++u) {
         const int i = i0 + u * 256, r = i / vpr, v = i - r * vpr;
         if (i < n) {
           const uint8_t* row = ck + (r0 + r) * pitch;
@@ -102,7 +105,7 @@ __global__ void __launch_bounds__(256) ckpt_unpack8_kernel(const uint8_t* __rest
         }
       }
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
+      for (int u = 0; u < UNPACK_UNROLL; ++u) {
         const int i = i0 + u * 256, r = i / vpr, v = i - r * vpr;
         if (i >= n) continue;
         const float unit = ck_unit(s[u]);

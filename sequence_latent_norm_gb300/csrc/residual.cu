@@ -213,36 +213,57 @@ __global__ void __launch_bounds__(GT, 2048 / GT) res_bwd_rows_kernel(const ResAr
   if (p.post && threadIdx.x == 0) p.part_alpha[blockIdx.x] = d_alpha;
 }
 
-// Sums of the column partials over their slots, in slot order within each of
-// 16 interleaved chains and then over the chains: blockIdx.y 0 gamma_post, 1
-// gamma_pre; block (0, 2) alpha.
-__global__ void __launch_bounds__(512) res_colsum_kernel(const float* part_post, const float* part_pre,
-                                                         const float* part_alpha, int slots, int d,
-                                                         float* dg_post, float* dg_pre,
-                                                         float* dalpha) {
-  __shared__ float sm[16][33];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+// Sums of the column partials over their slots, CW columns a block: 1024 / CW
+// chains of every so many'th slot, four loads at a time, added up in order.  32
+// columns, or, up to 1024 channels, 8 (one 32-byte sector of a slot), so that
+// there are blocks enough: 512 channels 8 us with 8 and 15 us with 32 columns,
+// 7168 channels 15 us and 9 us.  blockIdx.y 0: gamma_post, 1: gamma_pre; block
+// (0, 2): alpha.
+template <int CW>
+__global__ void __launch_bounds__(1024) res_colsum_kernel(const float* part_post, const float* part_pre,
+                                                          const float* part_alpha, int slots, int d,
+                                                          float* dg_post, float* dg_pre,
+                                                          float* dalpha) {
+  constexpr int NG = 1024 / CW;
+  __shared__ float sm[NG][CW + 1], sm2[8][CW + 1];
+  const int tid = threadIdx.x, col = tid % CW, g = tid / CW;
   if (blockIdx.y == 2) {
-    if (blockIdx.x || w || !dalpha) return;
+    if (blockIdx.x || tid >= 32 || !dalpha) return;
     float s = 0.f;
-    for (int k = lane; k < slots; k += 32) s += part_alpha[k];
+    for (int k = tid; k < slots; k += 32) s += part_alpha[k];
     s = warp_sum(s);
-    if (lane == 0) *dalpha = s;
+    if (tid == 0) *dalpha = s;
     return;
   }
   const float* part = blockIdx.y ? part_pre : part_post;
   float* out = blockIdx.y ? dg_pre : dg_post;
   if (!out) return;
-  const int c = blockIdx.x * 32 + lane;
+  const int c = blockIdx.x * CW + col;
   float s = 0.f;
   if (c < d)
-    for (int k = w; k < slots; k += 16) s += part[(long long)k * d + c];
-  sm[w][lane] = s;
+    for (int k0 = g; k0 < slots; k0 += NG * 4) {
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = k0 + NG * i;
+        v[i] = k < slots ? part[(long long)k * d + c] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s += v[i];
+    }
+  sm[g][col] = s;
   __syncthreads();
-  if (w == 0 && c < d) {
+  if (g < 8) {
     s = 0.f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) s += sm[k][lane];
+    for (int i = 0; i < NG / 8; ++i) s += sm[g * (NG / 8) + i][col];
+    sm2[g][col] = s;
+  }
+  __syncthreads();
+  if (g == 0 && c < d) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += sm2[i][col];
     out[c] = s;
   }
 }
@@ -344,7 +365,9 @@ cudaError_t launch_res_bwd(const laga_res_dims& d, const ResPtrs& x, cudaStream_
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   LaunchScope ls_("res_colsum", st);
-  res_colsum_kernel<<<dim3((d.d + 31) / 32, 3), 512, 0, st>>>(
+  const int cw = d.d <= 1024 ? 8 : 32;
+  const auto k = cw == 8 ? res_colsum_kernel<8> : res_colsum_kernel<32>;
+  k<<<dim3((d.d + cw - 1) / cw, 3), 1024, 0, st>>>(
       a.part_post, a.part_pre, a.part_alpha, slots, d.d,
       d.post && d.norm_post != LAGA_NORM_NONE ? x.dgamma_post : nullptr,
       d.pre ? x.dgamma_pre : nullptr, d.post ? x.dalpha : nullptr);

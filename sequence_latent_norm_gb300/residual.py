@@ -62,7 +62,7 @@ class ResidualNorm:
     norm_pre "layer" or "rms"; gate "none", "token" (logits [..., 1]) or
     "full" (logits [..., d]); io_dtype "bf16" or "fp32" of x, y, gate, h and
     their gradients.  Gains and alpha ([1]) are fp32.  A call takes any number
-    of rows and keeps nothing in the object."""
+    of rows and keeps none of its data in the object."""
 
     def __init__(self, d: int, *, post: bool = True, pre: bool = True, norm_post: str = "rms",
                  norm_pre: str = "rms", gate: str = "none", ckpt: bool = False,
@@ -87,9 +87,16 @@ class ResidualNorm:
         self.device = torch.device(device)
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        self._last = None
 
     def _c_dims(self, rows):
-        return _lib.make_res_dims(rows, self.d, **self._dims)
+        """The C dims for so many rows and their backward's scratch bytes; the
+        last ones are kept (and never changed), since calls mostly repeat."""
+        last = self._last
+        if last is None or last[0] != rows:
+            dims = _lib.make_res_dims(rows, self.d, **self._dims)
+            last = self._last = (rows, dims, _lib.res_workspace_bytes(dims))
+        return last[1], last[2]
 
     @staticmethod
     def _shape(t, name):
@@ -128,7 +135,7 @@ class ResidualNorm:
             ck_x = empty_checkpoint(full, dev) if self.ckpt and self.pre else None
             s_post = torch.empty(rows, 2, dtype=torch.float32, device=dev) if self.post else None
             s_pre = torch.empty(rows, 2, dtype=torch.float32, device=dev) if self.pre else None
-            _lib.res_fwd(self._c_dims(rows), px, py, *params,
+            _lib.res_fwd(self._c_dims(rows)[0], px, py, *params,
                          x_out.data_ptr() if self.post else 0, h.data_ptr() if self.pre else 0,
                          ck_y.data.data_ptr() if ck_y else 0, ck_x.data.data_ptr() if ck_x else 0,
                          s_post.data_ptr() if self.post else 0,
@@ -163,7 +170,7 @@ class ResidualNorm:
         s_pre = self._f32(saved.stat_pre, "saved.stat_pre", (rows, 2)) if self.pre else 0
         gate, alpha, g_post, g_pre = self._params(full, saved.gate, saved.alpha, saved.gamma_post,
                                                   saved.gamma_pre)
-        dev, dims = self.device, self._c_dims(rows)
+        dev, (dims, nb) = self.device, self._c_dims(rows)
         with on_stream(dev, stream) as st:
             def f32(on, n):
                 return torch.empty(n, dtype=torch.float32, device=dev) if on else None
@@ -173,7 +180,6 @@ class ResidualNorm:
             dgate = torch.empty_like(saved.gate) if self.gate != "none" else None
             dalpha, dg_post = f32(self.post, 1), f32(self.gain, self.d)
             dg_pre = f32(self.pre, self.d)
-            nb = _lib.res_workspace_bytes(dims)
             ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
 
             def ptr(t):
