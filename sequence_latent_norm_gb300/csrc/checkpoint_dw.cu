@@ -38,8 +38,7 @@
 //
 // Work split: tile counts rarely fill the 76 pairs evenly, so whole rounds of
 // one tile per pair run first, and the token steps of the tiles that are left
-// are dealt out evenly over all pairs, at least MIN_STEPS in a row each.  A
-// pair's part of such a tile is a fragment in the workspace; dw_join adds a
+// are dealt out evenly over all pairs.  A pair's part of such a tile is a fragment in the workspace; dw_join adds a
 // tile's fragments in token order.  Which pair takes what depends on the
 // sizes alone, so every run adds in the same order.
 #include <limits.h>
@@ -87,7 +86,6 @@ static_assert(W_DEC * REG_MISC + (W_EPI - W_DEC) * REG_DEC + (THREADS / 32 - W_E
 constexpr int CHAIN = 8;
 constexpr int TMEM_COLS = 512, ACC_COLS = 256;
 constexpr int PAIRS = 76;                    // one pair per two SMs
-constexpr int MIN_STEPS = 4;
 
 struct DwMaps {
   CUtensorMap codes, scales, dy;
@@ -611,8 +609,8 @@ DwPlan dw_plan(int rows, int d, int n, bool fp32) {
   p.pieces = pl.pieces;
   p.rounds = p.tiles / PAIRS;
   const long long left = (long long)(p.tiles - p.rounds * PAIRS) * p.steps;
-  const long long chunk =
-      std::max<long long>((left + PAIRS - 1) / PAIRS, std::min(p.steps, MIN_STEPS));
+  // (at least four steps a pair made small products 5 to 10 % slower)
+  const long long chunk = std::max<long long>((left + PAIRS - 1) / PAIRS, 1);
   pl.fits = (long long)p.rounds * p.steps + chunk + p.steps <= INT_MAX;
   if (!pl.fits) return pl;
   p.chunk = (int)chunk;

@@ -109,14 +109,44 @@ LAGA_DEVINL void team_sync(int team) {
 
 // Sum K values over a team.  Two alternating slots of partial sums: a slot is
 // written again two reductions later, behind the barrier in between.
+//
+// Plain form: every lane sums every value, then reads all the warps' sums
+// (broadcasts, independent of one another).  Shared form, for the 16 warps of
+// the largest team and several values: the lanes of a warp share the values
+// out first (lane l ends up with value l mod K) and then the warps' sums, ~30
+// instructions instead of ~120 for four values, in a longer chain.  The
+// 7168-channel backward takes 378 us with it and 410 us without; at 4096
+// channels (8 warps) it takes 61 us with it and 58 us without.
 template <int TEAM, int K>
 LAGA_DEVINL void team_sum(float (&v)[K], float (*red)[THREADS / 32][4], int team, int& slot) {
+  constexpr uint32_t ALL = 0xffffffffu;
+  constexpr int NW = TEAM / 32;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if constexpr (NW >= 16 && (K == 2 || K == 4)) {
+    const bool odd = lane & 1, two = lane & 2;
+    float x = (odd ? v[1] : v[0]) + __shfl_xor_sync(ALL, odd ? v[0] : v[1], 1);
+    if constexpr (K == 4) {
+      const float y = (odd ? v[3] : v[2]) + __shfl_xor_sync(ALL, odd ? v[2] : v[3], 1);
+      x = (two ? y : x) + __shfl_xor_sync(ALL, two ? x : y, 2);
+    }
+#pragma unroll
+    for (int o = K; o < 32; o <<= 1) x += __shfl_xor_sync(ALL, x, o);
+    if (lane < K) red[slot][w][lane] = x;
+    team_sync<TEAM>(team);
+    x = 0.f;
+#pragma unroll
+    for (int i = 0; i < NW; i += 32 / K) x += red[slot][team * NW + i + lane / K][lane % K];
+#pragma unroll
+    for (int o = K; o < 32; o <<= 1) x += __shfl_xor_sync(ALL, x, o);
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = __shfl_sync(ALL, x, k);
+    slot ^= 1;
+    return;
+  }
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
   if (TEAM == 32) return;
-  constexpr int NW = TEAM / 32;
-  const int w = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) == 0)
+  if (lane == 0)
 #pragma unroll
     for (int k = 0; k < K; ++k) red[slot][w][k] = v[k];
   team_sync<TEAM>(team);
