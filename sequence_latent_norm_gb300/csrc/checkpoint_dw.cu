@@ -34,7 +34,10 @@
 // (16384 tokens) came out 8.4e-6 of its value short, 50 times the error of
 // rounded fp32 sums.  So a chain is 64 MMAs at most, and the epilogue warps
 // add the chains in registers, rounding to nearest, while the next one fills
-// the other accumulator (1.7e-7).
+// the other accumulator (1.7e-7).  The products of an fp32 dy's pieces have
+// more bits to lose: their chain is two steps, and the smallest piece comes
+// first in each, while the accumulator is small (4.5e-7, largest piece first
+// 1.1e-6, one step a chain 1.2e-7 at 9 % more time; 16384 tokens).
 //
 // Work split: tile counts rarely fill the 76 pairs evenly, so whole rounds of
 // one tile per pair run first, and the token steps of the tiles that are left
@@ -83,7 +86,7 @@ static_assert(W_DEC % 4 == 0 && W_EPI % 4 == 0 && THREADS % 128 == 0, "whole war
 static_assert(W_DEC * REG_MISC + (W_EPI - W_DEC) * REG_DEC + (THREADS / 32 - W_EPI) * REG_EPI <=
                   THREADS / 32 * REG_LAUNCH,
               "the epilogue's warps grow on what the others give back");
-constexpr int CHAIN = 8;
+constexpr int CHAIN = 8, CHAIN_PIECES = 2;   // steps of one accumulation, bf16 and fp32 dy
 constexpr int TMEM_COLS = 512, ACC_COLS = 256;
 constexpr int PAIRS = 76;                    // one pair per two SMs
 
@@ -263,7 +266,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (rank == 0) mbar_arrive_expect_tx(&b_full[st], 2 * BOXES * BOX);
 #pragma unroll
             for (int b = 0; b < BOXES; ++b)
-              tma_load_3d_pair(dst + b * BOX, &tm.dy, bar, n0 + b * 64, w.step(p, j) * KT, s);
+              tma_load_3d_pair(dst + b * BOX, &tm.dy, bar, n0 + b * 64, w.step(p, j) * KT,
+                               p.pieces - 1 - s);
           }
       }
     }
@@ -605,7 +609,7 @@ DwPlan dw_plan(int rows, int d, int n, bool fp32) {
   p.n_tiles = (n + pl.bn - 1) / pl.bn;
   p.tiles = (p.groups + 1) / 2 * p.n_tiles;
   p.steps = (rows + KT - 1) / KT;
-  p.chain = std::max(1, CHAIN / pl.pieces);
+  p.chain = fp32 ? CHAIN_PIECES : CHAIN;
   p.pieces = pl.pieces;
   p.rounds = p.tiles / PAIRS;
   const long long left = (long long)(p.tiles - p.rounds * PAIRS) * p.steps;

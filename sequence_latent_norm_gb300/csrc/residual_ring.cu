@@ -456,8 +456,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     float m0 = 0.f, m1 = 0.f;
     // Teams up to 256 threads keep x^ and y^ from one pass over the row to the
     // next (16384 x 2048 from checkpoints: 97 us, 102 us decoding in every
-    // pass); for the one large team of a CTA the registers do not reach
-    // (16384 x 7168: 410 us decoding again, 498 us keeping them).
+    // pass); for the one large team of a CTA the registers do not reach, and
+    // keeping them took a fifth longer than decoding again (378 us at 16384 x
+    // 7168).
     constexpr bool KEEP = TEAM < 512;
     V8 hat[KEEP ? NV : 1];
     if (p.pre) {
