@@ -97,13 +97,21 @@ class LagaAttentionBlock:
         d_model] in h's dtype.  ``kept``, a Checkpoint8 with h = kept *
         kept_gain (fp32 [d_model] or None), is held instead of h."""
         B, S_r, d_model = h.shape
+        if kept is None:
+            if kept_gain is not None:
+                raise ValueError("kept_gain without kept: h is held as given")
+        elif not isinstance(kept, Checkpoint8):
+            raise TypeError("kept must be a Checkpoint8")
+        elif (kept.rows, kept.d) != (B * S_r, d_model):
+            raise ValueError(f"kept: a checkpoint of {kept.rows} rows of {kept.d}, expected "
+                             f"{B * S_r} of {d_model}")
         h_flat = h.reshape(B * S_r, d_model)
         q = (h_flat @ w_q).reshape(B, S_r, self.n_h, -1)
         c = (h_flat @ w_kva).reshape(B, S_r, -1)
         out, _ = self.attn.forward(q, c, w_kvb, gamma, cos, sin)
         out_flat = out.reshape(B * S_r, -1)
         if kept is None and self.checkpoint == "fp8":
-            kept = pack8(h_flat)
+            kept = pack8(h_flat.contiguous())
         elif kept is None:
             kept = h_flat
         self._saved = (kept, kept_gain, w_q, w_kva, w_o, out_flat, out.shape, h.shape)

@@ -85,6 +85,8 @@ class ResidualNorm:
         if not (0.0 < eps < math.inf):
             raise ValueError(f"eps={eps}: positive and finite")
         self.device = torch.device(device)
+        if self.device.type != "cuda":
+            raise ValueError(f"device {self.device}: a CUDA device")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self._last = None

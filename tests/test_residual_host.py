@@ -135,6 +135,8 @@ def test_python_refusals(lib):
     for d in (0, 16385):
         with pytest.raises(ValueError):
             laga.ResidualNorm(d, device="cuda:0")
+    with pytest.raises(ValueError, match="CUDA device"):
+        laga.ResidualNorm(64, device="cpu")
     op = laga.ResidualNorm(64, device="cuda:0")
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="expected cuda:0"):
@@ -155,3 +157,19 @@ def test_python_refusals(lib):
         laga.Checkpoint8(torch.zeros(4, 143, dtype=torch.uint8), 64)
     with pytest.raises(ValueError):
         laga.Checkpoint8(torch.zeros(4, 144, dtype=torch.uint8), 0)
+
+
+def test_block_refuses_a_kept_that_is_not_h():
+    import sequence_latent_norm_gb300 as laga
+    from sequence_latent_norm_gb300.block import LagaAttentionBlock
+    h = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    b = LagaAttentionBlock(None, 2)
+    with pytest.raises(ValueError, match="kept_gain"):
+        b.forward(h, *[None] * 7, kept_gain=torch.ones(64))
+    with pytest.raises(TypeError, match="Checkpoint8"):
+        b.forward(h, *[None] * 7, kept=h)
+    for rows, d in ((3, 64), (4, 128)):
+        ck = laga.Checkpoint8.__new__(laga.Checkpoint8)
+        ck.data, ck.d, ck.shape = torch.zeros(rows, 144, dtype=torch.uint8), d, (rows, d)
+        with pytest.raises(ValueError, match="expected 4 of 64"):
+            b.forward(h, *[None] * 7, kept=ck)

@@ -169,6 +169,12 @@ def test_block_with_an_8_bit_checkpoint():
     laga._lib.sync_check()
     assert isinstance(runs["fp8"][2], laga.Checkpoint8)
     assert torch.equal(runs["none"][0], runs["fp8"][0])
+    # an h with strides of its own is packed as what it holds
+    wide = torch.zeros(*t["h"].shape[:-1], 2 * t["h"].shape[-1], dtype=t["h"].dtype, device=DEV)
+    wide[..., ::2] = t["h"]
+    b = LagaAttentionBlock.single(wl.H, wl.S, device=torch.device(DEV), checkpoint="fp8")
+    b.forward(wide[..., ::2], *args)
+    assert torch.equal(b._saved[0].data, runs["fp8"][2].data)
     for k, v in runs["none"][1].items():
         w = runs["fp8"][1][k]
         if k in ("dw_q", "dw_kva"):
