@@ -14,6 +14,10 @@
 // beside the rings and a team has more than one row.  Column sums (the gains'
 // gradients) stay in registers over all of a team's rows and are written once,
 // as one partial row per team; residual.cu adds those up.
+//
+// A thread whose wait for a row gave up (the error word then says so) goes
+// through the rest of its rows without waiting, so that it still meets its team
+// at every barrier.
 #include <algorithm>
 
 #include "residual.cuh"
@@ -266,11 +270,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   const float alpha = p.post ? *p.x.alpha : 0.f;
   int slot = 0, stage = 0;
   uint32_t phase = 0;
+  bool ok = true;
   for (int it = 0; it < n_it; ++it) {
     const long long r = first + it * G;
     float tok = 0.f;
     if (p.gate == LAGA_GATE_TOKEN) tok = to_f32(static_cast<const T*>(p.x.gate)[r]);
-    if (!mbar_wait(&ring.bar[stage], phase, p.x.err)) return;
+    ok = ok && mbar_wait(&ring.bar[stage], phase, p.x.err);
     const uint8_t* buf = ring.buf + stage * q.stage_bytes;
     const uint8_t *bx = buf + q.src[F_X].off, *by = buf + q.src[F_Y].off, *bg = buf + q.src[F_G].off;
     V8 x[NV];
@@ -365,7 +370,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // is first used by the statistics below.
     auto refill = [&] {
       team_sync<TEAM>(ring.team);
-      if (tl == 0 && it + q.depth < n_it) ring.issue(q, stage, r + q.depth * G);
+      if (ok && tl == 0 && it + q.depth < n_it) ring.issue(q, stage, r + q.depth * G);
     };
     if (p.post) refill();
     if (p.pre) {
@@ -443,6 +448,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int k = 0; k < 4; ++k) acc_post[i].v[k] = acc_pre[i].v[k] = both(0.f);
   int slot = 0, stage = 0;
   uint32_t phase = 0;
+  bool ok = true;
   for (int it = 0; it < n_it; ++it) {
     const long long r = first + it * G;
     float tok = 0.f;
@@ -450,7 +456,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (p.gate == LAGA_GATE_TOKEN) tok = to_f32(static_cast<const T*>(p.x.gate)[r]);
     if (p.pre) st_pre = reinterpret_cast<const float2*>(p.x.stat_pre)[r];
     if (p.post) st_post = reinterpret_cast<const float2*>(p.x.stat_post)[r];
-    if (!mbar_wait(&ring.bar[stage], phase, p.x.err)) return;
+    ok = ok && mbar_wait(&ring.bar[stage], phase, p.x.err);
     const uint8_t* buf = ring.buf + stage * q.stage_bytes;
     const uint8_t *bd = buf + q.src[B_D].off, *bh = buf + q.src[B_DH].off;
     const uint8_t *bx = buf + q.src[B_X].off, *by = buf + q.src[B_Y].off, *bg = buf + q.src[B_G].off;
@@ -577,7 +583,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     // every value read from the row buffer has gone into a store by now
     team_sync<TEAM>(ring.team);
-    if (tl == 0 && it + q.depth < n_it) ring.issue(q, stage, r + q.depth * G);
+    if (ok && tl == 0 && it + q.depth < n_it) ring.issue(q, stage, r + q.depth * G);
     if (++stage == q.depth) {
       stage = 0;
       phase ^= 1;
