@@ -299,9 +299,12 @@ ResArgs make_args(const laga_res_dims& d, const ResPtrs& x) {
   return a;
 }
 
+// Lets the scalar kernel f have `arrays` fp32 rows of the widest width, whatever
+// this call needs: the limit belongs to the kernel, and another thread may be
+// about to launch it for another width.
 template <typename F>
-cudaError_t allow_smem(F* f, size_t bytes) {
-  return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+cudaError_t allow_rows(F* f, int arrays) {
+  return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, arrays * CK_MAX_D * 4);
 }
 
 }  // namespace
@@ -337,7 +340,7 @@ cudaError_t launch_res_fwd(const laga_res_dims& d, const ResPtrs& x, cudaStream_
   const bool f32 = d.io_dtype == LAGA_FP32, wide = rows_wide(d.d, 1);
   auto k = wide ? (f32 ? res_fwd_rows_kernel<float, 1024> : res_fwd_rows_kernel<__nv_bfloat16, 1024>)
                 : (f32 ? res_fwd_rows_kernel<float, 256> : res_fwd_rows_kernel<__nv_bfloat16, 256>);
-  cudaError_t e = allow_smem(k, smem);
+  cudaError_t e = allow_rows(k, 1);
   if (e != cudaSuccess) return e;
   LaunchScope ls_("res_fwd", st);
   k<<<std::min(d.rows, kSms * rows_ctas(d.d, 1)), wide ? 1024 : 256, smem, st>>>(a);
@@ -359,7 +362,7 @@ cudaError_t launch_res_bwd(const laga_res_dims& d, const ResPtrs& x, cudaStream_
     auto k = wide
                  ? (f32 ? res_bwd_rows_kernel<float, 1024> : res_bwd_rows_kernel<__nv_bfloat16, 1024>)
                  : (f32 ? res_bwd_rows_kernel<float, 256> : res_bwd_rows_kernel<__nv_bfloat16, 256>);
-    if ((e = allow_smem(k, smem)) != cudaSuccess) return e;
+    if ((e = allow_rows(k, 3)) != cudaSuccess) return e;
     LaunchScope ls_("res_bwd", st);
     k<<<slots, wide ? 1024 : 256, smem, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

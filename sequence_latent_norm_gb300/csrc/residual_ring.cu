@@ -693,8 +693,10 @@ cudaError_t launch(const char* name, Kernel k, const RingPlan& pl, const RingArg
                    const laga_res_dims& d, const ResArgs& a, cudaStream_t st) {
   const size_t smem = pl.gain_bytes + (size_t)(THREADS / pl.team) * pl.depth * q.stage_bytes;
   if (smem > 44 * 1024) {   // 48 KB with the static part need no opt-in
+    // the limit belongs to the kernel, which other threads may be launching
+    // with other sizes: it is the same in every call
     const cudaError_t e =
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
     if (e != cudaSuccess) return e;
   }
   LaunchScope ls_(name, st);

@@ -1,0 +1,88 @@
+"""Calls of the residual-stream operators and the 8-bit checkpoints that their
+documentation allows beyond one call at a time on the current stream."""
+
+import ctypes
+import threading
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+
+
+def _laga():
+    import sequence_latent_norm_gb300 as laga
+    return laga
+
+
+def _raw_calls(laga, rows, d, dtype, stream):
+    """A forward and a backward of both halves with a full gate as C calls on
+    buffers of their own, and the outputs."""
+    L = laga._lib
+    so, dt = L.load(), dict(bf16=torch.bfloat16, fp32=torch.float32)[dtype]
+    g = torch.Generator(device=DEV).manual_seed(d)
+    x, y, gate, dx, dh = (torch.randn(rows, d, generator=g, device=DEV).to(dt) for _ in range(5))
+    alpha, post, pre = (0.5 + torch.rand(n, generator=g, device=DEV) for n in (1, d, d))
+    x_out, h, dx_in, dy, dgate = (torch.empty_like(x) for _ in range(5))
+    st_post, st_pre = (torch.empty(rows, 2, device=DEV) for _ in range(2))
+    sums = [torch.empty(n, device=DEV) for n in (1, d, d)]
+    dims = L.make_res_dims(rows, d, gate="full", io_dtype=dtype)
+    ws = torch.empty(L.res_workspace_bytes(dims), dtype=torch.uint8, device=DEV)
+    st = ctypes.c_void_p(stream.cuda_stream)
+    ref = ctypes.byref(dims)
+
+    def ptrs(*ts):
+        return [None if t is None else ctypes.c_void_p(t.data_ptr()) for t in ts]
+
+    fwd = ptrs(x, y, gate, alpha, post, pre, x_out, h, None, None, st_post, st_pre)
+    bwd = ptrs(dx, dh, y, x_out, st_post, st_pre, gate, alpha, post, pre, dx_in, dy, dgate, *sums, ws)
+    outs = [x_out, h, st_post, st_pre, dx_in, dy, dgate, *sums]
+    keep = (x, y, gate, dx, dh, alpha, post, pre, ws, dims)
+    return (lambda: so.laga_res_fwd(ref, *fwd, st),
+            lambda: so.laga_res_bwd(ref, *bwd, ws.numel(), st), outs, keep)
+
+
+# Rows and widths of one kernel instance whose launches need different amounts
+# of shared memory: the rings of one team shape (one row a team, or several and
+# the gains), and the scalar kernels.
+SHARED = [((400, 8192), (20, 4104)), ((700, 4096), (20, 2056)), ((20, 5001), (20, 333)),
+          ((20, 16383), (20, 8201))]
+
+
+@pytest.mark.parametrize("one,other", SHARED)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_two_host_threads(one, other, dtype):
+    """Calls of two sizes from two threads, each on a stream of its own, succeed
+    and give what they give alone."""
+    laga = _laga()
+    streams = [torch.cuda.Stream(DEV) for _ in range(2)]
+    made = [_raw_calls(laga, *size, dtype, s) for size, s in zip((one, other), streams)]
+    torch.cuda.synchronize()
+    for fwd, bwd, _, _ in made:
+        assert fwd() == 0 and bwd() == 0
+    torch.cuda.synchronize()
+    want = [[t.clone() for t in outs] for _, _, outs, _ in made]
+    for which in (0, 1):
+        start, bad = threading.Barrier(2), []
+
+        def loop(call, stream):
+            start.wait()
+            for i in range(6000):
+                status = call()
+                if status:
+                    bad.append((i, status))
+                if i % 500 == 499:
+                    stream.synchronize()
+
+        threads = [threading.Thread(target=loop, args=(m[which], s)) for m, s in zip(made, streams)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+        assert not bad, (("forward", "backward")[which], len(bad), bad[0])
+    for (_, _, outs, _), w in zip(made, want):
+        assert all(torch.equal(a, b) for a, b in zip(outs, w))
+    laga._lib.sync_check()
