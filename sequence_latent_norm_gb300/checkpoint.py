@@ -5,6 +5,11 @@ power-of-two scale per 128 channels of a row (the byte layout is that of
 ``include/laga.h``): about one byte per element instead of two, every value
 exact in bf16.  :func:`pack8` makes one, ``unpack`` reads it back and
 :func:`weight_grad8` takes a weight gradient straight from the codes.
+
+``stream`` (a torch.cuda.Stream; None: the current one) is where a call runs
+and what its outputs' memory belongs to.  The caller orders it behind the work
+that makes the inputs, and other streams behind the call; the inputs
+themselves may be dropped as soon as the call returns.
 """
 
 from __future__ import annotations
@@ -21,17 +26,22 @@ IO_NAME = {torch.bfloat16: "bf16", torch.float32: "fp32"}
 class on_stream:
     """Run on ``device`` and ``stream`` (None: the device's current stream);
     entering gives the stream's handle.  What is allocated inside belongs to
-    that stream, so its memory is reused in that stream's order."""
+    that stream, so its memory is reused in that stream's order.  ``inputs``
+    (tensors or None) are read there: with a stream of the caller's they are
+    recorded on it, so that the caller may drop them behind the call."""
 
-    __slots__ = ("device", "stream", "inner")
+    __slots__ = ("device", "stream", "inner", "inputs")
 
-    def __init__(self, device, stream):
+    def __init__(self, device, stream, *inputs):
         if stream is not None and stream.device != device:
             raise ValueError(f"stream on {stream.device}, tensors on {device}")
-        self.device, self.stream, self.inner = device, stream, None
+        self.device, self.stream, self.inner, self.inputs = device, stream, None, inputs
 
     def __enter__(self):
         if self.stream is not None:
+            for t in self.inputs:
+                if t is not None:
+                    t.record_stream(self.stream)
             self.inner = torch.cuda.stream(self.stream)   # its device, too
         elif torch.cuda.current_device() != self.device.index:
             self.inner = torch.cuda.device(self.device)
@@ -103,7 +113,7 @@ class Checkpoint8:
         """The values, [*shape], in bf16 or fp32 (both hold them exactly)."""
         if dtype not in IO_NAME:
             raise ValueError(f"unpack to {dtype}: bf16 or fp32")
-        with on_stream(self.device, stream) as st:
+        with on_stream(self.device, stream, self.data) as st:
             x = torch.empty(self.shape, dtype=dtype, device=self.device)
             _lib.ckpt_unpack(self.rows, self.d, IO_NAME[dtype], self.data.data_ptr(),
                              x.data_ptr(), st)
@@ -123,7 +133,7 @@ def pack8(x: torch.Tensor, stream=None) -> Checkpoint8:
         raise TypeError("pack8 takes a bf16 or fp32 tensor")
     ptr = need(x, "x", x.dtype)
     rows, d = rows_of(x.shape)
-    with on_stream(x.device, stream) as st:
+    with on_stream(x.device, stream, x) as st:
         ck = empty_checkpoint(x.shape, x.device)
         _lib.ckpt_pack(rows, d, IO_NAME[x.dtype], ptr, ck.data.data_ptr(), st)
     return ck
@@ -141,7 +151,7 @@ def weight_grad8(ck: Checkpoint8, dy: torch.Tensor, gamma=None, stream=None) -> 
     dev, name = ck.device, IO_NAME[dy.dtype]
     dy_ptr = need(dy, "dy", dy.dtype, dev)
     g_ptr = 0 if gamma is None else need(gamma, "gamma", torch.float32, dev, (ck.d,))
-    with on_stream(dev, stream) as st:
+    with on_stream(dev, stream, ck.data, dy, gamma) as st:
         dw = torch.empty(ck.d, n, dtype=torch.float32, device=dev)
         nb = _lib.ckpt_dw_workspace_bytes(rows, ck.d, n, name)
         ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None

@@ -112,6 +112,11 @@ class ResidualNorm:
     def _f32(self, t, name, shape):
         return need(t, name, torch.float32, self.device, shape)
 
+    def _used(self, gate, alpha, gamma_post, gamma_pre):
+        """The gate logits, alpha and the gains, None where they are off."""
+        return (gate if self.gate != "none" else None, alpha if self.post else None,
+                gamma_post if self.gain else None, gamma_pre if self.pre else None)
+
     def _params(self, shape, gate, alpha, gamma_post, gamma_pre):
         """Addresses of the gate logits, alpha and the gains (0: off)."""
         d = (self.d,)
@@ -126,11 +131,14 @@ class ResidualNorm:
         """x, y [..., d]; see the class and the module for the rest."""
         rows, shape = self._shape(x, "x")
         full = (*shape[:-1], self.d)
+        if not self.post:
+            y = None
+        gate, alpha, gamma_post, gamma_pre = self._used(gate, alpha, gamma_post, gamma_pre)
         px = self._io(x, "x", full)
         py = self._io(y, "y", full) if self.post else 0
         params = self._params(full, gate, alpha, gamma_post, gamma_pre)
         dev = self.device
-        with on_stream(dev, stream) as st:
+        with on_stream(dev, stream, x, y, gate, alpha, gamma_post, gamma_pre) as st:
             x_out = torch.empty_like(x) if self.post else x
             h = torch.empty_like(x) if self.pre else None
             ck_y = empty_checkpoint(full, dev) if self.ckpt and self.post else None
@@ -142,10 +150,8 @@ class ResidualNorm:
                          ck_y.data.data_ptr() if ck_y else 0, ck_x.data.data_ptr() if ck_x else 0,
                          s_post.data_ptr() if self.post else 0,
                          s_pre.data_ptr() if self.pre else 0, st)
-        saved = ResidualSaved((ck_y or y) if self.post else None,
-                              (ck_x or x_out) if self.pre else None, s_post, s_pre,
-                              gate if self.gate != "none" else None, alpha if self.post else None,
-                              gamma_post if self.gain else None, gamma_pre if self.pre else None)
+        saved = ResidualSaved(ck_y or y, (ck_x or x_out) if self.pre else None, s_post, s_pre, gate,
+                              alpha, gamma_post, gamma_pre)
         return ResidualOut(x_out, h, saved)
 
     def _kept(self, t, name, shape, rows):
@@ -170,10 +176,15 @@ class ResidualNorm:
         k_x = self._kept(saved.x, "saved.x", full, rows) if self.pre else 0
         s_post = self._f32(saved.stat_post, "saved.stat_post", (rows, 2)) if self.post else 0
         s_pre = self._f32(saved.stat_pre, "saved.stat_pre", (rows, 2)) if self.pre else 0
-        gate, alpha, g_post, g_pre = self._params(full, saved.gate, saved.alpha, saved.gamma_post,
-                                                  saved.gamma_pre)
+        used = self._used(saved.gate, saved.alpha, saved.gamma_post, saved.gamma_pre)
+        gate, alpha, g_post, g_pre = self._params(full, *used)
         dev, (dims, nb) = self.device, self._c_dims(rows)
-        with on_stream(dev, stream) as st:
+        read = [dx_out, *used]
+        if self.post:
+            read += [saved.y.data, saved.stat_post]
+        if self.pre:
+            read += [dh, saved.x.data, saved.stat_pre]
+        with on_stream(dev, stream, *read) as st:
             def f32(on, n):
                 return torch.empty(n, dtype=torch.float32, device=dev) if on else None
 

@@ -86,3 +86,83 @@ def test_two_host_threads(one, other, dtype):
     for (_, _, outs, _), w in zip(made, want):
         assert all(torch.equal(a, b) for a, b in zip(outs, w))
     laga._lib.sync_check()
+
+
+def test_inputs_dropped_behind_a_call_on_another_stream():
+    """A call on another stream than the current one may be the last use of
+    its inputs: while the other stream is still busy with what came before,
+    memory that the caller has dropped is not handed out again."""
+    laga = _laga()
+    rows, d, n = 1000, 2048, 1024
+    s = torch.cuda.Stream(DEV)
+    plan = laga.ResidualNorm(d, gate="full", device=DEV)
+    plan8 = laga.ResidualNorm(d, gate="full", ckpt=True, device=DEV)
+    for p in (plan, plan8):        # whatever a first call loads or allocates
+        z = torch.zeros(rows, d, dtype=torch.bfloat16, device=DEV)
+        one = torch.ones(d, device=DEV)
+        r = p.forward(z, z, gate=z, alpha=one[:1], gamma_post=one, gamma_pre=one, stream=s)
+        p.backward(r.saved, z, z, stream=s)
+        laga.weight_grad8(laga.pack8(z, stream=s), z, stream=s)
+    del z, one, r
+    torch.cuda.synchronize()
+
+    def inputs():
+        g = torch.Generator(device=DEV).manual_seed(3)
+        t = {k: torch.randn(rows, d, generator=g, device=DEV).to(torch.bfloat16)
+             for k in ("x", "y", "gate", "dx", "dh")}
+        t["dq"] = torch.randn(rows, n, generator=g, device=DEV).to(torch.bfloat16)
+        t.update({k: 0.5 + torch.rand(m, generator=g, device=DEV)
+                  for k, m in (("alpha", 1), ("gamma_post", d), ("gamma_pre", d))})
+        return t
+
+    def fwd(p, t):
+        return p.forward(t["x"], t["y"], gate=t["gate"], alpha=t["alpha"],
+                         gamma_post=t["gamma_post"], gamma_pre=t["gamma_pre"], stream=s)
+
+    def kept(p):
+        t = inputs()
+        r = fwd(p, t)
+        torch.cuda.synchronize()
+        return dict(saved=r.saved, dx=t["dx"], dh=t["dh"])
+
+    def packed():
+        ck = laga.pack8(inputs()["x"], stream=s)
+        torch.cuda.synchronize()
+        t = inputs()
+        return dict(ck=ck, dq=t["dq"], gamma=t["gamma_pre"])
+
+    def take(r):
+        return [r.x, r.h, r.saved.stat_pre]
+
+    cases = {
+        "forward": (inputs, lambda t: take(fwd(plan, t))),
+        "forward in 8 bits": (inputs, lambda t: take(fwd(plan8, t))),
+        "backward": (lambda: kept(plan), lambda t: plan.backward(t["saved"], t["dx"], t["dh"],
+                                                                 stream=s)),
+        "backward in 8 bits": (lambda: kept(plan8),
+                               lambda t: plan8.backward(t["saved"], t["dx"], t["dh"], stream=s)),
+        "pack": (lambda: dict(x=inputs()["x"]), lambda t: [laga.pack8(t["x"], stream=s).data]),
+        "unpack": (packed, lambda t: [t["ck"].unpack(stream=s)]),
+        "weight gradient": (packed, lambda t: [laga.weight_grad8(t["ck"], t["dq"], t["gamma"],
+                                                                 stream=s)]),
+    }
+    bad = []
+    for name, (make, call) in cases.items():
+        t = make()
+        torch.cuda.synchronize()
+        want = call(t)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(100_000_000)           # ~50 ms
+        got = call(t)
+        t.clear()                                    # the last references
+        # what the current stream allocates and writes meanwhile
+        junk = [torch.full((k,), 77, dtype=torch.uint8, device=DEV)
+                for k in [rows * d * 2, rows * n * 2, rows * laga._lib.ckpt_row_bytes(d), rows * 8,
+                          d * 4, 4] * 8]
+        torch.cuda.synchronize()
+        if not all(torch.equal(a, b) for a, b in zip(got, want) if a is not None):
+            bad.append(name)
+        del junk
+    assert not bad, bad
+    laga._lib.sync_check()
