@@ -20,13 +20,19 @@ struct ResArgs {
 };
 
 // sigmoid(a) = 1 / (1 + e^-a) and 1 - sigmoid(a) = e^-a sigmoid(a), without
-// cancellation on either side.  e^-a is 2^(-a log2 e) by the hardware's
-// exponential: the product's rounding leaves it within 0.7 |a| 2^-24 and 2 ulp
-// of itself.  Below -87 the sigmoid stays at e^-87, the end of the normal
-// range, so that e^-a is finite.
+// cancellation on either side.  e^-a is 2^t, t = -a log2 e, by the hardware's
+// exponential (within 2^-22 of itself); the rounded product and constant move
+// it by another 1.23 |a| 2^-24 of itself.  Both results stay within (1.25 |a|
+// + 9) 2^-24 of themselves: far below a bf16 step, and for fp32 no more than
+// the gate's own rounding (a half step of a moves e^-a by |a| 2^-24) and a few
+// units.
+//
+// Below -87.3 the sigmoid would be subnormal: it is zero, so that a gate of
+// -inf shuts (and 1 - sigmoid(a) is given as zero with it: it only ever
+// multiplies sigmoid(a)).  a is held at -88.5 and above, where e^-a is finite.
 LAGA_DEVINL float2 sigmoid_pair(float a) {
   float e, s;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(a), "f"(-87.f));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(a), "f"(-88.5f));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a * -1.4426950408889634f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
   return make_float2(s, e * s);

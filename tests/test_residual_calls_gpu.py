@@ -1,15 +1,23 @@
-"""Calls of the residual-stream operators and the 8-bit checkpoints that their
-documentation allows beyond one call at a time on the current stream."""
+"""What the documentation of the residual-stream operators and the 8-bit
+checkpoints allows beyond one ordinary call at a time on the current stream:
+two host threads at once, inputs dropped behind a call on another stream, gate
+logits far from zero and without an end."""
 
 import ctypes
 import threading
 
+import numpy as np
 import pytest
 import torch
+
+from laga_inputs import as_f64
+from oracle import residual as ores
 
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda:0"
+U32 = 2.0 ** -24        # half a step of fp32, relative to the value
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: U32}
 
 
 def _laga():
@@ -166,3 +174,78 @@ def test_inputs_dropped_behind_a_call_on_another_stream():
         del junk
     assert not bad, bad
     laga._lib.sync_check()
+
+
+# Error of sigmoid(a) = 1 / (1 + e^-a) and of 1 - sigmoid(a) relative to
+# themselves, in units of u = 2^-24.  e^-a = 2^t with t = -a log2 e: the
+# rounded constant (0.23 u) and the rounded product (1 u) are each off by
+# their share of a log2 e, which moves 2^t by 1.23 |a| u of itself; the
+# hardware's exponential is within 2^-22 = 4 u; 1 + e^-a and its reciprocal
+# (2^-23) add 3 u, the product that makes 1 - sigmoid(a) one more.
+def _sigmoid_u(a):
+    return (1.25 * np.abs(a) + 9.0) * U32
+
+
+# below this the sigmoid is no normal fp32 number any more; it may be zero
+TINY = 2.0 ** -126
+
+FINITE = [-100.0, -95.0, -90.0, -88.0, -87.0, -86.0, -80.0, -60.0, -40.0, -20.0, -10.0, -5.0, -1.0,
+          -0.125, 0.0, 0.125, 1.0, 5.0, 10.0, 20.0, 40.0, 60.0, 80.0, 86.0, 87.0, 88.0, 90.0, 100.0]
+
+
+def _gate_run(gate, d, kind, dtype, x0=0.0):
+    """alpha = y = dx_out = 1 and no norm: x' = x + s, dy = s and dgate = s (1 -
+    s), each summed over the row for a token gate."""
+    plan = _laga().ResidualNorm(d, pre=False, norm_post="none", gate=kind, device=DEV,
+                                io_dtype="bf16" if dtype == torch.bfloat16 else "fp32")
+    rows = gate.shape[0]
+    x = torch.full((rows, d), x0, dtype=dtype, device=DEV)
+    y = torch.ones(rows, d, dtype=dtype, device=DEV)
+    r = plan.forward(x, y, gate=gate.to(DEV), alpha=torch.ones(1, device=DEV))
+    g = plan.backward(r.saved, y)
+    _laga()._lib.sync_check()
+    return as_f64(r.x), as_f64(g.dy), as_f64(g.dgate)
+
+
+@pytest.mark.parametrize("d", [512, 333])
+@pytest.mark.parametrize("kind", ["full", "token"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gate_logits_far_from_zero(d, kind, dtype):
+    a = torch.tensor(FINITE)
+    gate = (a.repeat(1 + d // len(a))[:d].repeat(5, 1) if kind == "full" else a[:, None]).to(dtype)
+    v = as_f64(gate)
+    s, c, u = ores.sigmoid(v), ores.sigmoid(-v), _sigmoid_u(v)
+    x, dy, dgate = _gate_run(gate, d, kind, dtype)
+    tol = s * (u + HALF[dtype]) * (1 + 2.0 ** -7) + TINY
+    assert (np.abs(x - s) <= tol).all() and (np.abs(dy - s) <= tol).all()
+    # s (1 - s): two of the errors and three products; d terms add d u at most
+    n, add = (d, d * U32) if kind == "token" else (1, 0.0)
+    tol = n * (s * c * (2 * u + 3 * U32 + add + HALF[dtype]) * (1 + 2.0 ** -7) + TINY)
+    assert (np.abs(dgate - n * s * c) <= tol).all()
+
+
+@pytest.mark.parametrize("d", [512, 333])
+@pytest.mark.parametrize("kind", ["full", "token"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gate_logits_without_an_end(d, kind, dtype):
+    """-inf shuts a gate and +inf opens it, exactly, and neither has a
+    gradient; a NaN is one in what it gates."""
+    inf, nan = float("inf"), float("nan")
+    if kind == "full":
+        gate = torch.zeros(4, d)
+        gate[0, 3], gate[1, 5], gate[2, d - 1] = -inf, inf, nan
+        at = (np.array([0, 1, 2]), np.array([3, 5, d - 1]))
+    else:
+        gate = torch.tensor([-inf, inf, nan, 0.0])[:, None]
+        at = (np.array([0, 1, 2]), slice(None))
+    for x0 in (0.0, 3.0):
+        x, dy, dgate = _gate_run(gate.to(dtype), d, kind, dtype, x0)
+        want = np.full((4, d), 0.5)
+        for i, s in enumerate((0.0, 1.0, nan)):
+            want[at[0][i], at[1] if kind == "token" else at[1][i]] = s
+        assert np.array_equal(x, x0 + want, equal_nan=True)
+        assert np.array_equal(dy, want, equal_nan=True)
+        want = want * (1 - want)
+        if kind == "token":     # rounded once: 333/4 = 83.25 has a bit more than bf16 holds
+            want = as_f64(torch.from_numpy(want.sum(axis=1, keepdims=True)).to(dtype))
+        assert np.array_equal(dgate, want, equal_nan=True)
