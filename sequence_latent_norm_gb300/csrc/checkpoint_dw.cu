@@ -608,7 +608,7 @@ DwPlan dw_plan(int rows, int d, int n, bool fp32) {
   p.groups = p.cols / CK_GROUP;
   p.n_tiles = (n + pl.bn - 1) / pl.bn;
   p.tiles = (p.groups + 1) / 2 * p.n_tiles;
-  p.steps = (rows + KT - 1) / KT;
+  p.steps = (int)(((long long)rows + KT - 1) / KT);
   p.chain = fp32 ? CHAIN_PIECES : CHAIN;
   p.pieces = pl.pieces;
   p.rounds = p.tiles / PAIRS;
