@@ -69,6 +69,12 @@ def need(t, name, dtype, device=None, shape=None):
     return t.data_ptr()
 
 
+def on_16(t):
+    """``t``, or a copy of it (of the current stream) if it starts off a 16-byte
+    boundary, as one layer's entry of a parameter tensor of all layers may."""
+    return t if t is None or t.data_ptr() % 16 == 0 else t.detach().clone()
+
+
 def rows_of(shape):
     """Rows and width of a [..., d] tensor seen as a matrix."""
     if len(shape) < 1:
@@ -142,7 +148,7 @@ def pack8(x: torch.Tensor, stream=None) -> Checkpoint8:
 def weight_grad8(ck: Checkpoint8, dy: torch.Tensor, gamma=None, stream=None) -> torch.Tensor:
     """dW [d, n] fp32 = diag(gamma) v^T dy of the checkpointed activation v
     [rows, d] and dy [..., n] (bf16 or fp32, as many rows): the gradient of W
-    in (v gamma) W.  gamma [d] fp32, or None for 1."""
+    in (v gamma) W.  gamma [d] fp32 (it may start anywhere), or None for 1."""
     if not isinstance(dy, torch.Tensor) or dy.dtype not in IO_NAME:
         raise TypeError("dy must be a bf16 or fp32 tensor")
     rows, n = rows_of(dy.shape)
@@ -155,6 +161,9 @@ def weight_grad8(ck: Checkpoint8, dy: torch.Tensor, gamma=None, stream=None) -> 
         dw = torch.empty(ck.d, n, dtype=torch.float32, device=dev)
         nb = _lib.ckpt_dw_workspace_bytes(rows, ck.d, n, name)
         ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
+        if g_ptr % 16:
+            gamma = on_16(gamma)
+            g_ptr = gamma.data_ptr()
         _lib.ckpt_dw(rows, ck.d, n, name, ck.data.data_ptr(), dy_ptr, g_ptr, dw.data_ptr(),
                      ws.data_ptr() if nb else 0, nb, st)
     return dw

@@ -20,7 +20,7 @@ import torch
 
 from . import _lib
 from .api import _TORCH_DT
-from .checkpoint import Checkpoint8, empty_checkpoint, need, on_stream, rows_of
+from .checkpoint import Checkpoint8, empty_checkpoint, need, on_16, on_stream, rows_of
 
 
 class ResidualSaved(NamedTuple):
@@ -61,8 +61,10 @@ class ResidualNorm:
     norm_post "layer", "rms" or "none" (a plain gated residual add);
     norm_pre "layer" or "rms"; gate "none", "token" (logits [..., 1]) or
     "full" (logits [..., d]); io_dtype "bf16" or "fp32" of x, y, gate, h and
-    their gradients.  Gains and alpha ([1]) are fp32.  A call takes any number
-    of rows and keeps none of its data in the object."""
+    their gradients.  Gains and alpha ([1]) are fp32 and may start anywhere (one
+    layer's entry of a tensor of all layers'); the other tensors start on a
+    16-byte boundary.  What is off is ignored where it is given.  A call takes
+    any number of rows and keeps none of its data in the object."""
 
     def __init__(self, d: int, *, post: bool = True, pre: bool = True, norm_post: str = "rms",
                  norm_pre: str = "rms", gate: str = "none", ckpt: bool = False,
@@ -126,6 +128,13 @@ class ResidualNorm:
                 self._f32(gamma_post, "gamma_post", d) if self.gain else 0,
                 self._f32(gamma_pre, "gamma_pre", d) if self.pre else 0)
 
+    @staticmethod
+    def _aligned(params, used):
+        """The addresses again, of copies of alpha and the gains where these start
+        off a 16-byte boundary; and the copies, to be held up to the launch."""
+        moved = [on_16(t) for t in used[1:]]
+        return (params[0], *(0 if t is None else t.data_ptr() for t in moved)), moved
+
     def forward(self, x, y=None, *, gate=None, alpha=None, gamma_post=None, gamma_pre=None,
                 stream=None) -> ResidualOut:
         """x, y [..., d]; see the class and the module for the rest."""
@@ -133,25 +142,26 @@ class ResidualNorm:
         full = (*shape[:-1], self.d)
         if not self.post:
             y = None
-        gate, alpha, gamma_post, gamma_pre = self._used(gate, alpha, gamma_post, gamma_pre)
+        used = self._used(gate, alpha, gamma_post, gamma_pre)
         px = self._io(x, "x", full)
         py = self._io(y, "y", full) if self.post else 0
-        params = self._params(full, gate, alpha, gamma_post, gamma_pre)
+        params = self._params(full, *used)
         dev = self.device
-        with on_stream(dev, stream, x, y, gate, alpha, gamma_post, gamma_pre) as st:
+        with on_stream(dev, stream, x, y, *used) as st:
             x_out = torch.empty_like(x) if self.post else x
             h = torch.empty_like(x) if self.pre else None
             ck_y = empty_checkpoint(full, dev) if self.ckpt and self.post else None
             ck_x = empty_checkpoint(full, dev) if self.ckpt and self.pre else None
             s_post = torch.empty(rows, 2, dtype=torch.float32, device=dev) if self.post else None
             s_pre = torch.empty(rows, 2, dtype=torch.float32, device=dev) if self.pre else None
+            if (params[1] | params[2] | params[3]) % 16:
+                params, moved = self._aligned(params, used)
             _lib.res_fwd(self._c_dims(rows)[0], px, py, *params,
                          x_out.data_ptr() if self.post else 0, h.data_ptr() if self.pre else 0,
                          ck_y.data.data_ptr() if ck_y else 0, ck_x.data.data_ptr() if ck_x else 0,
                          s_post.data_ptr() if self.post else 0,
                          s_pre.data_ptr() if self.pre else 0, st)
-        saved = ResidualSaved(ck_y or y, (ck_x or x_out) if self.pre else None, s_post, s_pre, gate,
-                              alpha, gamma_post, gamma_pre)
+        saved = ResidualSaved(ck_y or y, (ck_x or x_out) if self.pre else None, s_post, s_pre, *used)
         return ResidualOut(x_out, h, saved)
 
     def _kept(self, t, name, shape, rows):
@@ -177,7 +187,7 @@ class ResidualNorm:
         s_post = self._f32(saved.stat_post, "saved.stat_post", (rows, 2)) if self.post else 0
         s_pre = self._f32(saved.stat_pre, "saved.stat_pre", (rows, 2)) if self.pre else 0
         used = self._used(saved.gate, saved.alpha, saved.gamma_post, saved.gamma_pre)
-        gate, alpha, g_post, g_pre = self._params(full, *used)
+        params = self._params(full, *used)
         dev, (dims, nb) = self.device, self._c_dims(rows)
         read = [dx_out, *used]
         if self.post:
@@ -194,11 +204,13 @@ class ResidualNorm:
             dalpha, dg_post = f32(self.post, 1), f32(self.gain, self.d)
             dg_pre = f32(self.pre, self.d)
             ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
+            if (params[1] | params[2] | params[3]) % 16:
+                params, moved = self._aligned(params, used)
 
             def ptr(t):
                 return 0 if t is None else t.data_ptr()
 
-            _lib.res_bwd(dims, p_dx, p_dh, k_y, k_x, s_post, s_pre, gate, alpha, g_post, g_pre,
+            _lib.res_bwd(dims, p_dx, p_dh, k_y, k_x, s_post, s_pre, *params,
                          ptr(dx) if self.pre else 0, ptr(dy), ptr(dgate), ptr(dalpha),
                          ptr(dg_post), ptr(dg_pre), ptr(ws), nb, st)
         return ResidualGrads(dx, dy, dgate, dalpha, dg_post, dg_pre)

@@ -1,7 +1,8 @@
 """What the documentation of the residual-stream operators and the 8-bit
 checkpoints allows beyond one ordinary call at a time on the current stream:
-two host threads at once, inputs dropped behind a call on another stream, gate
-logits far from zero and without an end."""
+two host threads at once, inputs dropped behind a call on another stream,
+parameters that are slices of larger tensors, gate logits far from zero and
+without an end."""
 
 import ctypes
 import threading
@@ -173,6 +174,34 @@ def test_inputs_dropped_behind_a_call_on_another_stream():
             bad.append(name)
         del junk
     assert not bad, bad
+    laga._lib.sync_check()
+
+
+@pytest.mark.parametrize("d", [512, 333])
+def test_parameters_that_are_slices(d):
+    """alpha, the gains and a weight gradient's gain as a model holds them: one
+    layer's entries of a tensor of all layers', wherever they start."""
+    laga = _laga()
+    rows, layers = 40, 4
+    g = torch.Generator(device=DEV).manual_seed(d)
+    x, y, dx, dh = (torch.randn(rows, d, generator=g, device=DEV).to(torch.bfloat16)
+                    for _ in range(4))
+    alpha = 0.5 + torch.rand(layers, generator=g, device=DEV)
+    gains = 0.5 + torch.rand(2 * layers * d + 1, generator=g, device=DEV)
+    post, pre = gains[1:1 + layers * d].view(layers, d), gains[1 + layers * d:].view(layers, d)
+    for ckpt in (False, True):
+        plan = laga.ResidualNorm(d, ckpt=ckpt, device=DEV)
+        for i in range(layers):
+            outs = []
+            for own in (lambda v: v.clone(), lambda v: v):
+                par = dict(alpha=own(alpha[i:i + 1]), gamma_post=own(post[i]),
+                           gamma_pre=own(pre[i]))
+                r = plan.forward(x, y, **par)
+                out = [r.x, r.h, *plan.backward(r.saved, dx, dh)]
+                if ckpt:
+                    out.append(laga.weight_grad8(r.saved.x, dx, par["gamma_pre"]))
+                outs.append([v for v in out if v is not None])
+            assert all(torch.equal(a, b) for a, b in zip(*outs))
     laga._lib.sync_check()
 
 
