@@ -189,11 +189,13 @@ class ResidualNorm:
         used = self._used(saved.gate, saved.alpha, saved.gamma_post, saved.gamma_pre)
         params = self._params(full, *used)
         dev, (dims, nb) = self.device, self._c_dims(rows)
-        read = [dx_out, *used]
-        if self.post:
-            read += [saved.y.data, saved.stat_post]
-        if self.pre:
-            read += [dh, saved.x.data, saved.stat_pre]
+        read = []
+        if stream is not None:       # what on_stream records there
+            read = [dx_out, *used]
+            if self.post:
+                read += [saved.y.data, saved.stat_post]
+            if self.pre:
+                read += [dh, saved.x.data, saved.stat_pre]
         with on_stream(dev, stream, *read) as st:
             def f32(on, n):
                 return torch.empty(n, dtype=torch.float32, device=dev) if on else None
