@@ -20,6 +20,11 @@
 //           swizzled
 //   12-19   epilogue: adds up the accumulators of a tile in registers, then
 //           multiplies by gamma and stores
+// Decoders and epilogue wait as whole warps and run collective instructions
+// in between.  A lane whose wait gave up (the error word then says so) goes
+// through the rest without waiting and without telling anyone, so that its warp
+// stays whole: if it left, lanes whose wait had just succeeded would be stuck.
+//
 // A step is 128 tokens.  Every hand-over between warps costs a few hundred
 // clocks, whatever the step's size: 16384 x 7168 x 1536 takes 309 us with steps
 // of 128 tokens and 377 us with 64 (the rings as deep in tokens).  What bounds
@@ -358,16 +363,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int q = warp & 3, c0 = ((warp - W_EPI) >> 2) * HALF;
     uint32_t ic = 0;
     bool ok = true;
-    while (ok && w.next(p, pair)) {
+    while (w.next(p, pair)) {
       float2 acc[HALF / 2];
 #pragma unroll
       for (int j = 0; j < HALF / 2; ++j) acc[j] = make_float2(0.f, 0.f);
       for (int k0 = 0; k0 < w.kn; k0 += p.chain, ++ic) {
         const int buf = ic & 1;
-        if (!mbar_wait(&acc_full[buf], (ic >> 1) & 1, p.err)) {
-          ok = false;
-          break;
-        }
+        ok = ok && mbar_wait(&acc_full[buf], (ic >> 1) & 1, p.err);
         tc_fence_after();
 #pragma unroll
         for (int j = 0; j < HALF / 16; ++j) {
@@ -380,12 +382,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(smem_cluster_addr(&acc_empty[buf], 0));
+        if (ok && lane == 0) mbar_arrive_cluster(smem_cluster_addr(&acc_empty[buf], 0));
       }
-      if (!ok) break;
       const int r = (int)rank * CK_GROUP + channel_of(q * 32 + lane);   // row of the pair's tile
       const int row = (w.t / p.n_tiles) * 256 + r, n0 = (w.t % p.n_tiles) * BN + c0;
-      if (row < p.d) {
+      if (ok && row < p.d) {
         const float gain = p.gamma ? p.gamma[row] : 1.f;
         float* dst = w.frag >= 0 ? p.frag + ((long long)w.frag * 256 + r) * BN + c0
                                  : p.dw + (long long)row * p.n + n0;
@@ -431,22 +432,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     uint32_t byte[N];
     uint32_t base = 0;   // steps before this piece
     bool ok = true;
-    while (ok && w.next(p, pair)) {
+    while (w.next(p, pair)) {
       const int g = ((w.t / p.n_tiles) * 2 + (int)rank) & 15;
       const uint32_t end = base + w.kn;
       auto fetch = [&](uint32_t it) {
         const int sc = it % NC;
-        if (!mbar_wait(&c_full[sc], (it / NC) & 1, p.err)) return false;
+        ok = ok && mbar_wait(&c_full[sc], (it / NC) & 1, p.err);
         const uint8_t* src = sm + C_OFF + sc * C_BYTES;
 #pragma unroll
         for (int h = 0; h < N; ++h) {
           v[h] = *reinterpret_cast<const uint4*>(src + src_off[h & 1] + (h >> 1) * 8 * CK_GROUP);
           byte[h] = src[row_off[h & 1] + (h >> 1) * 8 * 16 + g];
         }
-        return true;
       };
-      ok = fetch(base);
-      for (uint32_t it = base; ok && it < end; ++it) {
+      fetch(base);
+      for (uint32_t it = base; it < end; ++it) {
         uint4 q[N];
         uint32_t e[N];
 #pragma unroll
@@ -454,14 +454,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           q[h] = v[h];
           e[h] = byte[h];
         }
-        if (it + 1 < end && !fetch(it + 1)) {
-          ok = false;
-          break;
-        }
-        if (it >= NA && !mbar_wait(&a_empty[(it - NA) % NE], ((it - NA) / NE) & 1, p.err)) {
-          ok = false;
-          break;
-        }
+        if (it + 1 < end) fetch(it + 1);
+        if (it >= NA) ok = ok && mbar_wait(&a_empty[(it - NA) % NE], ((it - NA) / NE) & 1, p.err);
         uint8_t* dst = sm + it % NA * A_BYTES;
 #pragma unroll
         for (int h = 0; h < N; ++h) {
@@ -476,7 +470,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // The codes are given back only here, where what was made of them has
         // been stored: an arrival can overtake loads that are still queued,
         // and the next codes then come in under them.
-        if (lane == 0) {
+        if (ok && lane == 0) {
           mbar_arrive(&c_empty[it % NC]);
           mbar_arrive(&a_full[it % NE]);
         }

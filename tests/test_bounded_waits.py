@@ -1,0 +1,42 @@
+"""Who may wait how: where a warp waits on an mbarrier as a whole, and runs
+collective instructions behind the wait, a lane whose bounded wait gave up
+has to stay with its warp (it goes on without waiting).  A lane that left would
+be waited for without a bound by those that a phase completing around the last
+poll let through.  This is read off the sources, since a wait that runs out in
+such a moment cannot be brought about."""
+
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "sequence_latent_norm_gb300", "csrc")
+
+
+def whole_warp_waits(path):
+    """(line, statement up to the wait) of every wait that is not in a block of
+    one lane's."""
+    src = re.sub(r"//[^\n]*", "", open(path).read())
+    out, blocks, text = [], [], ""
+    for m in re.finditer(r"[{};]|mbar_wait(?:_cluster)?\(|ring\.wait\(|[^{};]", src):
+        t = m.group()
+        if t == "{":
+            blocks.append(text)
+        elif t == "}":
+            blocks.pop()
+        elif t.endswith("wait("):
+            # one lane's, or inside a wait that is itself asked for by name
+            other = r"\b(lane|tl|threadIdx\.x) == 0\b|\bbool wait\("
+            if not any(re.search(other, b) for b in [*blocks, text]):
+                out.append((src.count("\n", 0, m.start()) + 1, " ".join((text + t).split())))
+        text = "" if t in "{};" else text + t
+    return out
+
+
+@pytest.mark.parametrize("name", ["checkpoint_dw.cu", "residual_ring.cu"])
+def test_lanes_that_gave_up_stay_with_their_warp(name):
+    waits = whole_warp_waits(os.path.join(CSRC, name))
+    assert waits
+    left = [(line, text) for line, text in waits if not re.search(r"\bok = ok && (mbar_|ring\.)wait", text)]
+    assert not left, f"{name}: these waits decide where their lane goes on: {left}"
