@@ -202,6 +202,14 @@ LAGA_DEVINL bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// A thread that copies leaves when its last copies have landed (of `it` in all,
+// one per barrier), also where it or those that it feeds gave up: they must
+// not arrive in shared memory that the CTA has left.
+template <int N>
+LAGA_DEVINL void wait_landed(uint64_t (&full)[N], uint32_t it, int* err) {
+  for (uint32_t i = it > N ? it - N : 0; i < it; ++i) mbar_wait(&full[i % N], (i / N) & 1, err);
+}
+
 template <int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     ckpt_dw_kernel(const __grid_constant__ DwMaps tm, const __grid_constant__ DwParams p) {
@@ -209,11 +217,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
   // Each CTA's: c_full, c_empty (codes), a_empty, b_empty, acc_full (the pair
-  // MMAs' commits arrive in both).  a_full: an arrival of every decoder warp,
+  // MMAs' commits arrive in both), mma_done.  a_full: an arrival of every decoder warp,
   // and in rank 0 one that says that rank 1's is complete.  Rank 0's: b_full
   // (both CTAs' dy bytes), acc_empty (epilogue warps of both).
   __shared__ uint64_t c_full[NC], c_empty[NC], a_full[NE], a_empty[NE], b_full[NB], b_empty[NB];
-  __shared__ uint64_t acc_full[2], acc_empty[2];
+  __shared__ uint64_t acc_full[2], acc_empty[2], mma_done;
   __shared__ uint32_t tmem_sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -237,6 +245,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 16);
     }
+    mbar_init(&mma_done, 1);
     fence_barrier_init();
   }
   if (warp == 3) {
@@ -275,6 +284,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                                p.pieces - 1 - s);
           }
       }
+      // Rank 0's barriers count both CTAs' bytes.  What rank 1 may have loaded
+      // beyond them was let through by commits of the MMA issuer, which leaves
+      // a whole wait's limit after its last one.
+      if (rank == 0) wait_landed(b_full, it, p.err);
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -297,6 +310,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           tma_load_2d(dst + CODE_BYTES, &tm.scales, &c_full[st], p.cols + (g & ~15), t0);
         }
       }
+      wait_landed(c_full, it, p.err);
     }
   } else if (warp == 2 && rank == 0) {
     if (lane == 0) {
@@ -344,6 +358,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           mma_commit_pair(&acc_full[buf]);
         }
       }
+      // the MMAs are done before the pair's shared memory and TMEM are left
+      mma_commit_pair(&mma_done);
+      mbar_wait(&mma_done, 0, p.err);
     }
   } else if (warp < W_DEC) {
     // Rank 1's warps 2 and 3, a step each in turn: announce the decoded tile

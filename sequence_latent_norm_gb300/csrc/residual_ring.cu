@@ -17,7 +17,9 @@
 //
 // A thread whose wait for a row gave up (the error word then says so) goes
 // through the rest of its rows without waiting, so that it still meets its team
-// at every barrier.
+// at every barrier.  Where that is the thread that fills the ring, it asks for no
+// further rows, and those on their way have had the whole limit of its wait: it
+// asked for all of them before.
 #include <algorithm>
 
 #include "residual.cuh"

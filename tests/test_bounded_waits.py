@@ -19,16 +19,16 @@ def whole_warp_waits(path):
     one lane's."""
     src = re.sub(r"//[^\n]*", "", open(path).read())
     out, blocks, text = [], [], ""
-    for m in re.finditer(r"[{};]|mbar_wait(?:_cluster)?\(|ring\.wait\(|[^{};]", src):
+    for m in re.finditer(r"[{};]|mbar_wait(?:_cluster)?\(|[^{};]", src):
         t = m.group()
         if t == "{":
             blocks.append(text)
         elif t == "}":
             blocks.pop()
-        elif t.endswith("wait("):
-            # one lane's, or inside a wait that is itself asked for by name
-            other = r"\b(lane|tl|threadIdx\.x) == 0\b|\bbool wait\("
-            if not any(re.search(other, b) for b in [*blocks, text]):
+        elif t.startswith("mbar_wait"):
+            # one lane's, or of a function that one lane calls
+            one = r"\b(lane|tl|threadIdx\.x) == 0\b|\bvoid wait_landed\("
+            if not any(re.search(one, b) for b in [*blocks, text]):
                 out.append((src.count("\n", 0, m.start()) + 1, " ".join((text + t).split())))
         text = "" if t in "{};" else text + t
     return out
@@ -38,5 +38,18 @@ def whole_warp_waits(path):
 def test_lanes_that_gave_up_stay_with_their_warp(name):
     waits = whole_warp_waits(os.path.join(CSRC, name))
     assert waits
-    left = [(line, text) for line, text in waits if not re.search(r"\bok = ok && (mbar_|ring\.)wait", text)]
+    left = [(line, text) for line, text in waits if not re.search(r"\bok = ok && mbar_wait", text)]
     assert not left, f"{name}: these waits decide where their lane goes on: {left}"
+
+
+@pytest.mark.parametrize("name,issue,landed", [
+    ("checkpoint_dw.cu", r"tma_load_3d_pair\(", r"wait_landed\(b_full, it, p\.err\);"),
+    ("checkpoint_dw.cu", r"tma_load_2d\(", r"wait_landed\(c_full, it, p\.err\);"),
+    ("checkpoint_dw.cu", r"mma_ss_pair\(", r"mbar_wait\(&mma_done, 0, p\.err\);")])
+def test_what_is_in_flight_is_waited_for(name, issue, landed):
+    """A kernel does not leave its shared memory to copies or products that it
+    has in flight, also where a wait gave up: behind the code that issues them
+    stands a wait for all of them, with a limit, like the others."""
+    src = open(os.path.join(CSRC, name)).read()
+    first = re.search(issue, src)
+    assert first and re.search(landed, src[first.end():]), name
