@@ -149,6 +149,8 @@ def weight_grad8(ck: Checkpoint8, dy: torch.Tensor, gamma=None, stream=None) -> 
     """dW [d, n] fp32 = diag(gamma) v^T dy of the checkpointed activation v
     [rows, d] and dy [..., n] (bf16 or fp32, as many rows): the gradient of W
     in (v gamma) W.  gamma [d] fp32 (it may start anywhere), or None for 1."""
+    if not isinstance(ck, Checkpoint8):
+        raise TypeError("weight_grad8 takes a Checkpoint8")
     if not isinstance(dy, torch.Tensor) or dy.dtype not in IO_NAME:
         raise TypeError("dy must be a bf16 or fp32 tensor")
     rows, n = rows_of(dy.shape)

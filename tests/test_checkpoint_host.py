@@ -1,5 +1,5 @@
-"""Sizes of the weight gradient from 8-bit checkpoints at the top of their
-accepted range, before any CUDA call."""
+"""The weight gradient from 8-bit checkpoints before any CUDA call: sizes at
+the top of their accepted range, and what is not a checkpoint."""
 
 import pytest
 import torch
@@ -37,3 +37,11 @@ def test_the_most_rows_need_their_workspace(lib):
         for ws, n in ((None, 0), (p[3], nb - 1)):
             assert so.laga_ckpt_dw(rows, 128, 8, 0, p[0], p[1], None, p[2], ws, n, None) == \
                 lib.LAGA_ERR_WORKSPACE
+
+
+def test_what_is_not_a_checkpoint_is_refused(lib):
+    import sequence_latent_norm_gb300 as laga
+    dy = torch.zeros(4, 8, dtype=torch.bfloat16)
+    for ck in (None, dy, torch.zeros(4, 144, dtype=torch.uint8)):
+        with pytest.raises(TypeError, match="Checkpoint8"):
+            laga.weight_grad8(ck, dy)
