@@ -177,6 +177,48 @@ def test_inputs_dropped_behind_a_call_on_another_stream():
     laga._lib.sync_check()
 
 
+def test_a_captured_call_on_a_forked_stream():
+    """A capture that forks to another stream and joins it again, with inputs
+    made and dropped inside: replayed on other values it gives what eager calls
+    give."""
+    laga = _laga()
+    rows, d = 300, 640
+    plan = laga.ResidualNorm(d, gate="full", ckpt=True, device=DEV)
+    gain = torch.rand(d + 1, device=DEV)[1:]          # off a 16-byte boundary
+    alpha = torch.full((1,), 0.5, device=DEV)
+    side = torch.cuda.Stream(DEV)
+
+    def step(src, stream):
+        x, y, gate, dx, dh = ((src * k).to(torch.bfloat16) for k in (1, 2, 3, 4, 5))
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        r = plan.forward(x, y, gate=gate, alpha=alpha, gamma_post=gain, gamma_pre=gain,
+                         stream=stream)
+        g = plan.backward(r.saved, dx, dh, stream=stream)
+        dw = laga.weight_grad8(r.saved.x, dx, gain, stream=stream)
+        v = laga.pack8(x, stream=stream).unpack(stream=stream)
+        del x, y, gate, dx, dh
+        junk = torch.full((rows, d), 9.0, dtype=torch.bfloat16, device=DEV)
+        if stream is not None:
+            torch.cuda.current_stream().wait_stream(stream)
+        return [r.x, r.h, *g, v, dw], junk
+
+    src = torch.randn(rows, d, device=DEV)
+    step(src, None)
+    step(src, side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs, junk = step(src, side)
+    src.copy_(torch.randn(rows, d, device=DEV))
+    want, _ = step(src, side)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    laga._lib.sync_check()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
 @pytest.mark.parametrize("d", [512, 333])
 def test_parameters_that_are_slices(d):
     """alpha, the gains and a weight gradient's gain as a model holds them: one
