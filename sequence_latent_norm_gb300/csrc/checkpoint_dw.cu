@@ -207,7 +207,8 @@ LAGA_DEVINL bool mbar_test(uint64_t* bar, uint32_t parity) {
 // not arrive in shared memory that the CTA has left.
 template <int N>
 LAGA_DEVINL void wait_landed(uint64_t (&full)[N], uint32_t it, int* err) {
-  for (uint32_t i = it > N ? it - N : 0; i < it; ++i) mbar_wait(&full[i % N], (i / N) & 1, err);
+  for (uint32_t i = it > N ? it - N : 0; i < it; ++i)
+    mbar_wait_each(&full[i % N], (i / N) & 1, err);
 }
 
 template <int BN>
@@ -270,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         for (int j = 0; ok && j < w.kn; ++j)
           for (int s = 0; s < p.pieces; ++s, ++it) {
             const int st = it % NB;
-            if (it >= NB && !mbar_wait(&b_empty[st], (it / NB - 1) & 1, p.err)) {
+            if (it >= NB && !mbar_wait_each(&b_empty[st], (it / NB - 1) & 1, p.err)) {
               ok = false;
               break;
             }
@@ -300,7 +301,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         for (int j = 0; j < w.kn; ++j, ++it) {
           const int t0 = w.step(p, j) * KT;
           const int st = it % NC;
-          if (it >= NC && !mbar_wait(&c_empty[st], (it / NC - 1) & 1, p.err)) {
+          if (it >= NC && !mbar_wait_each(&c_empty[st], (it / NC - 1) & 1, p.err)) {
             ok = false;
             break;
           }
@@ -329,14 +330,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           const uint32_t dst = tmem + (uint32_t)(buf * ACC_COLS);
           const int k1 = min(k0 + p.chain, w.kn);
           for (int k = k0; ok && k < k1; ++k, ++ia) {
-            if (!a_ready && !mbar_wait(&a_full[ia % NE], (ia / NE) & 1, p.err)) {
+            if (!a_ready && !mbar_wait_each(&a_full[ia % NE], (ia / NE) & 1, p.err)) {
               ok = false;
               break;
             }
             const uint32_t alo = sdesc_lo(smem_u32(sm + ia % NA * A_BYTES), BOX);
             for (int s = 0; s < p.pieces; ++s, ++ib) {
               const int st = ib % NB;
-              if (!b_ready && !mbar_wait(&b_full[st], (ib / NB) & 1, p.err)) {
+              if (!b_ready && !mbar_wait_each(&b_full[st], (ib / NB) & 1, p.err)) {
                 ok = false;
                 break;
               }
@@ -360,7 +361,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       // the MMAs are done before the pair's shared memory and TMEM are left
       mma_commit_pair(&mma_done);
-      mbar_wait(&mma_done, 0, p.err);
+      mbar_wait_each(&mma_done, 0, p.err);
     }
   } else if (warp < W_DEC) {
     // Rank 1's warps 2 and 3, a step each in turn: announce the decoded tile
@@ -370,7 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (lane == 0 && rank == 1) {
       const uint32_t total = (uint32_t)(p.rounds * p.steps + w.left);
       for (uint32_t it = warp & 1; it < total; it += 2) {
-        if (!mbar_wait(&a_full[it % NE], (it / NE) & 1, p.err)) break;
+        if (!mbar_wait_each(&a_full[it % NE], (it / NE) & 1, p.err)) break;
         mbar_arrive_cluster(smem_cluster_addr(&a_full[it % NE], 0));
       }
     }
@@ -386,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       for (int j = 0; j < HALF / 2; ++j) acc[j] = make_float2(0.f, 0.f);
       for (int k0 = 0; k0 < w.kn; k0 += p.chain, ++ic) {
         const int buf = ic & 1;
-        ok = ok && mbar_wait(&acc_full[buf], (ic >> 1) & 1, p.err);
+        ok = ok && mbar_wait_each(&acc_full[buf], (ic >> 1) & 1, p.err);
         tc_fence_after();
 #pragma unroll
         for (int j = 0; j < HALF / 16; ++j) {
@@ -454,7 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const uint32_t end = base + w.kn;
       auto fetch = [&](uint32_t it) {
         const int sc = it % NC;
-        ok = ok && mbar_wait(&c_full[sc], (it / NC) & 1, p.err);
+        ok = ok && mbar_wait_each(&c_full[sc], (it / NC) & 1, p.err);
         const uint8_t* src = sm + C_OFF + sc * C_BYTES;
 #pragma unroll
         for (int h = 0; h < N; ++h) {
@@ -472,7 +473,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           e[h] = byte[h];
         }
         if (it + 1 < end) fetch(it + 1);
-        if (it >= NA) ok = ok && mbar_wait(&a_empty[(it - NA) % NE], ((it - NA) / NE) & 1, p.err);
+        if (it >= NA)
+          ok = ok && mbar_wait_each(&a_empty[(it - NA) % NE], ((it - NA) / NE) & 1, p.err);
         uint8_t* dst = sm + it % NA * A_BYTES;
 #pragma unroll
         for (int h = 0; h < N; ++h) {

@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const long long r = first + it * G;
     float tok = 0.f;
     if (p.gate == LAGA_GATE_TOKEN) tok = to_f32(static_cast<const T*>(p.x.gate)[r]);
-    ok = ok && mbar_wait(&ring.bar[stage], phase, p.x.err);
+    ok = ok && mbar_wait_each(&ring.bar[stage], phase, p.x.err);
     const uint8_t* buf = ring.buf + stage * q.stage_bytes;
     const uint8_t *bx = buf + q.src[F_X].off, *by = buf + q.src[F_Y].off, *bg = buf + q.src[F_G].off;
     V8 x[NV];
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (p.gate == LAGA_GATE_TOKEN) tok = to_f32(static_cast<const T*>(p.x.gate)[r]);
     if (p.pre) st_pre = reinterpret_cast<const float2*>(p.x.stat_pre)[r];
     if (p.post) st_post = reinterpret_cast<const float2*>(p.x.stat_post)[r];
-    ok = ok && mbar_wait(&ring.bar[stage], phase, p.x.err);
+    ok = ok && mbar_wait_each(&ring.bar[stage], phase, p.x.err);
     const uint8_t* buf = ring.buf + stage * q.stage_bytes;
     const uint8_t *bd = buf + q.src[B_D].off, *bh = buf + q.src[B_DH].off;
     const uint8_t *bx = buf + q.src[B_X].off, *by = buf + q.src[B_Y].off, *bg = buf + q.src[B_G].off;

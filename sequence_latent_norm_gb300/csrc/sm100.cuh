@@ -66,10 +66,35 @@ constexpr uint32_t kWaitPolls = 1u << 22;
 
 // Bounded wait for the phase with the given parity to complete.  Returns
 // false (and records a timeout in *err) if it never completes.
+//
+// The lanes of a warp that wait in one call poll and leave together: where one
+// saw the phase complete at the last poll and another did not, the first would
+// be left alone at the warp's next collective instruction.  (A lane that gets
+// through at the first probe needs no vote: the phase is complete, so everyone's
+// next poll says so.)
 LAGA_DEVINL bool mbar_wait(uint64_t* bar, uint32_t parity, int* err) {
   // Phase already complete: one probe, no loop (the common case on the
   // issue paths, where a few hundred cycles per wait show up as tensor-core
   // idle time).
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t together = __activemask();
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    const bool seen = mbar_try_wait(bar, parity);
+    if (__any_sync(together, seen)) {
+      if (!seen) mbar_try_wait(bar, parity);   // complete now: this lane's own acquire
+      return true;
+    }
+    if (i > kSpinPolls) __nanosleep(256);
+  }
+  if (err) atomicExch(err, DEV_ERR_TIMEOUT);
+  return false;
+}
+
+// The same without votes, each lane for itself: for one lane's wait, and for
+// warps whose lanes go through the same code whatever the answer.  (The weight
+// gradient from checkpoints, a chain of short waits, is 4 to 9 % slower with
+// them; the attention kernels are not.)
+LAGA_DEVINL bool mbar_wait_each(uint64_t* bar, uint32_t parity, int* err) {
   if (mbar_try_wait(bar, parity)) return true;
   for (uint32_t i = 0; i < kWaitPolls; ++i) {
     if (mbar_try_wait(bar, parity)) return true;

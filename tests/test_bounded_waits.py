@@ -19,7 +19,7 @@ def whole_warp_waits(path):
     one lane's."""
     src = re.sub(r"//[^\n]*", "", open(path).read())
     out, blocks, text = [], [], ""
-    for m in re.finditer(r"[{};]|mbar_wait(?:_cluster)?\(|[^{};]", src):
+    for m in re.finditer(r"[{};]|mbar_wait(?:_each|_cluster)?\(|[^{};]", src):
         t = m.group()
         if t == "{":
             blocks.append(text)
@@ -45,7 +45,7 @@ def test_lanes_that_gave_up_stay_with_their_warp(name):
 @pytest.mark.parametrize("name,issue,landed", [
     ("checkpoint_dw.cu", r"tma_load_3d_pair\(", r"wait_landed\(b_full, it, p\.err\);"),
     ("checkpoint_dw.cu", r"tma_load_2d\(", r"wait_landed\(c_full, it, p\.err\);"),
-    ("checkpoint_dw.cu", r"mma_ss_pair\(", r"mbar_wait\(&mma_done, 0, p\.err\);")])
+    ("checkpoint_dw.cu", r"mma_ss_pair\(", r"mbar_wait_each\(&mma_done, 0, p\.err\);")])
 def test_what_is_in_flight_is_waited_for(name, issue, landed):
     """A kernel does not leave its shared memory to copies or products that it
     has in flight, also where a wait gave up: behind the code that issues them
@@ -53,3 +53,15 @@ def test_what_is_in_flight_is_waited_for(name, issue, landed):
     src = open(os.path.join(CSRC, name)).read()
     first = re.search(issue, src)
     assert first and re.search(landed, src[first.end():]), name
+
+
+@pytest.mark.parametrize("name", ["attn_fwd.cu", "attn_bwd_dq.cu", "attn_bwd_kv.cu", "gemm_tc.cu"])
+def test_lanes_that_leave_leave_together(name):
+    """Kernels whose warps leave a loop on a wait's answer take the wait that
+    votes on every poll."""
+    waits = whole_warp_waits(os.path.join(CSRC, name))
+    assert waits and all(text.endswith("mbar_wait(") for _, text in waits)
+    wait = re.search(r"bool mbar_wait\(.*?\n}\n", open(os.path.join(CSRC, "sm100.cuh")).read(),
+                     re.S).group()
+    loop = re.search(r"for \(uint32_t i = 0; i < kWaitPolls; \+\+i\) \{(.*)\n  \}\n", wait, re.S).group(1)
+    assert re.findall(r"if \((.*)\) \{\n[^}]*return true;", loop) == ["__any_sync(together, seen)"]
