@@ -153,7 +153,7 @@ class LagaAttentionBlock:
 
 
 class LagaResidualStack:
-    """Attention blocks on a residual stream x [B, S_r, d_model]:
+    """Attention blocks on a residual stream x [B, S_r, d_model] (contiguous):
 
         h_l = N_pre(x_l) gamma_pre,  y_l = block_l(h_l),
         x_{l+1} = x_l + alpha s N_post(y_l) gamma_post
@@ -162,7 +162,9 @@ class LagaResidualStack:
     a plain gated residual add) and gate as for ResidualNorm.  ``ckpt`` holds
     the normalised x and y of every layer as 8-bit checkpoints; the one of x
     also serves the layer's dW_q and dW_kv_a, so neither x nor h is held in
-    the I/O type."""
+    the I/O type.  Gate logits are given as tensors and their gradients given
+    back; a gate that is computed from x or h on the way needs ResidualNorm in
+    the caller's own loop."""
 
     def __init__(self, blocks, d_model: int, *, norm_pre: str = "rms", norm_post: str = "none",
                  gate: str = "none", ckpt: bool = False, io_dtype: str = "bf16", eps: float = 1e-5,

@@ -27,6 +27,8 @@ template <typename T>
 LAGA_DEVINL void st1(void* p, long long i, float v) { static_cast<T*>(p)[i] = from_f32<T>(v); }
 
 // ---------------------------------------------------- rows of any width
+// (what the ring kernels do not take: widths that are no multiple of 8, and
+// fp32 backwards too wide for a ring)
 // One CTA per row, one element per access, the row's fp32 values in shared
 // memory between the passes, and the backward's column sums beside them over
 // all rows of a CTA.  Warp w owns the 128-channel groups w, w + GT / 32, ...,
@@ -273,9 +275,9 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // Rows of any width: 2048 threads an SM (32 registers each), which hide the
 // latency of the scalar accesses, in CTAs of 256 threads, or of 1024 where
 // shared memory does not hold `arrays` fp32 rows for eight CTAs.  With 41
-// registers and so fewer threads the forward took 110 us instead of 86 (4096 x
+// registers and so fewer threads the forward took 110 us instead of 87 (4096 x
 // 5001 bf16), and with 256 threads throughout, the sums in global memory, the
-// backward 443 us instead of 294.
+// backward 443 us instead of 297.
 bool rows_wide(int d, int arrays) { return arrays * d * 4 + 2048 > 220 * 1024 / 8; }
 int rows_ctas(int d, int arrays) {
   return std::max(1, std::min(rows_wide(d, arrays) ? 2 : 8, 220 * 1024 / (arrays * d * 4 + 2048)));

@@ -1,5 +1,5 @@
 // What the residual-stream kernels share (residual.cu: rows of any width;
-// residual_ring.cu: rows of a multiple of 8 channels).
+// residual_ring.cu: rows of a multiple of 8 channels that fit its rings).
 #pragma once
 
 #include "ckpt8.cuh"

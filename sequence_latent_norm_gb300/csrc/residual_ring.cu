@@ -1,7 +1,16 @@
 // The residual stream for rows of a multiple of 8 channels (the formulas are
-// in residual.cu).  All of it is bound by HBM: per element a bf16 junction
-// with a full gate moves 10 bytes forward and, from 8-bit checkpoints, 12
-// backward, against 36 and 73 instructions (d = 7168).
+// in residual.cu) whose tensors fit shared memory together, one row of each:
+// all but an fp32 backward of both halves with a full gate and no checkpoints
+// above 11520 channels, which residual.cu takes.
+//
+// Per element a bf16 junction with a full gate moves 10 bytes forward and, from
+// 8-bit checkpoints, 12 backward, against 36 and 73 instructions (d = 7168).
+// The forward is bound by HBM (16384 x 7168: 195 us, 0.89 of the measured
+// rate), the backward by the latency of its one team an SM, which meets twice a
+// row with nothing to overlap (379 us, 0.64 of the rate, 1.96 of 4 instructions
+// a cycle).  Above 8192 channels a thread of the backward holds four vectors and
+// spills some 450 bytes: 4096 rows from checkpoints take 111 us at 8192
+// channels, 226 us at 8200 and 355 us at 16384.
 //
 // A CTA of 512 threads per SM is cut into teams; a team walks rows, one at a
 // time, and each team has a ring of row buffers in shared memory that one
@@ -122,7 +131,7 @@ LAGA_DEVINL void team_sync(int team) {
 // the largest team and several values: the lanes of a warp share the values
 // out first (lane l ends up with value l mod K) and then the warps' sums, ~30
 // instructions instead of ~120 for four values, in a longer chain.  The
-// 7168-channel backward takes 378 us with it and 410 us without; at 4096
+// 7168-channel backward takes 379 us with it and 410 us without; at 4096
 // channels (8 warps) it takes 61 us with it and 58 us without.
 template <int TEAM, int K>
 LAGA_DEVINL void team_sum(float (&v)[K], float (*red)[THREADS / 32][4], int team, int& slot) {
@@ -466,7 +475,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // Teams up to 256 threads keep x^ and y^ from one pass over the row to the
     // next (16384 x 2048 from checkpoints: 97 us, 102 us decoding in every
     // pass); for the one large team of a CTA the registers do not reach, and
-    // keeping them took a fifth longer than decoding again (378 us at 16384 x
+    // keeping them took a fifth longer than decoding again (379 us at 16384 x
     // 7168).
     constexpr bool KEEP = TEAM < 512;
     V8 hat[KEEP ? NV : 1];

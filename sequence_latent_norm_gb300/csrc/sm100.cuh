@@ -67,8 +67,8 @@ constexpr uint32_t kWaitPolls = 1u << 22;
 // Bounded wait for the phase with the given parity to complete.  Returns
 // false (and records a timeout in *err) if it never completes.
 //
-// The lanes of a warp that wait in one call poll and leave together: where one
-// saw the phase complete at the last poll and another did not, the first would
+// The lanes of a warp that wait in one call, for the same phase of the same
+// barrier, poll and leave together: where one saw the phase complete at the last poll and another did not, the first would
 // be left alone at the warp's next collective instruction.  (A lane that gets
 // through at the first probe needs no vote: the phase is complete, so everyone's
 // next poll says so.)
