@@ -218,11 +218,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
   // Each CTA's: c_full, c_empty (codes), a_empty, b_empty, acc_full (the pair
-  // MMAs' commits arrive in both), mma_done.  a_full: an arrival of every decoder warp,
+  // MMAs' commits arrive in both).  a_full: an arrival of every decoder warp,
   // and in rank 0 one that says that rank 1's is complete.  Rank 0's: b_full
   // (both CTAs' dy bytes), acc_empty (epilogue warps of both).
   __shared__ uint64_t c_full[NC], c_empty[NC], a_full[NE], a_empty[NE], b_full[NB], b_empty[NB];
-  __shared__ uint64_t acc_full[2], acc_empty[2], mma_done;
+  __shared__ uint64_t acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -246,7 +246,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 16);
     }
-    mbar_init(&mma_done, 1);
     fence_barrier_init();
   }
   if (warp == 3) {
@@ -359,9 +358,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           mma_commit_pair(&acc_full[buf]);
         }
       }
-      // the MMAs are done before the pair's shared memory and TMEM are left
-      mma_commit_pair(&mma_done);
-      mbar_wait_each(&mma_done, 0, p.err);
+      // The MMAs, whose last commit covers them all, are done before the pair's
+      // shared memory and TMEM are left, also where the epilogue gave up.
+      if (ic > 0) mbar_wait_each(&acc_full[(ic - 1) & 1], ((ic - 1) >> 1) & 1, p.err);
     }
   } else if (warp < W_DEC) {
     // Rank 1's warps 2 and 3, a step each in turn: announce the decoded tile
@@ -380,14 +379,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // this warp: 32 channels (TMEM lanes) and half of the tile's columns
     const int q = warp & 3, c0 = ((warp - W_EPI) >> 2) * HALF;
     uint32_t ic = 0;
-    bool ok = true;
+    uint32_t polls = kWaitPolls;
     while (w.next(p, pair)) {
       float2 acc[HALF / 2];
 #pragma unroll
       for (int j = 0; j < HALF / 2; ++j) acc[j] = make_float2(0.f, 0.f);
       for (int k0 = 0; k0 < w.kn; k0 += p.chain, ++ic) {
         const int buf = ic & 1;
-        ok = ok && mbar_wait_each(&acc_full[buf], (ic >> 1) & 1, p.err);
+        mbar_wait_or_pass(&acc_full[buf], (ic >> 1) & 1, polls, p.err);
         tc_fence_after();
 #pragma unroll
         for (int j = 0; j < HALF / 16; ++j) {
@@ -400,11 +399,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive_cluster(smem_cluster_addr(&acc_empty[buf], 0));
+        if (lane == 0 && polls) mbar_arrive_cluster(smem_cluster_addr(&acc_empty[buf], 0));
       }
       const int r = (int)rank * CK_GROUP + channel_of(q * 32 + lane);   // row of the pair's tile
       const int row = (w.t / p.n_tiles) * 256 + r, n0 = (w.t % p.n_tiles) * BN + c0;
-      if (ok && row < p.d) {
+      if (polls && row < p.d) {
         const float gain = p.gamma ? p.gamma[row] : 1.f;
         float* dst = w.frag >= 0 ? p.frag + ((long long)w.frag * 256 + r) * BN + c0
                                  : p.dw + (long long)row * p.n + n0;
@@ -449,13 +448,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     uint4 v[N];
     uint32_t byte[N];
     uint32_t base = 0;   // steps before this piece
-    bool ok = true;
+    uint32_t polls = kWaitPolls;
     while (w.next(p, pair)) {
       const int g = ((w.t / p.n_tiles) * 2 + (int)rank) & 15;
       const uint32_t end = base + w.kn;
       auto fetch = [&](uint32_t it) {
         const int sc = it % NC;
-        ok = ok && mbar_wait_each(&c_full[sc], (it / NC) & 1, p.err);
+        mbar_wait_or_pass(&c_full[sc], (it / NC) & 1, polls, p.err);
         const uint8_t* src = sm + C_OFF + sc * C_BYTES;
 #pragma unroll
         for (int h = 0; h < N; ++h) {
@@ -474,7 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         if (it + 1 < end) fetch(it + 1);
         if (it >= NA)
-          ok = ok && mbar_wait_each(&a_empty[(it - NA) % NE], ((it - NA) / NE) & 1, p.err);
+          mbar_wait_or_pass(&a_empty[(it - NA) % NE], ((it - NA) / NE) & 1, polls, p.err);
         uint8_t* dst = sm + it % NA * A_BYTES;
 #pragma unroll
         for (int h = 0; h < N; ++h) {
@@ -489,7 +488,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // The codes are given back only here, where what was made of them has
         // been stored: an arrival can overtake loads that are still queued,
         // and the next codes then come in under them.
-        if (ok && lane == 0) {
+        if (lane == 0 && polls) {
           mbar_arrive(&c_empty[it % NC]);
           mbar_arrive(&a_full[it % NE]);
         }

@@ -91,9 +91,7 @@ LAGA_DEVINL bool mbar_wait(uint64_t* bar, uint32_t parity, int* err) {
 }
 
 // The same without votes, each lane for itself: for one lane's wait, and for
-// warps whose lanes go through the same code whatever the answer.  (The weight
-// gradient from checkpoints, a chain of short waits, is 4 to 9 % slower with
-// them; the attention kernels are not.)
+// warps whose lanes go through the same code whatever the answer.
 LAGA_DEVINL bool mbar_wait_each(uint64_t* bar, uint32_t parity, int* err) {
   if (mbar_try_wait(bar, parity)) return true;
   for (uint32_t i = 0; i < kWaitPolls; ++i) {
@@ -102,6 +100,22 @@ LAGA_DEVINL bool mbar_wait_each(uint64_t* bar, uint32_t parity, int* err) {
   }
   if (err) atomicExch(err, DEV_ERR_TIMEOUT);
   return false;
+}
+
+// For warps whose lanes go through the same code whatever the answer, and have
+// nothing to ask before they wait: `polls`, kWaitPolls at first, is how long a
+// lane still waits, and 0 once one of its waits gave up.  (The weight gradient
+// from checkpoints is a chain of short waits: with votes it is 4 to 9 % slower,
+// with a flag that is asked before every wait 1 to 2 %; the attention kernels
+// gain nothing from either.)
+LAGA_DEVINL void mbar_wait_or_pass(uint64_t* bar, uint32_t parity, uint32_t& polls, int* err) {
+  if (mbar_try_wait(bar, parity)) return;
+  for (uint32_t i = 0; i < polls; ++i) {
+    if (mbar_try_wait(bar, parity)) return;
+    if (i > kSpinPolls) __nanosleep(256);
+  }
+  if (polls && err) atomicExch(err, DEV_ERR_TIMEOUT);
+  polls = 0;
 }
 
 // 2^x with the hardware approximation (MUFU.EX2; flushes subnormals).

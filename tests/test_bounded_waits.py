@@ -19,7 +19,7 @@ def whole_warp_waits(path):
     one lane's."""
     src = re.sub(r"//[^\n]*", "", open(path).read())
     out, blocks, text = [], [], ""
-    for m in re.finditer(r"[{};]|mbar_wait(?:_each|_cluster)?\(|[^{};]", src):
+    for m in re.finditer(r"[{};]|mbar_wait(?:_each|_or_pass|_cluster)?\(|[^{};]", src):
         t = m.group()
         if t == "{":
             blocks.append(text)
@@ -38,14 +38,15 @@ def whole_warp_waits(path):
 def test_lanes_that_gave_up_stay_with_their_warp(name):
     waits = whole_warp_waits(os.path.join(CSRC, name))
     assert waits
-    left = [(line, text) for line, text in waits if not re.search(r"\bok = ok && mbar_wait", text)]
+    stays = r"\bok = ok && mbar_wait_each\($|^(if \([^()]*\) )?mbar_wait_or_pass\($"
+    left = [(line, text) for line, text in waits if not re.search(stays, text)]
     assert not left, f"{name}: these waits decide where their lane goes on: {left}"
 
 
 @pytest.mark.parametrize("name,issue,landed", [
     ("checkpoint_dw.cu", r"tma_load_3d_pair\(", r"wait_landed\(b_full, it, p\.err\);"),
     ("checkpoint_dw.cu", r"tma_load_2d\(", r"wait_landed\(c_full, it, p\.err\);"),
-    ("checkpoint_dw.cu", r"mma_ss_pair\(", r"mbar_wait_each\(&mma_done, 0, p\.err\);")])
+    ("checkpoint_dw.cu", r"mma_ss_pair\(", r"if \(ic > 0\) mbar_wait_each\(&acc_full\[")])
 def test_what_is_in_flight_is_waited_for(name, issue, landed):
     """A kernel does not leave its shared memory to copies or products that it
     has in flight, also where a wait gave up: behind the code that issues them
