@@ -8,8 +8,10 @@ exact in bf16.  :func:`pack8` makes one, ``unpack`` reads it back and
 
 ``stream`` (a torch.cuda.Stream; None: the current one) is where a call runs
 and what its outputs' memory belongs to.  The caller orders it behind the work
-that makes the inputs, and other streams behind the call; the inputs
-themselves may be dropped as soon as the call returns.
+that makes the inputs, and other streams behind the call.  With a stream given,
+the inputs may be dropped as soon as the call returns, whichever stream their
+memory belongs to; without one that holds for memory of the current stream, as
+for torch's own operators.
 """
 
 from __future__ import annotations

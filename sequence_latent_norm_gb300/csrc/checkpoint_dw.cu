@@ -26,7 +26,7 @@
 // stays whole: if it left, lanes whose wait had just succeeded would be stuck.
 //
 // A step is 128 tokens.  Every hand-over between warps costs a few hundred
-// clocks, whatever the step's size: 16384 x 7168 x 1536 takes 308 us with steps
+// clocks, whatever the step's size: 16384 x 7168 x 1536 takes 306 us with steps
 // of 128 tokens and 377 us with 64 (the rings as deep in tokens).  What bounds
 // it is that chain of hand-overs (codes, decoded tile, MMAs, and back) over
 // the three v tiles that shared memory holds: without its decoding it takes
@@ -600,7 +600,7 @@ DwPlan dw_plan(int rows, int d, int n, bool fp32) {
   DwPlan pl;
   // Columns per tile: a step costs MMA time in proportion to BN, and no less
   // than a tile of 128 columns, which the decoders set the pace of; ties go to
-  // the wider tile (1536 columns: 308 us in tiles of 256, 374 us of 192; 576
+  // the wider tile (1536 columns: 306 us in tiles of 256, 374 us of 192; 576
   // columns fit three tiles of 192).
   long long best = -1;
   for (const int bn : {256, 192, 128}) {

@@ -70,7 +70,7 @@ def test_stack_weight_gradients_are_of_the_checkpoint_and_its_gain(layer):
     """dW_q and dW_kv_a of a layer are diag(gamma_pre) v^T dy of the values v
     that its checkpoint stands for and the gradients that its block's compute
     gives: within the weight gradient's own bound, (rows + 64) 2^-23 of the
-    terms' magnitudes, where a gain left out would move them by 0.2 of it."""
+    terms' magnitudes, which they pass nearly everywhere without the gain."""
     laga = _laga()
     from sequence_latent_norm_gb300.block import LagaAttentionBlock, LagaResidualStack
     n, d_model = 2, 192
