@@ -253,8 +253,8 @@ laga_status laga_diag_mma_rate(int form, int n, int n_acc, int run, int n_instr,
 /* Static text for a status code. */
 const char* laga_status_string(laga_status status);
 
-/* Number of kernel launches the last laga_fwd, laga_bwd, laga_res_* or
- * laga_ckpt_* call on this host thread enqueued (0 after an error).  For
+/* Number of kernel launches the last laga_fwd, laga_bwd or laga_res_* call, or
+ * one on 8-bit rows or experts, on this host thread enqueued (0 after an error).  For
  * launch accounting. */
 int laga_last_launch_count(void);
 
@@ -398,6 +398,118 @@ size_t laga_ckpt_dw_workspace_bytes(int rows, int d, int n, laga_dtype dy_dtype)
 laga_status laga_ckpt_dw(int rows, int d, int n, laga_dtype dy_dtype, const void* ck,
                          const void* dy, const float* gamma, float* dw, void* ws,
                          size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Products of 8-bit operands, and experts.  An 8-bit weight is held in the
+ * checkpoints' row format, with one scale per block of 128 x 128, in two
+ * matrices with the same values: the rows of W^T ([n, laga_ckpt_row_bytes(k)],
+ * for y = v W) and the rows of W ([k, laga_ckpt_row_bytes(n)], for dx = dy W^T).
+ * The weights of several experts lie one behind the other.
+ *
+ * Experts' rows.  A router picks top_k of its experts for every token; the
+ * pairs (token t, choice j), numbered t top_k + j, are sorted by expert,
+ * pairs of one expert in their own order.  The rows of local expert e are
+ * start[e] .. start[e + 1] - 1; start[e] is a multiple of `align`, and the rows
+ * that this leaves between the experts belong to no pair.  Rows from
+ * start[local] on exist in the buffers and are never written, nor read for
+ * any output (but for pair, -1 there).
+ * ------------------------------------------------------------------------ */
+typedef enum { LAGA_SCORE_SIGMOID = 0, LAGA_SCORE_SOFTMAX = 1 } laga_score;
+
+typedef struct {
+  int tokens;            /* >= 0                                              */
+  int experts;           /* 1 .. 1024                                         */
+  int top_k;             /* 1 .. 32, no more than the chosen groups hold      */
+  int groups;            /* 1 .. 32 equal groups of neighbouring experts      */
+  int top_groups;        /* groups that a token may choose from               */
+  laga_score score;
+  int renormalise;       /* 1: a token's weights are divided by their sum     */
+  float scale;           /* factor of the weights, finite                     */
+  int first, local;      /* this rank's experts: first .. first + local - 1   */
+  int align;             /* 1, or 128 (the weight gradient needs that)        */
+  laga_dtype io_dtype;   /* logits and their gradient                         */
+} laga_route_dims;
+
+/* Rows that the pairs of `tokens` tokens can need (0 if the dims are invalid),
+ * and bytes of scratch of laga_route_fwd.  Host-only. */
+size_t laga_route_rows(const laga_route_dims* dims);
+size_t laga_route_workspace_bytes(const laga_route_dims* dims);
+
+/* Choice and weights.
+ *   s = sigmoid(logits) or softmax(logits);  c = s + bias (the bias chooses
+ *   only);  a group's score is the sum of its two best c;  of the top_groups
+ *   best groups the top_k best c are chosen;  of equal ones the lowest index.
+ *   weight = scale s, or scale s / (sum of the chosen s + 1e-20).
+ * The order is that of c in 64 bits.  An expert whose logit or bias is -inf is
+ * off; a choice that finds no expert on has expert -1 and weight 0.  A NaN
+ * (or +inf under a softmax) counts as off and makes the token's weights NaN.
+ *   logits [tokens, experts]; bias [experts] fp32 or NULL
+ *   expert [tokens, top_k] (output)   index among all experts, best first
+ *   weight [tokens, top_k] fp32 (output)
+ *   row    [tokens, top_k] (output)   the pair's row, -1: none on this rank
+ *   pair   [laga_route_rows] (output) the row's pair, -1: none
+ *   start  [local + 1] (output) */
+laga_status laga_route_fwd(const laga_route_dims* dims, const void* logits, const float* bias,
+                           int* expert, float* weight, int* row, int* pair, int* start, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* Gradient of the logits for dweight [tokens, top_k] fp32, at fixed choice.
+ * Choices of -1 take no part; an expert that `expert` holds twice counts twice. */
+laga_status laga_route_bwd(const laga_route_dims* dims, const void* logits, const int* expert,
+                           const float* dweight, void* dlogits, void* stream);
+
+/* w [experts, k, n] (dtype; 1 <= k, n <= 16384) in 8 bits: fwd [experts n,
+ * laga_ckpt_row_bytes(k)] and, unless NULL, bwd [experts k,
+ * laga_ckpt_row_bytes(n)].  A block that holds an infinity or a NaN stands
+ * for NaN. */
+laga_status laga_weight_pack(int experts, int k, int n, laga_dtype dtype, const void* w,
+                             void* fwd, void* bwd, void* stream);
+
+/* y[r, j] = sum_i a[r, i] b[e n + j, i] of 8-bit rows
+ *   a [rows, laga_ckpt_row_bytes(k)]; b [max(experts, 1) n, laga_ckpt_row_bytes(k)]
+ *   start [experts + 1] (device): row r is expert e's (see above); experts 0:
+ *   one matrix b for all rows, start ignored
+ *   y [rows, n] (output, out_dtype), 1 <= n <= 16384
+ * Products are exact, sums in fp32, in an order that the sizes fix. */
+size_t laga_mm8_workspace_bytes(int rows, int k, int n, int experts, laga_dtype out_dtype);
+laga_status laga_mm8(int rows, int k, int n, int experts, laga_dtype out_dtype, const void* a,
+                     const void* b, const int* start, void* y, void* ws, size_t ws_bytes,
+                     void* stream);
+
+/* laga_ckpt_dw by expert: dw [experts, d, n], expert e over its rows of v and
+ * dy; start[e] are multiples of 128, and rows that belong to no pair are zero
+ * in ck and dy, as the calls here leave them. */
+size_t laga_experts_dw_workspace_bytes(int rows, int d, int n, int experts, laga_dtype dy_dtype);
+laga_status laga_experts_dw(int rows, int d, int n, int experts, laga_dtype dy_dtype,
+                            const void* ck, const void* dy, const float* gamma, const int* start,
+                            float* dw, void* ws, size_t ws_bytes, void* stream);
+
+/* Rows of tokens in 8 bits, ck [tokens, row bytes of d], as experts' rows out
+ * [rows, .]; rows of no pair are zero.  end: device address of the number of
+ * rows in use, start + local. */
+laga_status laga_spread8(int rows, int tokens, int top_k, int d, const void* ck, const int* pair,
+                         const int* end, void* out, void* stream);
+
+/* out[t] = sum_j weight[t, j] y[row[t, j]], in fp32, j ascending; weight NULL:
+ * 1; a row of -1 adds nothing.  y [rows, d], out [tokens, d] (output). */
+laga_status laga_combine_fwd(int tokens, int top_k, int rows, int d, laga_dtype dtype,
+                             const void* y, const float* weight, const int* row, void* out,
+                             void* stream);
+
+/* Its gradients: dy [rows, d] (output; rows of no pair are zero) and, unless
+ * NULL, dweight [tokens, top_k] fp32 (output; y is needed for it alone). */
+laga_status laga_combine_bwd(int tokens, int top_k, int rows, int d, laga_dtype dtype,
+                             const void* dout, const void* y, const float* weight, const int* row,
+                             const int* pair, const int* end, void* dy, float* dweight,
+                             void* stream);
+
+/* a = silu(g) u of gu [rows, 2 f] = [g | u] as checkpoint rows ck [rows,
+ * laga_ckpt_row_bytes(f)], and its gradient dgu [rows, 2 f] for da [rows, f].
+ * end as for laga_spread8, or NULL: all rows. */
+laga_status laga_swiglu_fwd(int rows, int f, laga_dtype dtype, const void* gu, const int* end,
+                            void* ck, void* stream);
+laga_status laga_swiglu_bwd(int rows, int f, laga_dtype dtype, const void* gu, const void* da,
+                            const int* end, void* dgu, void* stream);
 
 /* Per-kernel timing for measurement.  While enabled, every kernel the
  * library launches is bracketed by two CUDA events recorded on its own

@@ -1,0 +1,198 @@
+"""fp64 oracle of routing, 8-bit products by expert, and the gated activation.
+
+Plain NumPy, written from the definitions in include/laga.h; shares no code
+with the CUDA path.  Test infrastructure only.
+"""
+
+import numpy as np
+
+from .residual import GROUP, E_MAX, E_MIN, pack, row_layout, unpack
+
+TINY = 1e-20
+
+
+# ------------------------------------------------------------------ routing
+def scores(logits, score):
+    """Scores of fp64 logits [T, E]; a token all of whose experts are off has zeros."""
+    if score == "sigmoid":
+        with np.errstate(over="ignore"):
+            return 1.0 / (1.0 + np.exp(-logits))
+    m = logits.max(axis=1, keepdims=True)
+    p = np.exp(logits - np.where(np.isfinite(m), m, 0.0))
+    z = p.sum(axis=1, keepdims=True)
+    return np.divide(p, z, out=np.zeros_like(p), where=z > 0)
+
+
+def best(v, n):
+    """Indices of the n largest of v, best first, the lowest of equal ones first;
+    -inf does not count."""
+    order = sorted(range(len(v)), key=lambda i: (-v[i], i))
+    return [i for i in order[:n] if v[i] > -np.inf]
+
+
+def choose(logits, bias, *, top_k, groups=1, top_groups=1, score="sigmoid", renormalise=True,
+           scale=1.0):
+    """(expert [T, k], weight [T, k]) of fp64 logits [T, E]."""
+    T, E = logits.shape
+    b = np.zeros(E) if bias is None else bias
+    nan = np.isnan(logits) | np.isnan(b)
+    if score == "softmax":
+        nan = nan | (logits == np.inf)
+    l = np.where(nan, -np.inf, logits)
+    s = scores(l, score)
+    c = np.where(l == -np.inf, -np.inf, s + np.where(np.isnan(b), 0.0, b))
+    expert, weight = np.full((T, top_k), -1, np.int32), np.zeros((T, top_k))
+    size = E // groups
+    for t in range(T):
+        row = c[t].copy()
+        if top_groups < groups:
+            total = []
+            for g in range(groups):
+                two = best(row[g * size:(g + 1) * size], 2)
+                total.append(sum(row[g * size + i] for i in two) if two else -np.inf)
+            keep = best(total, top_groups)
+            for g in range(groups):
+                if g not in keep:
+                    row[g * size:(g + 1) * size] = -np.inf
+        e = best(row, top_k)
+        expert[t, :len(e)] = e
+        w = s[t, e]
+        weight[t, :len(e)] = scale * (w / (w.sum() + TINY) if renormalise else w)
+        if nan[t].any():
+            weight[t, :len(e)] = np.nan
+    return expert, weight
+
+
+def order(expert, *, first=0, local, align, rows):
+    """(row, pair, start) of the choices: pairs of the local experts, by expert."""
+    T, k = expert.shape
+    row, pair = np.full(T * k, -1, np.int32), np.full(rows, -1, np.int32)
+    start = [0]
+    flat = expert.reshape(-1)
+    for e in range(first, first + local):
+        p = np.flatnonzero(flat == e)
+        at = start[-1] + np.arange(len(p))
+        row[p], pair[at] = at, p
+        start.append(start[-1] + -(-len(p) // align) * align)
+    return row.reshape(T, k), pair, np.array(start, np.int32)
+
+
+def route_bwd(logits, expert, dweight, *, score="sigmoid", renormalise=True, scale=1.0):
+    """Gradient of fp64 logits for the weights' dweight at fixed choice."""
+    s = scores(logits, score)
+    out = np.zeros_like(logits)
+    for t in range(len(logits)):
+        on = np.flatnonzero(expert[t] >= 0)
+        e, dw = expert[t, on], scale * dweight[t, on]
+        v = s[t, e]
+        if renormalise:
+            D = v.sum() + TINY
+            dv = dw / D - (dw * v).sum() / D ** 2
+        else:
+            dv = dw
+        ds = np.zeros(logits.shape[1])
+        np.add.at(ds, e, dv)
+        if score == "sigmoid":
+            with np.errstate(over="ignore"):
+                out[t] = ds * s[t] / (1.0 + np.exp(logits[t]))
+        else:
+            out[t] = s[t] * (ds - (ds * s[t]).sum())
+    return out
+
+
+# ------------------------------------------------------------------ 8 bits
+def pack_weight(w):
+    """(fwd, bwd) bytes of fp64 weights [E, K, N], one scale per 128 x 128 block."""
+    E, K, N = w.shape
+    ck, pk = row_layout(K)
+    cn, pn = row_layout(N)
+    g = np.zeros((E, ck, cn))
+    g[:, :K, :N] = w
+    fwd, bwd = np.zeros((E, N, pk), np.uint8), np.zeros((E, K, pn), np.uint8)
+    for e in range(E):
+        for i in range(0, ck, GROUP):
+            for j in range(0, cn, GROUP):
+                b = g[e, i:i + GROUP, j:j + GROUP]
+                # one group of 128 x 128 values: the row format's rule for a scale
+                m, x = np.frexp(np.abs(b).max()) if np.isfinite(b).all() else (0.0, 0)
+                x = x - 9 if m <= 448.0 / 512.0 else x - 8
+                x = E_MIN if m == 0 else min(max(x, E_MIN), E_MAX)
+                byte = x + 127 if np.isfinite(b).all() else 255
+                # codes: each value as a row of its own under that scale
+                unit = np.zeros((b.size, 2))
+                unit[:, 0] = np.where(np.isfinite(b), np.clip(b, -448.0 * 2.0 ** x, 448.0 * 2.0 ** x),
+                                      0.0).reshape(-1)
+                unit[:, 1] = 448.0 * 2.0 ** x
+                code = pack(unit)[:, 0].reshape(b.shape) if byte != 255 else np.zeros(b.shape, np.uint8)
+                ni, nj = min(GROUP, K - i), min(GROUP, N - j)
+                fwd[e, j:j + nj, i:i + GROUP] = code[:, :nj].T
+                fwd[e, j:j + nj, ck + i // GROUP] = byte
+                bwd[e, i:i + ni, j:j + GROUP] = code[:ni]
+                bwd[e, i:i + ni, cn + j // GROUP] = byte
+    return fwd.reshape(E * N, pk), bwd.reshape(E * K, pn)
+
+
+def mm8(a, b, k, n, start=None):
+    """y[r] = a[r] b_e^T of 8-bit rows, and the sum of the terms' magnitudes;
+    rows behind the last one in use are zero here."""
+    va, vb = unpack(a, k), unpack(b, k)
+    y, mag = np.zeros((len(a), n)), np.zeros((len(a), n))
+    for e in range(len(b) // n):
+        lo, hi = (0, len(a)) if start is None else (start[e], start[e + 1])
+        w = vb[e * n:(e + 1) * n]
+        y[lo:hi], mag[lo:hi] = va[lo:hi] @ w.T, np.abs(va[lo:hi]) @ np.abs(w).T
+    return y, mag
+
+
+def spread(buf, pair, top_k):
+    out = np.zeros((len(pair), buf.shape[1]), np.uint8)
+    out[pair >= 0] = buf[pair[pair >= 0] // top_k]
+    return out
+
+
+def weight_grad(buf, d, dy, start, gamma=None):
+    """dw [E, d, n], and the sum of the terms' magnitudes."""
+    v = unpack(buf, d) * (1.0 if gamma is None else gamma)
+    seg = [(start[e], start[e + 1]) for e in range(len(start) - 1)]
+    return (np.stack([v[a:b].T @ dy[a:b] for a, b in seg]),
+            np.stack([np.abs(v[a:b]).T @ np.abs(dy[a:b]) for a, b in seg]))
+
+
+# ------------------------------------------------------------------ rows back
+def combine(y, weight, row):
+    """out [T, d], and the sum of the terms' magnitudes."""
+    out, mag = (np.zeros((len(row), y.shape[1])) for _ in range(2))
+    for t in range(len(row)):
+        for j, r in enumerate(row[t]):
+            if r >= 0:
+                out[t] += weight[t, j] * y[r]
+                mag[t] += np.abs(weight[t, j] * y[r])
+    return out, mag
+
+
+def combine_bwd(dout, y, weight, row):
+    """(dy, dweight, sum of dweight's terms' magnitudes)."""
+    dy = np.zeros_like(y)
+    dw, mag = np.zeros(row.shape), np.zeros(row.shape)
+    for t in range(len(row)):
+        for j, r in enumerate(row[t]):
+            if r >= 0:
+                dy[r] = weight[t, j] * dout[t]
+                dw[t, j] = (dout[t] * y[r]).sum()
+                mag[t, j] = np.abs(dout[t] * y[r]).sum()
+    return dy, dw, mag
+
+
+# ------------------------------------------------------------------ activation
+def swiglu(gu):
+    f = gu.shape[1] // 2
+    with np.errstate(over="ignore"):
+        return gu[:, :f] / (1.0 + np.exp(-gu[:, :f])) * gu[:, f:]
+
+
+def swiglu_bwd(gu, da):
+    f = gu.shape[1] // 2
+    g, u = gu[:, :f], gu[:, f:]
+    with np.errstate(over="ignore"):
+        s, r = 1.0 / (1.0 + np.exp(-g)), 1.0 / (1.0 + np.exp(g))
+    return np.concatenate([da * u * s * (1.0 + g * r), da * g * s], axis=1)

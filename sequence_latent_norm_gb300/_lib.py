@@ -21,6 +21,7 @@ DTYPES = {"bf16": 0, "fp32": 1}
 NORMS = {"layer": 0, "rms": 1}
 POST_NORMS = {**NORMS, "none": 2}
 GATES = {"none": 0, "token": 1, "full": 2}
+SCORES = {"sigmoid": 0, "softmax": 1}
 WS_SAVED, WS_BWD, WS_FWD = 0, 1, 2
 
 EXPORTED = ("laga_workspace_bytes", "laga_workspace_tensor", "laga_fwd", "laga_fwd_scratch",
@@ -29,7 +30,11 @@ EXPORTED = ("laga_workspace_bytes", "laga_workspace_tensor", "laga_fwd", "laga_f
             "laga_profile_enable", "laga_profile_reset", "laga_profile_read",
             "laga_norm_rope_bwd_noalloc", "laga_selftest_wait_timeout", "laga_diag_mma_rate",
             "laga_res_fwd", "laga_res_bwd", "laga_res_workspace_bytes", "laga_ckpt_row_bytes",
-            "laga_ckpt_pack", "laga_ckpt_unpack", "laga_ckpt_dw", "laga_ckpt_dw_workspace_bytes")
+            "laga_ckpt_pack", "laga_ckpt_unpack", "laga_ckpt_dw", "laga_ckpt_dw_workspace_bytes",
+            "laga_route_rows", "laga_route_workspace_bytes", "laga_route_fwd", "laga_route_bwd",
+            "laga_weight_pack", "laga_mm8", "laga_mm8_workspace_bytes", "laga_experts_dw",
+            "laga_experts_dw_workspace_bytes", "laga_spread8", "laga_combine_fwd",
+            "laga_combine_bwd", "laga_swiglu_fwd", "laga_swiglu_bwd")
 
 
 class LagaDims(ctypes.Structure):
@@ -46,6 +51,13 @@ class LagaResDims(ctypes.Structure):
                 ("pre", ctypes.c_int), ("norm_post", ctypes.c_int), ("norm_pre", ctypes.c_int),
                 ("eps", ctypes.c_float), ("gate", ctypes.c_int), ("ckpt", ctypes.c_int),
                 ("io_dtype", ctypes.c_int)]
+
+
+class LagaRouteDims(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int), ("experts", ctypes.c_int), ("top_k", ctypes.c_int),
+                ("groups", ctypes.c_int), ("top_groups", ctypes.c_int), ("score", ctypes.c_int),
+                ("renormalise", ctypes.c_int), ("scale", ctypes.c_float), ("first", ctypes.c_int),
+                ("local", ctypes.c_int), ("align", ctypes.c_int), ("io_dtype", ctypes.c_int)]
 
 
 class LagaError(RuntimeError):
@@ -118,6 +130,18 @@ def load(path: str = LIB_PATH):
     lib.laga_ckpt_dw.restype = I
     lib.laga_ckpt_dw_workspace_bytes.argtypes = [I, I, I, I]
     lib.laga_ckpt_dw_workspace_bytes.restype = S
+    Q = ctypes.POINTER(LagaRouteDims)
+    for name, args in (("route_fwd", [Q] + [P] * 8 + [S, P]), ("route_bwd", [Q] + [P] * 5),
+                       ("weight_pack", [I] * 4 + [P] * 4), ("mm8", [I] * 5 + [P] * 5 + [S, P]),
+                       ("experts_dw", [I] * 5 + [P] * 6 + [S, P]), ("spread8", [I] * 4 + [P] * 5),
+                       ("combine_fwd", [I] * 5 + [P] * 5), ("combine_bwd", [I] * 5 + [P] * 9),
+                       ("swiglu_fwd", [I] * 3 + [P] * 4), ("swiglu_bwd", [I] * 3 + [P] * 5)):
+        f = getattr(lib, "laga_" + name)
+        f.argtypes, f.restype = args, I
+    for name, args in (("route_rows", [Q]), ("route_workspace_bytes", [Q]),
+                       ("mm8_workspace_bytes", [I] * 5), ("experts_dw_workspace_bytes", [I] * 5)):
+        f = getattr(lib, "laga_" + name)
+        f.argtypes, f.restype = args, S
     _lib = lib
     return lib
 
@@ -283,3 +307,89 @@ def ckpt_dw(rows, d, n, dy_dtype, ck, dy, gamma, dw, ws, ws_bytes, stream=0):
     """laga_ckpt_dw with raw device addresses (ints; gamma 0: no row gain)."""
     _check(load().laga_ckpt_dw(rows, d, n, DTYPES[dy_dtype], ck, dy, gamma, dw, ws, ws_bytes,
                                stream), "laga_ckpt_dw")
+
+
+def make_route_dims(tokens, experts, top_k, *, groups=1, top_groups=1, score="sigmoid",
+                    renormalise=True, scale=1.0, first=0, local=None, align=128,
+                    io_dtype="fp32") -> LagaRouteDims:
+    return LagaRouteDims(tokens, experts, top_k, groups, top_groups, SCORES[score],
+                         int(renormalise), scale, first, experts if local is None else local,
+                         align, DTYPES[io_dtype])
+
+
+def route_rows(dims: LagaRouteDims) -> int:
+    """Rows that the pairs can need (0: none, or invalid dims)."""
+    return int(load().laga_route_rows(ctypes.byref(dims)))
+
+
+def route_workspace_bytes(dims: LagaRouteDims) -> int:
+    return int(load().laga_route_workspace_bytes(ctypes.byref(dims)))
+
+
+def route_fwd(dims: LagaRouteDims, logits, bias, expert, weight, row, pair, start, ws, ws_bytes,
+              stream=0):
+    """laga_route_fwd with raw device addresses (ints; bias 0: none)."""
+    _check(load().laga_route_fwd(ctypes.byref(dims), logits, bias, expert, weight, row, pair,
+                                 start, ws, ws_bytes, stream), "laga_route_fwd")
+
+
+def route_bwd(dims: LagaRouteDims, logits, expert, dweight, dlogits, stream=0):
+    """laga_route_bwd with raw device addresses (ints)."""
+    _check(load().laga_route_bwd(ctypes.byref(dims), logits, expert, dweight, dlogits, stream),
+           "laga_route_bwd")
+
+
+def weight_pack(experts, k, n, dtype, w, fwd, bwd, stream=0):
+    """laga_weight_pack with raw device addresses (ints; bwd 0: not written)."""
+    _check(load().laga_weight_pack(experts, k, n, DTYPES[dtype], w, fwd, bwd, stream),
+           "laga_weight_pack")
+
+
+def mm8_workspace_bytes(rows, k, n, experts, out_dtype) -> int:
+    return int(load().laga_mm8_workspace_bytes(rows, k, n, experts, DTYPES[out_dtype]))
+
+
+def mm8(rows, k, n, experts, out_dtype, a, b, start, y, ws, ws_bytes, stream=0):
+    """laga_mm8 with raw device addresses (ints; experts 0: one matrix b)."""
+    _check(load().laga_mm8(rows, k, n, experts, DTYPES[out_dtype], a, b, start, y, ws, ws_bytes,
+                           stream), "laga_mm8")
+
+
+def experts_dw_workspace_bytes(rows, d, n, experts, dy_dtype) -> int:
+    return int(load().laga_experts_dw_workspace_bytes(rows, d, n, experts, DTYPES[dy_dtype]))
+
+
+def experts_dw(rows, d, n, experts, dy_dtype, ck, dy, gamma, start, dw, ws, ws_bytes, stream=0):
+    """laga_experts_dw with raw device addresses (ints; gamma 0: no row gain)."""
+    _check(load().laga_experts_dw(rows, d, n, experts, DTYPES[dy_dtype], ck, dy, gamma, start, dw,
+                                  ws, ws_bytes, stream), "laga_experts_dw")
+
+
+def spread8(rows, tokens, top_k, d, ck, pair, end, out, stream=0):
+    """laga_spread8 with raw device addresses (ints)."""
+    _check(load().laga_spread8(rows, tokens, top_k, d, ck, pair, end, out, stream),
+           "laga_spread8")
+
+
+def combine_fwd(tokens, top_k, rows, d, dtype, y, weight, row, out, stream=0):
+    """laga_combine_fwd with raw device addresses (ints; weight 0: ones)."""
+    _check(load().laga_combine_fwd(tokens, top_k, rows, d, DTYPES[dtype], y, weight, row, out,
+                                   stream), "laga_combine_fwd")
+
+
+def combine_bwd(tokens, top_k, rows, d, dtype, dout, y, weight, row, pair, end, dy, dweight,
+                stream=0):
+    """laga_combine_bwd with raw device addresses (ints; y and dweight 0: no dweight)."""
+    _check(load().laga_combine_bwd(tokens, top_k, rows, d, DTYPES[dtype], dout, y, weight, row,
+                                   pair, end, dy, dweight, stream), "laga_combine_bwd")
+
+
+def swiglu_fwd(rows, f, dtype, gu, end, ck, stream=0):
+    """laga_swiglu_fwd with raw device addresses (ints; end 0: all rows)."""
+    _check(load().laga_swiglu_fwd(rows, f, DTYPES[dtype], gu, end, ck, stream), "laga_swiglu_fwd")
+
+
+def swiglu_bwd(rows, f, dtype, gu, da, end, dgu, stream=0):
+    """laga_swiglu_bwd with raw device addresses (ints; end 0: all rows)."""
+    _check(load().laga_swiglu_bwd(rows, f, DTYPES[dtype], gu, da, end, dgu, stream),
+           "laga_swiglu_bwd")

@@ -147,10 +147,14 @@ def pack8(x: torch.Tensor, stream=None) -> Checkpoint8:
     return ck
 
 
-def weight_grad8(ck: Checkpoint8, dy: torch.Tensor, gamma=None, stream=None) -> torch.Tensor:
+def weight_grad8(ck: Checkpoint8, dy: torch.Tensor, gamma=None, stream=None, *,
+                 routes=None) -> torch.Tensor:
     """dW [d, n] fp32 = diag(gamma) v^T dy of the checkpointed activation v
     [rows, d] and dy [..., n] (bf16 or fp32, as many rows): the gradient of W
-    in (v gamma) W.  gamma [d] fp32 (it may start anywhere), or None for 1."""
+    in (v gamma) W.  gamma [d] fp32 (it may start anywhere), or None for 1.
+    With ``routes`` (a Routes of align 128) dW [experts, d, n], every expert's
+    over its own rows; rows of no pair must be zero in both, as spread8,
+    swiglu8 and combine_grad leave them."""
     if not isinstance(ck, Checkpoint8):
         raise TypeError("weight_grad8 takes a Checkpoint8")
     if not isinstance(dy, torch.Tensor) or dy.dtype not in IO_NAME:
@@ -161,13 +165,26 @@ def weight_grad8(ck: Checkpoint8, dy: torch.Tensor, gamma=None, stream=None) -> 
     dev, name = ck.device, IO_NAME[dy.dtype]
     dy_ptr = need(dy, "dy", dy.dtype, dev)
     g_ptr = 0 if gamma is None else need(gamma, "gamma", torch.float32, dev, (ck.d,))
-    with on_stream(dev, stream, ck.data, dy, gamma) as st:
-        dw = torch.empty(ck.d, n, dtype=torch.float32, device=dev)
-        nb = _lib.ckpt_dw_workspace_bytes(rows, ck.d, n, name)
+    start, lead = 0, ()
+    if routes is not None:
+        start, lead = routes.check(dev)[2], (routes.experts,)
+        if rows != routes.rows:
+            raise ValueError(f"dy has {rows} rows, the routes {routes.rows}")
+        if routes.align != 128:
+            raise ValueError(f"weight_grad8 by expert: routes of align {routes.align}, not 128")
+    with on_stream(dev, stream, ck.data, dy, gamma, routes and routes.start) as st:
+        dw = torch.empty(*lead, ck.d, n, dtype=torch.float32, device=dev)
+        nb = (_lib.experts_dw_workspace_bytes(rows, ck.d, n, routes.experts, name) if routes
+              else _lib.ckpt_dw_workspace_bytes(rows, ck.d, n, name))
         ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
         if g_ptr % 16:
             gamma = on_16(gamma)
             g_ptr = gamma.data_ptr()
-        _lib.ckpt_dw(rows, ck.d, n, name, ck.data.data_ptr(), dy_ptr, g_ptr, dw.data_ptr(),
-                     ws.data_ptr() if nb else 0, nb, st)
+        w_ptr = ws.data_ptr() if nb else 0
+        if routes is None:
+            _lib.ckpt_dw(rows, ck.d, n, name, ck.data.data_ptr(), dy_ptr, g_ptr, dw.data_ptr(),
+                         w_ptr, nb, st)
+        else:
+            _lib.experts_dw(rows, ck.d, n, routes.experts, name, ck.data.data_ptr(), dy_ptr, g_ptr,
+                            start, dw.data_ptr(), w_ptr, nb, st)
     return dw

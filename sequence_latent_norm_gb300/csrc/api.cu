@@ -495,6 +495,242 @@ laga_status laga_ckpt_dw(int rows, int d, int n, laga_dtype dy_dtype, const void
   });
 }
 
+// ------------------------------------------------------ 8-bit products, experts
+static bool width_ok(int d) { return d >= 1 && d <= CK_MAX_D; }
+static bool experts_ok(int n) { return n >= 0 && n <= ROUTE_MAX_EXPERTS; }
+
+size_t laga_route_rows(const laga_route_dims* dims) {
+  return route_check(dims) == LAGA_OK ? (size_t)route_rows(*dims) : 0;
+}
+size_t laga_route_workspace_bytes(const laga_route_dims* dims) {
+  return route_check(dims) == LAGA_OK ? route_ws_bytes(*dims) : 0;
+}
+
+laga_status laga_route_fwd(const laga_route_dims* dims, const void* logits, const float* bias,
+                           int* expert, float* weight, int* row, int* pair, int* start, void* ws,
+                           size_t ws_bytes, void* stream) {
+  t_launches = 0;
+  const laga_status s = route_check(dims);
+  if (s != LAGA_OK) return s;
+  const laga_route_dims d = *dims;
+  const bool some = d.tokens > 0;
+  const size_t need_bytes = route_ws_bytes(d);
+  PtrCheck c;
+  c.need(some, logits);
+  c.need(bias != nullptr, bias);
+  c.need(some, expert);
+  c.need(some, weight);
+  c.need(some, row);
+  c.need(some, pair);
+  c.need(true, start);
+  c.need(need_bytes > 0 && ws, ws);
+  if (c.status() != LAGA_OK) return c.status();
+  if (need_bytes > 0 && (!ws || ws_bytes < need_bytes)) return LAGA_ERR_WORKSPACE;
+  return run_launches("laga_route_fwd", [&] {
+    return cuda_status(launch_route_fwd(d, logits, bias, expert, weight, row, pair, start,
+                                        static_cast<unsigned char*>(ws),
+                                        static_cast<cudaStream_t>(stream)));
+  });
+}
+
+laga_status laga_route_bwd(const laga_route_dims* dims, const void* logits, const int* expert,
+                           const float* dweight, void* dlogits, void* stream) {
+  t_launches = 0;
+  const laga_status s = route_check(dims);
+  if (s != LAGA_OK) return s;
+  const laga_route_dims d = *dims;
+  PtrCheck c;
+  c.need(d.tokens > 0, logits);
+  c.need(d.tokens > 0, expert);
+  c.need(d.tokens > 0, dweight);
+  c.need(d.tokens > 0, dlogits);
+  if (c.status() != LAGA_OK) return c.status();
+  return run_launches("laga_route_bwd", [&] {
+    return cuda_status(launch_route_bwd(d, logits, expert, dweight, dlogits,
+                                        static_cast<cudaStream_t>(stream)));
+  });
+}
+
+laga_status laga_weight_pack(int experts, int k, int n, laga_dtype dtype, const void* w,
+                             void* fwd, void* bwd, void* stream) {
+  t_launches = 0;
+  if (experts < 1 || !experts_ok(experts) || !width_ok(k) || !width_ok(n) || !dtype_ok(dtype))
+    return LAGA_ERR_ARG;
+  PtrCheck c;
+  c.need(true, w);
+  c.need(true, fwd);
+  c.need(bwd != nullptr, bwd);
+  if (c.status() != LAGA_OK) return c.status();
+  return run_launches("laga_weight_pack", [&] {
+    return cuda_status(launch_weight_pack(experts, k, n, dtype == LAGA_FP32, w, fwd, bwd,
+                                          static_cast<cudaStream_t>(stream)));
+  });
+}
+
+static bool mm8_sizes_ok(int rows, int k, int n, int experts, laga_dtype dtype) {
+  return rows >= 0 && rows <= 0x7fffffff - 1024 && width_ok(k) && width_ok(n) &&
+         experts_ok(experts) && dtype_ok(dtype);
+}
+
+size_t laga_mm8_workspace_bytes(int rows, int k, int n, int experts, laga_dtype out_dtype) {
+  return mm8_sizes_ok(rows, k, n, experts, out_dtype)
+             ? mm8_ws_bytes(rows, k, n, experts, out_dtype == LAGA_FP32)
+             : 0;
+}
+
+laga_status laga_mm8(int rows, int k, int n, int experts, laga_dtype out_dtype, const void* a,
+                     const void* b, const int* start, void* y, void* ws, size_t ws_bytes,
+                     void* stream) {
+  t_launches = 0;
+  if (!mm8_sizes_ok(rows, k, n, experts, out_dtype)) return LAGA_ERR_ARG;
+  const bool fp32 = out_dtype == LAGA_FP32;
+  const size_t need_bytes = mm8_ws_bytes(rows, k, n, experts, fp32);
+  PtrCheck c;
+  c.need(rows > 0, a);
+  c.need(rows > 0, b);
+  c.need(rows > 0 && experts > 0, start);
+  c.need(rows > 0, y);
+  c.need(need_bytes > 0 && ws, ws);
+  if (c.status() != LAGA_OK) return c.status();
+  if (need_bytes > 0 && (!ws || ws_bytes < need_bytes)) return LAGA_ERR_WORKSPACE;
+  return run_launches("laga_mm8", [&] {
+    int* err = nullptr;
+    const laga_status e = err_word(&err);
+    return e != LAGA_OK ? e
+                        : cuda_status(launch_mm8(rows, k, n, experts, fp32, a, b, start, y,
+                                                 static_cast<unsigned char*>(ws), err,
+                                                 static_cast<cudaStream_t>(stream)));
+  });
+}
+
+static bool experts_dw_sizes_ok(int rows, int d, int n, int experts, laga_dtype dtype) {
+  return rows >= 0 && rows <= 0x7fffffff - 1024 && width_ok(d) && n >= 1 && n <= CK_MAX_N &&
+         experts >= 1 && experts_ok(experts) && dtype_ok(dtype);
+}
+
+size_t laga_experts_dw_workspace_bytes(int rows, int d, int n, int experts, laga_dtype dy_dtype) {
+  return experts_dw_sizes_ok(rows, d, n, experts, dy_dtype)
+             ? experts_dw_ws_bytes(rows, d, n, experts, dy_dtype == LAGA_FP32)
+             : 0;
+}
+
+laga_status laga_experts_dw(int rows, int d, int n, int experts, laga_dtype dy_dtype,
+                            const void* ck, const void* dy, const float* gamma, const int* start,
+                            float* dw, void* ws, size_t ws_bytes, void* stream) {
+  t_launches = 0;
+  if (!experts_dw_sizes_ok(rows, d, n, experts, dy_dtype)) return LAGA_ERR_ARG;
+  const bool fp32 = dy_dtype == LAGA_FP32;
+  const size_t need_bytes = experts_dw_ws_bytes(rows, d, n, experts, fp32);
+  PtrCheck c;
+  c.need(rows > 0, ck);
+  c.need(rows > 0, dy);
+  c.need(gamma != nullptr, gamma);
+  c.need(rows > 0, start);
+  c.need(true, dw);
+  c.need(need_bytes > 0 && ws, ws);
+  if (c.status() != LAGA_OK) return c.status();
+  if (need_bytes > 0 && (!ws || ws_bytes < need_bytes)) return LAGA_ERR_WORKSPACE;
+  return run_launches("laga_experts_dw", [&] {
+    int* err = nullptr;
+    const laga_status e = err_word(&err);
+    return e != LAGA_OK ? e
+                        : cuda_status(launch_experts_dw(rows, d, n, experts, fp32, ck, dy, gamma,
+                                                        start, dw,
+                                                        static_cast<unsigned char*>(ws), err,
+                                                        static_cast<cudaStream_t>(stream)));
+  });
+}
+
+static bool rows_ok(int tokens, int top_k, int rows) {
+  return tokens >= 0 && top_k >= 1 && top_k <= ROUTE_MAX_K && rows >= 0 &&
+         (long long)tokens * top_k <= 0x7fffffff;
+}
+
+laga_status laga_spread8(int rows, int tokens, int top_k, int d, const void* ck, const int* pair,
+                         const int* end, void* out, void* stream) {
+  t_launches = 0;
+  if (!rows_ok(tokens, top_k, rows) || !width_ok(d)) return LAGA_ERR_ARG;
+  PtrCheck c;
+  c.need(rows > 0 && tokens > 0, ck);
+  c.need(rows > 0, pair);
+  c.need(rows > 0, out);
+  if (c.status() != LAGA_OK) return c.status();
+  if (rows > 0 && !end) return LAGA_ERR_ARG;
+  return run_launches("laga_spread8", [&] {
+    return cuda_status(launch_spread8(rows, tokens, top_k, d, ck, pair, end, out,
+                                      static_cast<cudaStream_t>(stream)));
+  });
+}
+
+laga_status laga_combine_fwd(int tokens, int top_k, int rows, int d, laga_dtype dtype,
+                             const void* y, const float* weight, const int* row, void* out,
+                             void* stream) {
+  t_launches = 0;
+  if (!rows_ok(tokens, top_k, rows) || !width_ok(d) || !dtype_ok(dtype)) return LAGA_ERR_ARG;
+  PtrCheck c;
+  c.need(rows > 0 && tokens > 0, y);
+  c.need(weight != nullptr, weight);
+  c.need(tokens > 0, row);
+  c.need(tokens > 0, out);
+  if (c.status() != LAGA_OK) return c.status();
+  return run_launches("laga_combine_fwd", [&] {
+    return cuda_status(launch_combine_fwd(tokens, top_k, rows, d, dtype == LAGA_FP32, y, weight,
+                                          row, out, static_cast<cudaStream_t>(stream)));
+  });
+}
+
+laga_status laga_combine_bwd(int tokens, int top_k, int rows, int d, laga_dtype dtype,
+                             const void* dout, const void* y, const float* weight, const int* row,
+                             const int* pair, const int* end, void* dy, float* dweight,
+                             void* stream) {
+  t_launches = 0;
+  if (!rows_ok(tokens, top_k, rows) || !width_ok(d) || !dtype_ok(dtype)) return LAGA_ERR_ARG;
+  PtrCheck c;
+  c.need(tokens > 0, dout);
+  c.need(rows > 0 && dweight, y);
+  c.need(weight != nullptr, weight);
+  c.need(tokens > 0, row);
+  c.need(rows > 0, pair);
+  c.need(rows > 0, dy);
+  c.need(dweight != nullptr, dweight);
+  if (c.status() != LAGA_OK) return c.status();
+  if (rows > 0 && !end) return LAGA_ERR_ARG;
+  return run_launches("laga_combine_bwd", [&] {
+    return cuda_status(launch_combine_bwd(tokens, top_k, rows, d, dtype == LAGA_FP32, dout,
+                                          dweight ? y : nullptr, weight, row, pair, end, dy,
+                                          dweight, static_cast<cudaStream_t>(stream)));
+  });
+}
+
+laga_status laga_swiglu_fwd(int rows, int f, laga_dtype dtype, const void* gu, const int* end,
+                            void* ck, void* stream) {
+  t_launches = 0;
+  if (rows < 0 || !width_ok(f) || !dtype_ok(dtype)) return LAGA_ERR_ARG;
+  PtrCheck c;
+  c.need(rows > 0, gu);
+  c.need(rows > 0, ck);
+  if (c.status() != LAGA_OK) return c.status();
+  return run_launches("laga_swiglu_fwd", [&] {
+    return cuda_status(launch_swiglu_fwd(rows, f, dtype == LAGA_FP32, gu, end, ck,
+                                         static_cast<cudaStream_t>(stream)));
+  });
+}
+
+laga_status laga_swiglu_bwd(int rows, int f, laga_dtype dtype, const void* gu, const void* da,
+                            const int* end, void* dgu, void* stream) {
+  t_launches = 0;
+  if (rows < 0 || !width_ok(f) || !dtype_ok(dtype)) return LAGA_ERR_ARG;
+  PtrCheck c;
+  c.need(rows > 0, gu);
+  c.need(rows > 0, da);
+  c.need(rows > 0, dgu);
+  if (c.status() != LAGA_OK) return c.status();
+  return run_launches("laga_swiglu_bwd", [&] {
+    return cuda_status(launch_swiglu_bwd(rows, f, dtype == LAGA_FP32, gu, da, end, dgu,
+                                         static_cast<cudaStream_t>(stream)));
+  });
+}
+
 laga_status laga_selftest_wait_timeout(void* stream) {
   int* w = nullptr;
   laga_status s = err_word(&w);

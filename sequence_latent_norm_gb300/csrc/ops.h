@@ -39,4 +39,43 @@ cudaError_t launch_ckpt_dw(int rows, int d, int n, bool fp32, const void* ck, co
                            const float* gamma, float* dw, unsigned char* ws, int* err,
                            cudaStream_t st);
 
+// ---- routing and experts
+constexpr int ROUTE_MAX_EXPERTS = 1024, ROUTE_MAX_K = 32;
+
+laga_status route_check(const laga_route_dims* dims);
+long long route_rows(const laga_route_dims& d);
+size_t route_ws_bytes(const laga_route_dims& d);
+cudaError_t launch_route_fwd(const laga_route_dims& d, const void* logits, const float* bias,
+                             int* expert, float* weight, int* row, int* pair, int* start,
+                             unsigned char* ws, cudaStream_t st);
+cudaError_t launch_route_bwd(const laga_route_dims& d, const void* logits, const int* expert,
+                             const float* dweight, void* dlogits, cudaStream_t st);
+
+// `end`: device address of the number of rows in use (start[experts]).
+cudaError_t launch_spread8(int rows, int tokens, int top_k, int d, const void* ck, const int* pair,
+                           const int* end, void* out, cudaStream_t st);
+cudaError_t launch_combine_fwd(int tokens, int top_k, int rows, int d, bool fp32, const void* y,
+                               const float* weight, const int* row, void* out, cudaStream_t st);
+cudaError_t launch_combine_bwd(int tokens, int top_k, int rows, int d, bool fp32, const void* dout,
+                               const void* y, const float* weight, const int* row, const int* pair,
+                               const int* end, void* dy, float* dweight, cudaStream_t st);
+cudaError_t launch_swiglu_fwd(int rows, int f, bool fp32, const void* gu, const int* end, void* ck,
+                              cudaStream_t st);
+cudaError_t launch_swiglu_bwd(int rows, int f, bool fp32, const void* gu, const void* da,
+                              const int* end, void* dgu, cudaStream_t st);
+
+cudaError_t launch_weight_pack(int experts, int K, int N, bool fp32, const void* w, void* fwd,
+                               void* bwd, cudaStream_t st);
+size_t mm8_ws_bytes(int rows, int K, int N, int experts, bool fp32);
+cudaError_t launch_mm8(int rows, int K, int N, int experts, bool fp32, const void* a,
+                       const void* b, const int* start, void* y, unsigned char* ws, int* err,
+                       cudaStream_t st);
+
+// Weight gradient by expert: the rows of expert e are start[e] .. start[e + 1],
+// multiples of 128.
+size_t experts_dw_ws_bytes(int rows, int d, int n, int experts, bool fp32);
+cudaError_t launch_experts_dw(int rows, int d, int n, int experts, bool fp32, const void* ck,
+                              const void* dy, const float* gamma, const int* start, float* dw,
+                              unsigned char* ws, int* err, cudaStream_t st);
+
 }  // namespace laga
