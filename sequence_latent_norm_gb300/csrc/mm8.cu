@@ -1,0 +1,468 @@
+// Products of 8-bit rows on the tensor cores (include/laga.h: laga_mm8):
+//   y[r, j] = sum_i a[r, i] b[e n + j, i]
+// with e4m3 codes and one power-of-two scale per 128 of i on both sides.  The
+// block-scaled MMA (kind::mxf8f6f4) takes such scales itself, one UE8M0 byte
+// per 32 of i: the checkpoints' scale bytes are that format (b stands for
+// 2^(b - 127), 255 for NaN), and four neighbouring MMAs (K = 32) name the same
+// byte.  So codes and scales go from HBM to the tensor core as they are.
+//
+// M = columns of y (rows of b), N = rows of y (rows of a): a tile's N can be
+// any multiple of 32, so that experts with few rows, and single tokens, cost
+// what they need, and b, which is the larger operand then, is streamed through
+// full 256-row tiles.
+//
+// Persistent pairs of CTAs (two-CTA clusters, cta_group::2): CTA rank r holds
+// 128 of a tile's rows of b and half of its rows of a.  8 warps:
+//   0     TMA producer of codes         (ring of STAGES, K = 128 each)
+//   1     MMA issuer (rank 0), TMEM allocator
+//   2     scale loader: four stages' bytes of each row, a 32-bit word, into the
+//         32 x 128-bit layout that tcgen05.cp spreads over TMEM (ring of SF_SLOTS)
+//   4-7   epilogue: accumulator -> registers -> y (or, where K is split, fp32
+//         partial sums, which mm8_join adds up in order)
+// TMEM: two accumulators of up to 224 columns, so that one drains while the
+// other fills, and four sets of scales.
+#include <algorithm>
+
+#include "ckpt8.cuh"
+#include "common.cuh"
+#include "kernels.h"
+#include "ops.h"
+#include "sm100.cuh"
+#include "tmap.h"
+
+namespace laga {
+namespace {
+using namespace sm100;
+
+constexpr int KS = CK_GROUP;                 // codes of i per stage
+constexpr int FT = 256;                      // rows of b per tile
+constexpr int TN_MAX = 224;                  // rows of a per tile
+constexpr int STAGES = 6;
+constexpr int W_BYTES = 128 * KS, X_BYTES = TN_MAX / 2 * KS;
+constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
+constexpr int SF_SLOTS = 4, SF_BYTES = 3 * 512;   // 128 rows of b, 2 x 128 of a
+constexpr int SF_OFF = STAGES * STAGE_BYTES;
+constexpr int SMEM_BYTES = SF_OFF + SF_SLOTS * SF_BYTES + 1024;
+constexpr int THREADS = 256;
+constexpr int TMEM_COLS = 512, SF_COL = 2 * TN_MAX, SF_SETS = 4, SF_COLS = 16;
+static_assert(SF_COL + SF_SETS * SF_COLS <= TMEM_COLS, "tensor memory");
+// A set of scales is written again SF_SETS groups of 4 stages later.  By then
+// the MMAs that read it are done: the ring lets STAGES of them be in flight.
+static_assert((SF_SETS - 1) * 4 >= STAGES, "scales outlive the MMAs that read them");
+constexpr int PAIRS = 76;                    // one pair per two SMs
+constexpr int BAND = 8;                      // column tiles that run side by side
+constexpr int WMAX = ROUTE_MAX_EXPERTS;
+
+struct Maps {
+  CUtensorMap w, x;
+};
+struct Params {
+  int rows, n, experts;    // experts 0: one matrix
+  int tn;                  // rows of a per tile, a multiple of 32
+  int f_tiles;             // column tiles
+  int steps;               // stages of the whole K
+  int splits, split_steps; // pieces of K, stages of each
+  int pitch, cols;         // bytes of a row of a and b, of its codes
+  int bf16;
+  const uint8_t *a, *b;
+  const int* start;
+  void* y;                 // or the partial sums [splits, rows, n]
+  int* err;
+};
+
+// The experts' first rows, and the row tiles in front of each.
+struct Segments {
+  int start[WMAX + 1], tiles[WMAX + 1];
+};
+
+// A pair's tiles in turn: rows r0 .. r1 of expert e, column tile f, stages k0 ..
+struct Walk {
+  int t, e;                // next tile, and the expert of the last one
+  int r0, r1, f, k0, kn, z;
+
+  LAGA_DEVINL explicit Walk(int pair) : t(pair), e(0) {}
+  LAGA_DEVINL bool next(const Params& p, const Segments& s) {
+    const int per = p.f_tiles * p.splits, E = max(p.experts, 1);
+    while (e < E && t >= s.tiles[e + 1] * per) ++e;
+    if (e >= E) return false;
+    const int q = t - s.tiles[e] * per, tt = s.tiles[e + 1] - s.tiles[e];
+    z = q % p.splits;
+    const int u = q / p.splits;
+    const int band = u / (BAND * tt), fb = min(BAND, p.f_tiles - band * BAND);
+    const int v = u - band * BAND * tt;
+    f = band * BAND + v % fb;
+    r0 = s.start[e] + v / fb * p.tn;
+    r1 = min(s.start[e + 1], r0 + p.tn);
+    k0 = z * p.split_steps;
+    kn = min(p.split_steps, p.steps - k0);
+    t += gridDim.x >> 1;
+    return true;
+  }
+  // N of the tile's MMAs
+  LAGA_DEVINL int width() const { return (r1 - r0 + 31) / 32 * 32; }
+};
+
+// Block-scaled MMA: D (+)= (A scaleA) (B scaleB)^T, both CTAs of the pair.
+LAGA_DEVINL void mma_mx_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                             uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X"
+      " [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+// e4m3 operands, K-major, UE8M0 scales; `byte`: which of a scale word's four.
+LAGA_DEVINL uint32_t idesc_mx(int n, int byte) {
+  return (uint32_t)byte << 4 | (uint32_t)(n >> 3) << 17 | 1u << 23 | (uint32_t)(FT >> 4) << 24 |
+         (uint32_t)byte << 29;
+}
+// 32 x 128 bits of shared memory into 32 lanes x 4 columns, for all four
+// quadrants of lanes, in both CTAs (each from its own shared memory).
+LAGA_DEVINL void copy_scales_pair(uint32_t taddr, uint32_t saddr) {
+  const uint64_t desc = (uint64_t)(8u | 1u << 14) << 32 | ((saddr >> 4) & 0x3fffu);
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+
+// A thread that copies leaves when its last copies have landed.
+template <int N>
+LAGA_DEVINL void wait_landed(uint64_t (&full)[N], uint32_t it, int* err) {
+  for (uint32_t i = it > N ? it - N : 0; i < it; ++i)
+    mbar_wait_each(&full[i % N], (i / N) & 1, err);
+}
+
+template <typename T>
+LAGA_DEVINL void store_tile(const Params& p, const Walk& w, T* y, uint32_t acc, int q, int lane,
+                            int col0) {
+  const int j = col0 + lane;
+  const int n = w.r1 - w.r0;
+  T* dst = y + ((long long)w.z * p.rows + w.r0) * p.n + j;
+  for (int c0 = 0; c0 < n; c0 += 32) {
+    uint32_t u[32];
+    tmem_ld32(tmem_addr(acc, q, c0), u);
+    if (j < p.n) {
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        if (c0 + c < n) dst[(long long)(c0 + c) * p.n] = from_f32<T>(__uint_as_float(u[c]));
+    }
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    mm8_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  // full, sf_full, acc_empty: rank 0's, counting both CTAs; empty, sf_empty,
+  // acc_full: each CTA's, by the pair MMAs' commits
+  __shared__ uint64_t full[STAGES], empty[STAGES], sf_full[SF_SLOTS], sf_empty[SF_SLOTS];
+  __shared__ uint64_t acc_full[2], acc_empty[2];
+  __shared__ uint32_t tmem_sh;
+  __shared__ Segments seg;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < SF_SLOTS; ++i) {
+      mbar_init(&sf_full[i], 2);
+      mbar_init(&sf_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 8);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&tmem_sh, TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  if (warp == 2) {
+    // row tiles in front of each expert: a scan, 32 experts at a time
+    const int E = max(p.experts, 1);
+    int carry = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane;
+      int s = 0, t = 0;
+      if (e < E) {
+        s = p.experts ? min(p.start[e], p.rows) : 0;
+        t = p.experts ? min(p.start[e + 1], p.rows) : p.rows;
+      }
+      const int own = e < E && t > s ? (t - s + p.tn - 1) / p.tn : 0;
+      int sum = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      if (e < E) {
+        seg.start[e] = s;
+        seg.tiles[e] = carry + sum - own;
+        if (e == E - 1) {
+          seg.start[E] = t;
+          seg.tiles[E] = carry + sum;
+        }
+      }
+      carry += __shfl_sync(0xffffffffu, sum, 31);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // both CTAs' barriers exist before anything signals them
+  tc_fence_after();
+  const uint32_t tmem = tmem_sh;
+  Walk w(blockIdx.x >> 1);
+  const int half = p.tn / 2;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tm.w);
+      tma_prefetch_desc(&tm.x);
+      uint32_t it = 0;
+      bool ok = true;
+      while (ok && w.next(p, seg)) {
+        const int row_w = w.e * p.n + w.f * FT + (int)rank * 128;
+        const int row_x = w.r0 + (int)rank * (w.width() / 2);
+        for (int k = 0; k < w.kn; ++k, ++it) {
+          const int st = it % STAGES;
+          if (it >= STAGES && !mbar_wait_each(&empty[st], (it / STAGES - 1) & 1, p.err)) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = sm + st * STAGE_BYTES;
+          const uint32_t bar = smem_cluster_addr(&full[st], 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * (W_BYTES + half * KS));
+          tma_load_2d_pair(dst, &tm.w, bar, (w.k0 + k) * KS, row_w);
+          tma_load_2d_pair(dst + W_BYTES, &tm.x, bar, (w.k0 + k) * KS, row_x);
+        }
+      }
+      if (rank == 0) wait_landed(full, it, p.err);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      uint32_t it = 0, group = 0, tile = 0;
+      bool ok = true;
+      while (ok && w.next(p, seg)) {
+        const int buf = tile & 1;
+        if (tile >= 2 && !mbar_wait_cluster(&acc_empty[buf], ((tile >> 1) - 1) & 1, p.err)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(buf * TN_MAX);
+        const int n = w.width();
+        for (int k = 0; ok && k < w.kn; ++group) {
+          const int slot = group % SF_SLOTS;
+          if (!mbar_wait_cluster(&sf_full[slot], (group / SF_SLOTS) & 1, p.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sf = tmem + SF_COL + (uint32_t)(group % SF_SETS * SF_COLS);
+          const uint32_t src = smem_u32(sm + SF_OFF + slot * SF_BYTES);
+          copy_scales_pair(sf, src);
+          copy_scales_pair(sf + 4, src + 512);
+          if (n > 128) copy_scales_pair(sf + 8, src + 1024);
+          const int k1 = min(k + 4, w.kn);
+          for (int byte = 0; k < k1; ++k, ++byte, ++it) {
+            const int st = it % STAGES;
+            if (!mbar_wait_each(&full[st], (it / STAGES) & 1, p.err)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t wa = smem_u32(sm + st * STAGE_BYTES);
+            const uint32_t alo = sdesc_lo(wa, 16), blo = sdesc_lo(wa + W_BYTES, 16);
+            const uint32_t idesc = idesc_mx(n, byte);
+#pragma unroll
+            for (int kk = 0; kk < KS / 32; ++kk)
+              mma_mx_pair(d, sdesc_make(alo + kk * 2), sdesc_make(blo + kk * 2), idesc, sf, sf + 4,
+                          (k > 0 || kk > 0) ? 1u : 0u);
+            mma_commit_pair(&empty[st]);
+          }
+          mma_commit_pair(&sf_empty[slot]);
+        }
+        mma_commit_pair(&acc_full[buf]);
+        ++tile;
+      }
+      // the MMAs are done before the pair's shared memory and TMEM are left
+      if (tile > 0) mbar_wait_each(&acc_full[(tile - 1) & 1], ((tile - 1) >> 1) & 1, p.err);
+    }
+  } else if (warp == 2) {
+    // Lane l holds the words of rows l, l + 32, ... of each 128.  A lane whose
+    // wait gave up goes on without waiting and without telling anyone.
+    uint32_t group = 0;
+    uint32_t polls = kWaitPolls;
+    while (w.next(p, seg)) {
+      const int rows_b = max(p.experts, 1) * p.n;   // at most 2^24
+      const int row_w = w.e * p.n + w.f * FT + (int)rank * 128;
+      for (int k = 0; k < w.kn; k += 4, ++group) {
+        // k0 is a multiple of 4 stages: whole words of scale bytes
+        const uint32_t off = (uint32_t)(p.cols + w.k0 + k);
+        uint32_t v[12];
+#pragma unroll
+        for (int i = 0; i < 12; ++i) {
+          const long long r = i < 4 ? row_w + 32 * i + lane : w.r0 + 32 * (i - 4) + lane;
+          const bool in = i < 4 ? r < rows_b : r < w.r1;
+          v[i] = in ? *reinterpret_cast<const uint32_t*>((i < 4 ? p.b : p.a) + r * p.pitch + off)
+                    : 0u;
+        }
+        const int slot = group % SF_SLOTS;
+        if (group >= SF_SLOTS)
+          mbar_wait_or_pass(&sf_empty[slot], (group / SF_SLOTS - 1) & 1, polls, p.err);
+        uint4* dst = reinterpret_cast<uint4*>(sm + SF_OFF + slot * SF_BYTES) + lane;
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          dst[32 * i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && polls) mbar_arrive_cluster(smem_cluster_addr(&sf_full[slot], 0));
+      }
+    }
+  } else if (warp >= 4) {
+    const int q = warp & 3;
+    uint32_t polls = kWaitPolls;
+    for (uint32_t tile = 0; w.next(p, seg); ++tile) {
+      const int buf = tile & 1;
+      mbar_wait_or_pass(&acc_full[buf], (tile >> 1) & 1, polls, p.err);
+      tc_fence_after();
+      const uint32_t acc = tmem + (uint32_t)(buf * TN_MAX);
+      const int col0 = w.f * FT + (int)rank * 128 + q * 32;
+      if (p.bf16)
+        store_tile(p, w, static_cast<__nv_bfloat16*>(p.y), acc, q, lane, col0);
+      else
+        store_tile(p, w, static_cast<float*>(p.y), acc, q, lane, col0);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && polls) mbar_arrive_cluster(smem_cluster_addr(&acc_empty[buf], 0));
+    }
+  }
+  // neither CTA leaves while the pair's MMAs or the other CTA's arrivals may
+  // still touch its shared memory or TMEM
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, TMEM_COLS);
+  }
+  cluster_sync();
+}
+
+// The pieces of K added up in order.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    mm8_join_kernel(const float* __restrict__ part, T* __restrict__ y, const int* __restrict__ end,
+                    int rows, int n, int splits) {
+  const long long all = (long long)rows * n;
+  const long long used = (end ? (long long)min(rows, *end) : rows) * n;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < used; i += gridDim.x * 256LL) {
+    float s = part[i];
+    for (int z = 1; z < splits; ++z) s += part[z * all + i];
+    y[i] = from_f32<T>(s);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+struct Mm8Plan {
+  int tn, f_tiles, steps, splits, split_steps;
+};
+
+Mm8Plan mm8_plan(int rows, int K, int N, int experts) {
+  Mm8Plan pl{};
+  pl.f_tiles = (N + FT - 1) / FT;
+  pl.steps = ck_cols(K) / KS;
+  // Rows of a tile: the fewest clocks of the fullest pair, a stage costing its
+  // MMAs, or the bytes that it loads at about 45 a clock, or its issue.
+  const int used = experts ? std::min(experts, rows) : 1;
+  const int each = (rows + used - 1) / used;
+  double best = -1.0;
+  for (int tn = 32; tn <= TN_MAX; tn += 32) {
+    const long long tiles = (long long)used * ((each + tn - 1) / tn) * pl.f_tiles;
+    const long long turns = (tiles + PAIRS - 1) / PAIRS;
+    const double stage = std::max({2.0 * tn, (W_BYTES + tn / 2 * KS) / 45.0, 220.0});
+    const double cost = turns * (pl.steps * stage + 600.0);
+    if (best < 0 || cost < best) {
+      best = cost;
+      pl.tn = tn;
+    }
+  }
+  const long long tiles = (long long)used * ((each + pl.tn - 1) / pl.tn) * pl.f_tiles;
+  // Pieces of K where the tiles leave half of the pairs without work: whole
+  // words of scale bytes, 4 stages, at least
+  const int words = (pl.steps + 3) / 4;
+  int splits = 1;
+  if (2 * tiles <= PAIRS) splits = (int)std::min<long long>(PAIRS / tiles, words);
+  pl.split_steps = (words + splits - 1) / splits * 4;
+  pl.splits = (pl.steps + pl.split_steps - 1) / pl.split_steps;
+  return pl;
+}
+
+cudaError_t code_map(CUtensorMap* out, const void* base, uint64_t width, uint64_t rows,
+                     uint64_t pitch, uint32_t box_rows) {
+  auto enc = tmap_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {width, rows}, str[1] = {pitch};
+  const cuuint32_t box[2] = {KS, box_rows}, one[2] = {1, 1};
+  const CUresult r = enc(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, str,
+                         box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+size_t mm8_ws_bytes(int rows, int K, int N, int experts, bool fp32) {
+  if (rows == 0) return 0;
+  const Mm8Plan pl = mm8_plan(rows, K, N, experts);
+  return pl.splits > 1 ? (size_t)pl.splits * rows * N * 4 : 0;
+}
+
+cudaError_t launch_mm8(int rows, int K, int N, int experts, bool fp32, const void* a,
+                       const void* b, const int* start, void* y, unsigned char* ws, int* err,
+                       cudaStream_t st) {
+  if (rows == 0) return cudaSuccess;
+  const Mm8Plan pl = mm8_plan(rows, K, N, experts);
+  Params p{};
+  p.rows = rows; p.n = N; p.experts = experts;
+  p.tn = pl.tn; p.f_tiles = pl.f_tiles; p.steps = pl.steps;
+  p.splits = pl.splits; p.split_steps = pl.split_steps;
+  p.pitch = ck_pitch(K); p.cols = ck_cols(K);
+  p.bf16 = !fp32 && pl.splits == 1;
+  p.a = static_cast<const uint8_t*>(a);
+  p.b = static_cast<const uint8_t*>(b);
+  p.start = start;
+  p.y = pl.splits > 1 ? static_cast<void*>(ws) : y;
+  p.err = err;
+  const int blocks = std::max(experts, 1);
+  Maps tm;
+  cudaError_t e;
+  if ((e = code_map(&tm.w, b, p.cols, (uint64_t)blocks * N, p.pitch, 128)) != cudaSuccess) return e;
+  if ((e = code_map(&tm.x, a, p.cols, rows, p.pitch, pl.tn / 2)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(mm8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                SMEM_BYTES)) != cudaSuccess)
+    return e;
+  const long long most = ((long long)rows / pl.tn + std::min(blocks, rows)) * pl.f_tiles * pl.splits;
+  {
+    LaunchScope ls_("mm8", st);
+    mm8_kernel<<<2 * (int)std::min<long long>(PAIRS, most), THREADS, SMEM_BYTES, st>>>(tm, p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (pl.splits > 1) {
+    const int grid = (int)std::min<long long>(((long long)rows * N + 255) / 256, 152 * 8);
+    const int* end = experts ? start + experts : nullptr;
+    LaunchScope ls_("mm8_join", st);
+    const float* part = reinterpret_cast<const float*>(ws);
+    if (fp32)
+      mm8_join_kernel<<<grid, 256, 0, st>>>(part, static_cast<float*>(y), end, rows, N, pl.splits);
+    else
+      mm8_join_kernel<<<grid, 256, 0, st>>>(part, static_cast<__nv_bfloat16*>(y), end, rows, N,
+                                            pl.splits);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace laga
