@@ -12,12 +12,14 @@
 // full 256-row tiles.
 //
 // Persistent pairs of CTAs (two-CTA clusters, cta_group::2): CTA rank r holds
-// 128 of a tile's rows of b and half of its rows of a.  8 warps:
-//   0     TMA producer of codes         (ring of STAGES, K = 128 each)
+// 128 of a tile's rows of b and half of its rows of a.  12 warps:
+//   0     TMA producer of codes         (ring of STAGES, two steps of K = 128 each)
 //   1     MMA issuer (rank 0), TMEM allocator
-//   2     scale loader: four stages' bytes of each row, a 32-bit word, into the
-//         32 x 128-bit layout that tcgen05.cp spreads over TMEM (ring of SF_SLOTS)
-//   4-7   epilogue: accumulator -> registers -> y (or, where K is split, fp32
+//   2     scale loader: four steps' bytes of each row, a 32-bit word, into the
+//         32 x 128-bit layout that tcgen05.cp spreads over TMEM; 16 steps' words
+//         at a time (ring of SF_SLOTS), since loading them and telling the other
+//         CTA takes some 2500 clocks
+//   4-11  epilogue: accumulator -> registers -> y (or, where K is split, fp32
 //         partial sums, which mm8_join adds up in order)
 // TMEM: two accumulators of up to 224 columns, so that one drains while the
 // other fills, and four sets of scales.
@@ -34,36 +36,43 @@ namespace laga {
 namespace {
 using namespace sm100;
 
-constexpr int KS = CK_GROUP;                 // codes of i per stage
+constexpr int KS = CK_GROUP;                 // codes of i per step, the swizzled width
+constexpr int HALVES = 2;                    // steps per stage
 constexpr int FT = 256;                      // rows of b per tile
 constexpr int TN_MAX = 224;                  // rows of a per tile
-constexpr int STAGES = 6;
+constexpr int STAGES = 3;
 constexpr int W_BYTES = 128 * KS, X_BYTES = TN_MAX / 2 * KS;
-constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
-constexpr int SF_SLOTS = 4, SF_BYTES = 3 * 512;   // 128 rows of b, 2 x 128 of a
+constexpr int X_OFF = HALVES * W_BYTES, STAGE_BYTES = X_OFF + HALVES * X_BYTES;
+constexpr int SF_BYTES = 3 * 512;            // 4 steps' words of 128 rows of b, 2 x 128 of a
+constexpr int SF_WORDS = 4, SF_SLOTS = 2;    // such words in a slot of the ring
+constexpr int SF_STEPS = 4 * SF_WORDS;
 constexpr int SF_OFF = STAGES * STAGE_BYTES;
-constexpr int SMEM_BYTES = SF_OFF + SF_SLOTS * SF_BYTES + 1024;
-constexpr int THREADS = 256;
+constexpr int SLOT_BYTES = 2048, OUT_OFF = SF_OFF + SF_SLOTS * SF_WORDS * SF_BYTES;
+constexpr int EPI_WARPS = 8;
+constexpr int SMEM_BYTES = OUT_OFF + EPI_WARPS * SLOT_BYTES + 1024;
+constexpr int THREADS = 128 + 32 * EPI_WARPS;
 constexpr int TMEM_COLS = 512, SF_COL = 2 * TN_MAX, SF_SETS = 4, SF_COLS = 16;
 static_assert(SF_COL + SF_SETS * SF_COLS <= TMEM_COLS, "tensor memory");
-// A set of scales is written again SF_SETS groups of 4 stages later.  By then
-// the MMAs that read it are done: the ring lets STAGES of them be in flight.
-static_assert((SF_SETS - 1) * 4 >= STAGES, "scales outlive the MMAs that read them");
+// A set of scales is written again SF_SETS groups of 4 steps later.  By then the
+// MMAs that read it are done: the ring lets STAGES stages be in flight.
+static_assert((SF_SETS - 1) * 4 >= STAGES * HALVES, "scales outlive the MMAs that read them");
+static_assert(4 % HALVES == 0, "whole stages under a word of scales");
 constexpr int PAIRS = 76;                    // one pair per two SMs
 constexpr int BAND = 8;                      // column tiles that run side by side
 constexpr int WMAX = ROUTE_MAX_EXPERTS;
 
 struct Maps {
-  CUtensorMap w, x;
+  CUtensorMap w, x, y;
 };
 struct Params {
   int rows, n, experts;    // experts 0: one matrix
   int tn;                  // rows of a per tile, a multiple of 32
   int f_tiles;             // column tiles
-  int steps;               // stages of the whole K
-  int splits, split_steps; // pieces of K, stages of each
+  int steps;               // steps of the whole K
+  int splits, split_steps; // pieces of K, steps of each
   int pitch, cols;         // bytes of a row of a and b, of its codes
   int bf16;
+  int mapped;              // y has a tensor map
   const uint8_t *a, *b;
   const int* start;
   void* y;                 // or the partial sums [splits, rows, n]
@@ -75,7 +84,7 @@ struct Segments {
   int start[WMAX + 1], tiles[WMAX + 1];
 };
 
-// A pair's tiles in turn: rows r0 .. r1 of expert e, column tile f, stages k0 ..
+// A pair's tiles in turn: rows r0 .. r1 of expert e, column tile f, steps k0 ..
 struct Walk {
   int t, e;                // next tile, and the expert of the last one
   int r0, r1, f, k0, kn, z;
@@ -126,6 +135,19 @@ LAGA_DEVINL void copy_scales_pair(uint32_t taddr, uint32_t saddr) {
                : "memory");
 }
 
+// Whether a phase has completed, without waiting for it.
+LAGA_DEVINL bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // A thread that copies leaves when its last copies have landed.
 template <int N>
 LAGA_DEVINL void wait_landed(uint64_t (&full)[N], uint32_t it, int* err) {
@@ -133,19 +155,41 @@ LAGA_DEVINL void wait_landed(uint64_t (&full)[N], uint32_t it, int* err) {
     mbar_wait_each(&full[i % N], (i / N) & 1, err);
 }
 
+// This warp's 32 columns of y, from the accumulator's lanes, which are columns
+// here, to rows: through a slot of [rows][32 columns] in shared memory and a
+// tensor store, or (a tile's last rows, widths that no tensor map takes) lane
+// by lane.  Of the two warps of these columns each takes every other 32 rows.
 template <typename T>
-LAGA_DEVINL void store_tile(const Params& p, const Walk& w, T* y, uint32_t acc, int q, int lane,
-                            int col0) {
+LAGA_DEVINL void store_tile(const Params& p, const CUtensorMap* ym, const Walk& w, uint32_t acc,
+                            int q, int lane, int first, int col0, uint8_t* out) {
+  constexpr int R = SLOT_BYTES / (32 * sizeof(T));   // rows of a slot
   const int j = col0 + lane;
   const int n = w.r1 - w.r0;
-  T* dst = y + ((long long)w.z * p.rows + w.r0) * p.n + j;
-  for (int c0 = 0; c0 < n; c0 += 32) {
+  const long long row0 = (long long)w.z * p.rows + w.r0;
+  T* dst = static_cast<T*>(p.y) + row0 * p.n + j;
+  for (int c0 = first; c0 < n; c0 += 64) {
     uint32_t u[32];
     tmem_ld32(tmem_addr(acc, q, c0), u);
-    if (j < p.n) {
 #pragma unroll
-      for (int c = 0; c < 32; ++c)
-        if (c0 + c < n) dst[(long long)(c0 + c) * p.n] = from_f32<T>(__uint_as_float(u[c]));
+    for (int h = 0; h < 32; h += R) {
+      if (p.mapped && c0 + h + R <= n) {
+        T* slot = reinterpret_cast<T*>(out);
+        if (lane == 0) bulk_wait_read0();     // the store that last read the slot
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < R; ++c) slot[c * 32 + lane] = from_f32<T>(__uint_as_float(u[h + c]));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (col0 < p.n) tma_store_2d(ym, slot, col0, (int)row0 + c0 + h);
+          bulk_commit();
+        }
+      } else if (j < p.n) {
+#pragma unroll
+        for (int c = 0; c < R; ++c)
+          if (c0 + h + c < n)
+            dst[(long long)(c0 + h + c) * p.n] = from_f32<T>(__uint_as_float(u[h + c]));
+      }
     }
   }
 }
@@ -175,7 +219,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 8);
+      mbar_init(&acc_empty[i], 2 * EPI_WARPS);
     }
     fence_barrier_init();
   }
@@ -229,7 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       while (ok && w.next(p, seg)) {
         const int row_w = w.e * p.n + w.f * FT + (int)rank * 128;
         const int row_x = w.r0 + (int)rank * (w.width() / 2);
-        for (int k = 0; k < w.kn; ++k, ++it) {
+        for (int k = 0; k < w.kn; k += HALVES, ++it) {
           const int st = it % STAGES;
           if (it >= STAGES && !mbar_wait_each(&empty[st], (it / STAGES - 1) & 1, p.err)) {
             ok = false;
@@ -237,51 +281,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           uint8_t* dst = sm + st * STAGE_BYTES;
           const uint32_t bar = smem_cluster_addr(&full[st], 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * (W_BYTES + half * KS));
-          tma_load_2d_pair(dst, &tm.w, bar, (w.k0 + k) * KS, row_w);
-          tma_load_2d_pair(dst + W_BYTES, &tm.x, bar, (w.k0 + k) * KS, row_x);
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * HALVES * (W_BYTES + half * KS));
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h) {   // (a step behind the last one is zeros)
+            tma_load_2d_pair(dst + h * W_BYTES, &tm.w, bar, (w.k0 + k + h) * KS, row_w);
+            tma_load_2d_pair(dst + X_OFF + h * X_BYTES, &tm.x, bar, (w.k0 + k + h) * KS, row_x);
+          }
         }
       }
       if (rank == 0) wait_landed(full, it, p.err);
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      uint32_t it = 0, group = 0, tile = 0;
+      // This thread's own instructions set the pace (MMAs of 112 clocks): everything that can is carried along instead of computed.
+      uint32_t group = 0, set = 0, tile = 0;
+      uint32_t st = 0, parity = 0;         // the next stage and its phase
+      bool ready = false;                  // it has been seen full
       bool ok = true;
+      const uint32_t ring = sdesc_lo(smem_u32(sm), 16);
+      uint32_t alo = ring;
       while (ok && w.next(p, seg)) {
         const int buf = tile & 1;
         if (tile >= 2 && !mbar_wait_cluster(&acc_empty[buf], ((tile >> 1) - 1) & 1, p.err)) break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(buf * TN_MAX);
         const int n = w.width();
-        for (int k = 0; ok && k < w.kn; ++group) {
+        const bool wide = n > 128;
+        const uint32_t idesc0 = idesc_mx(n, 0);
+        uint32_t more = 0;
+        for (int left = w.kn; ok && left > 0; left -= SF_STEPS, ++group) {
           const int slot = group % SF_SLOTS;
           if (!mbar_wait_cluster(&sf_full[slot], (group / SF_SLOTS) & 1, p.err)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sf = tmem + SF_COL + (uint32_t)(group % SF_SETS * SF_COLS);
-          const uint32_t src = smem_u32(sm + SF_OFF + slot * SF_BYTES);
-          copy_scales_pair(sf, src);
-          copy_scales_pair(sf + 4, src + 512);
-          if (n > 128) copy_scales_pair(sf + 8, src + 1024);
-          const int k1 = min(k + 4, w.kn);
-          for (int byte = 0; k < k1; ++k, ++byte, ++it) {
-            const int st = it % STAGES;
-            if (!mbar_wait_each(&full[st], (it / STAGES) & 1, p.err)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t wa = smem_u32(sm + st * STAGE_BYTES);
-            const uint32_t alo = sdesc_lo(wa, 16), blo = sdesc_lo(wa + W_BYTES, 16);
-            const uint32_t idesc = idesc_mx(n, byte);
+          uint32_t src = smem_u32(sm + SF_OFF + slot * (SF_WORDS * SF_BYTES));
+          const int words = min(left, SF_STEPS);
+          for (int i0 = 0; ok && i0 < words; i0 += 4, src += SF_BYTES) {
+            const uint32_t sf = tmem + SF_COL + (uint32_t)(set++ % SF_SETS * SF_COLS);
+            copy_scales_pair(sf, src);
+            copy_scales_pair(sf + 4, src + 512);
+            if (wide) copy_scales_pair(sf + 8, src + 1024);
+            const int m = min(4, words - i0);
+            uint32_t idesc = idesc0;
+            for (int i = 0; i < m; i += HALVES) {
+              if (!ready && !mbar_wait_each(&full[st], parity, p.err)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t now = st, a = alo, b = alo + (X_OFF >> 4);
+              st = st + 1 == STAGES ? 0 : st + 1;
+              parity ^= st == 0;
+              alo = st == 0 ? ring : alo + (STAGE_BYTES >> 4);
+              // ask for the next stage now: the answer arrives while these MMAs
+              // are issued
+              ready = mbar_test(&full[st], parity);
 #pragma unroll
-            for (int kk = 0; kk < KS / 32; ++kk)
-              mma_mx_pair(d, sdesc_make(alo + kk * 2), sdesc_make(blo + kk * 2), idesc, sf, sf + 4,
-                          (k > 0 || kk > 0) ? 1u : 0u);
-            mma_commit_pair(&empty[st]);
+              for (int h = 0; h < HALVES; ++h) {
+                if (h > 0 && i + h >= m) break;
+#pragma unroll
+                for (int kk = 0; kk < KS / 32; ++kk)
+                  mma_mx_pair(d, sdesc_make(a + (h * W_BYTES + kk * 32 >> 4)),
+                              sdesc_make(b + (h * X_BYTES + kk * 32 >> 4)), idesc, sf, sf + 4,
+                              h + kk > 0 ? 1u : more);
+                idesc += 1u << 4 | 1u << 29;
+              }
+              more = 1;
+              mma_commit_pair(&empty[now]);
+            }
           }
           mma_commit_pair(&sf_empty[slot]);
         }
@@ -299,24 +368,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     while (w.next(p, seg)) {
       const int rows_b = max(p.experts, 1) * p.n;   // at most 2^24
       const int row_w = w.e * p.n + w.f * FT + (int)rank * 128;
-      for (int k = 0; k < w.kn; k += 4, ++group) {
-        // k0 is a multiple of 4 stages: whole words of scale bytes
+      for (int k = 0; k < w.kn; k += SF_STEPS, ++group) {
+        // k0 is a multiple of 4 steps: whole words of scale bytes
         const uint32_t off = (uint32_t)(p.cols + w.k0 + k);
-        uint32_t v[12];
+        uint32_t v[SF_WORDS][12];
 #pragma unroll
         for (int i = 0; i < 12; ++i) {
           const long long r = i < 4 ? row_w + 32 * i + lane : w.r0 + 32 * (i - 4) + lane;
           const bool in = i < 4 ? r < rows_b : r < w.r1;
-          v[i] = in ? *reinterpret_cast<const uint32_t*>((i < 4 ? p.b : p.a) + r * p.pitch + off)
-                    : 0u;
+          const uint8_t* src = (i < 4 ? p.b : p.a) + r * p.pitch + off;
+#pragma unroll
+          for (int j = 0; j < SF_WORDS; ++j)
+            v[j][i] = in && k + 4 * j < w.kn ? *reinterpret_cast<const uint32_t*>(src + 4 * j) : 0u;
         }
         const int slot = group % SF_SLOTS;
         if (group >= SF_SLOTS)
           mbar_wait_or_pass(&sf_empty[slot], (group / SF_SLOTS - 1) & 1, polls, p.err);
-        uint4* dst = reinterpret_cast<uint4*>(sm + SF_OFF + slot * SF_BYTES) + lane;
+        uint4* dst = reinterpret_cast<uint4*>(sm + SF_OFF + slot * (SF_WORDS * SF_BYTES)) + lane;
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-          dst[32 * i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        for (int j = 0; j < SF_WORDS; ++j)
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            dst[j * (SF_BYTES / 16) + 32 * i] =
+                make_uint4(v[j][4 * i], v[j][4 * i + 1], v[j][4 * i + 2], v[j][4 * i + 3]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && polls) mbar_arrive_cluster(smem_cluster_addr(&sf_full[slot], 0));
@@ -325,6 +399,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   } else if (warp >= 4) {
     const int q = warp & 3;
     uint32_t polls = kWaitPolls;
+    uint8_t* slot = sm + OUT_OFF + (warp - 4) * SLOT_BYTES;
+    const int first = (warp - 4) / 4 * 32;
+    if (lane == 0) tma_prefetch_desc(&tm.y);
     for (uint32_t tile = 0; w.next(p, seg); ++tile) {
       const int buf = tile & 1;
       mbar_wait_or_pass(&acc_full[buf], (tile >> 1) & 1, polls, p.err);
@@ -332,13 +409,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const uint32_t acc = tmem + (uint32_t)(buf * TN_MAX);
       const int col0 = w.f * FT + (int)rank * 128 + q * 32;
       if (p.bf16)
-        store_tile(p, w, static_cast<__nv_bfloat16*>(p.y), acc, q, lane, col0);
+        store_tile<__nv_bfloat16>(p, &tm.y, w, acc, q, lane, first, col0, slot);
       else
-        store_tile(p, w, static_cast<float*>(p.y), acc, q, lane, col0);
+        store_tile<float>(p, &tm.y, w, acc, q, lane, first, col0, slot);
       tc_fence_before();
       __syncwarp();
       if (lane == 0 && polls) mbar_arrive_cluster(smem_cluster_addr(&acc_empty[buf], 0));
     }
+    if (lane == 0) bulk_wait_read0();
+    __syncwarp();
   }
   // neither CTA leaves while the pair's MMAs or the other CTA's arrivals may
   // still touch its shared memory or TMEM
@@ -413,6 +492,20 @@ cudaError_t code_map(CUtensorMap* out, const void* base, uint64_t width, uint64_
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// y (or the partial sums) [rows, n] in boxes of 32 columns x a slot's rows.
+cudaError_t out_map(CUtensorMap* out, void* base, uint64_t n, uint64_t rows, bool bf16) {
+  auto enc = tmap_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const uint32_t size = bf16 ? 2 : 4;
+  const cuuint64_t dims[2] = {n, rows}, str[1] = {n * size};
+  const cuuint32_t box[2] = {32, SLOT_BYTES / (32 * size)}, one[2] = {1, 1};
+  const CUresult r =
+      enc(out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base,
+          dims, str, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace
 
 size_t mm8_ws_bytes(int rows, int K, int N, int experts, bool fp32) {
@@ -442,6 +535,12 @@ cudaError_t launch_mm8(int rows, int K, int N, int experts, bool fp32, const voi
   cudaError_t e;
   if ((e = code_map(&tm.w, b, p.cols, (uint64_t)blocks * N, p.pitch, 128)) != cudaSuccess) return e;
   if ((e = code_map(&tm.x, a, p.cols, rows, p.pitch, pl.tn / 2)) != cudaSuccess) return e;
+  // rows that start on 16 bytes, and row numbers within a coordinate's 31 bits
+  p.mapped = (uint64_t)N * (p.bf16 ? 2 : 4) % 16 == 0 && (long long)pl.splits * rows <= 0x7fffffff;
+  tm.y = tm.x;
+  if (p.mapped &&
+      (e = out_map(&tm.y, p.y, N, (uint64_t)pl.splits * rows, p.bf16)) != cudaSuccess)
+    return e;
   if ((e = cudaFuncSetAttribute(mm8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 SMEM_BYTES)) != cudaSuccess)
     return e;
