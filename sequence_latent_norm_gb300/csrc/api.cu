@@ -605,7 +605,8 @@ laga_status laga_mm8(int rows, int k, int n, int experts, laga_dtype out_dtype, 
 
 static bool experts_dw_sizes_ok(int rows, int d, int n, int experts, laga_dtype dtype) {
   return rows >= 0 && rows <= 0x7fffffff - 1024 && width_ok(d) && n >= 1 && n <= CK_MAX_N &&
-         experts >= 1 && experts_ok(experts) && dtype_ok(dtype);
+         experts >= 1 && experts_ok(experts) && dtype_ok(dtype) &&
+         experts_dw_fits(rows, d, n, experts, dtype == LAGA_FP32);
 }
 
 size_t laga_experts_dw_workspace_bytes(int rows, int d, int n, int experts, laga_dtype dy_dtype) {

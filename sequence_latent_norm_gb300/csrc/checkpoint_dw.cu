@@ -1,4 +1,5 @@
-// Weight gradient from an 8-bit checkpoint (include/laga.h: laga_ckpt_dw):
+// Weight gradient from an 8-bit checkpoint (include/laga.h: laga_ckpt_dw,
+// laga_experts_dw):
 //   dw[c, j] = gamma[c] sum_t v[t, c] dy[t, j],   v = code * 2^e,
 // M = channels, N = columns of dy, K = tokens, on the tensor cores.  v is a
 // bf16 number exactly, so the codes are turned into bf16 operand tiles on the
@@ -49,9 +50,14 @@
 // are dealt out evenly over all pairs.  A pair's part of such a tile is a fragment in the workspace; dw_join adds a
 // tile's fragments in token order.  Which pair takes what depends on the
 // sizes alone, so every run adds in the same order.
+//
+// By expert, a tile belongs to one and goes over its rows, whole steps, whose
+// number the device alone knows: whole rounds go by tile count, and the left-
+// over tiles' steps are counted out by every pair for itself.
 #include <limits.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ckpt8.cuh"
 #include "common.cuh"
@@ -110,15 +116,98 @@ struct DwParams {
   const float* gamma;
   float *dw, *frag;
   int* err;
+  // by expert; `tiles` is one expert's, and rounds are of all experts'
+  int experts, rows;
+  const int* start;        // first row of each expert, whole steps
 };
 
-// A pair's work, piece by piece: kn steps from k0 on of tile t.  frag < 0: a
-// whole tile, stored to the output.
-struct Walk {
+// What the device adds up by expert, in shared memory: the experts' first steps
+// and the steps in front of each left-over tile.
+struct Counts {
+  int first[ROUTE_MAX_EXPERTS + 1];
+  int left[PAIRS + 1], total_left, chunk;
+};
+LAGA_DEVINL int first_step(const DwParams& p, int e) { return min(p.start[e], p.rows) / KT; }
+// By one whole warp; left-over tile i is tile rounds * PAIRS + i of all.
+LAGA_DEVINL void count_left(const DwParams& p, Counts& c, int lane) {
+  const int t0 = p.rounds * PAIRS, n = p.experts * p.tiles - t0;
+  int carry = 0;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int i = i0 + lane, e = (t0 + min(i, n - 1)) / p.tiles;
+    const int own = i < n ? max(first_step(p, e + 1) - first_step(p, e), 0) : 0;
+    int sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (i < n) c.left[i + 1] = carry + sum;
+    carry += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  if (lane == 0) {
+    c.left[0] = 0;
+    c.total_left = carry;
+    c.chunk = max((carry + PAIRS - 1) / PAIRS, 1);
+  }
+}
+
+// A pair's work, piece by piece: kn steps from k0 on of tile t (of expert e).
+// frag < 0: a whole tile, stored to the output.
+template <bool BY_EXPERT>
+struct Walk;
+
+template <>
+struct Walk<true> {
+  int t, e, k0, kn, frag;
+  int i, tile, u, end;           // tile, step and end of the share of the left-over tiles
+
+  LAGA_DEVINL Walk(const DwParams& p, const Counts& c, int pair) {
+    u = min(pair * c.chunk, c.total_left);
+    end = min(u + c.chunk, c.total_left);
+    tile = 0;
+    i = 0;
+  }
+  LAGA_DEVINL bool next(const DwParams& p, const Counts& c, int pair) {
+    int all;                     // the tile's number among all experts'
+    if (i < p.rounds) {
+      all = i++ * PAIRS + pair;
+      frag = -1;
+    } else if (u < end) {
+      while (c.left[tile + 1] <= u) ++tile;
+      all = p.rounds * PAIRS + tile;
+      frag = tile + pair;        // counts up by one piece at a time
+    } else {
+      return false;
+    }
+    e = all / p.tiles;
+    t = all - e * p.tiles;
+    k0 = c.first[e];
+    kn = max(c.first[e + 1] - k0, 0);
+    if (frag >= 0) {
+      k0 += u - c.left[tile];
+      kn = min(c.left[tile + 1], end) - u;
+      u += kn;
+    }
+    return true;
+  }
+  LAGA_DEVINL int step(const DwParams& p, int j) const {
+    return k0 + (j + ((t / p.n_tiles) & 7)) % kn;
+  }
+  LAGA_DEVINL long long out_row(const DwParams& p) const { return (long long)e * p.d; }
+  // Steps of all pieces; the walk is at its end then.
+  LAGA_DEVINL uint32_t count(const DwParams& p, const Counts& c, int pair) {
+    uint32_t n = 0;
+    while (next(p, c, pair)) n += kn;
+    return n;
+  }
+};
+
+template <>
+struct Walk<false> {
   int t, k0, kn, frag;
   int i, next_t, next_k, left;   // of the pair's share of the left-over tiles
 
-  LAGA_DEVINL Walk(const DwParams& p, int pair) {
+  LAGA_DEVINL Walk(const DwParams& p, const Counts&, int pair) {
     const long long total = (long long)(p.tiles - p.rounds * PAIRS) * p.steps;
     const long long u = min((long long)pair * p.chunk, total);
     left = (int)min((long long)p.chunk, total - u);
@@ -126,7 +215,7 @@ struct Walk {
     next_k = (int)(u % p.steps);
     i = 0;
   }
-  LAGA_DEVINL bool next(const DwParams& p, int pair) {
+  LAGA_DEVINL bool next(const DwParams& p, const Counts&, int pair) {
     if (i < p.rounds) {
       t = i * PAIRS + pair;
       k0 = 0;
@@ -151,6 +240,10 @@ struct Walk {
   // apart).
   LAGA_DEVINL int step(const DwParams& p, int j) const {
     return k0 + (j + ((t / p.n_tiles) & 7)) % kn;
+  }
+  LAGA_DEVINL long long out_row(const DwParams& p) const { return 0; }
+  LAGA_DEVINL uint32_t count(const DwParams& p, const Counts&, int pair) {
+    return (uint32_t)(p.rounds * p.steps + left);
   }
 };
 
@@ -211,7 +304,7 @@ LAGA_DEVINL void wait_landed(uint64_t (&full)[N], uint32_t it, int* err) {
     mbar_wait_each(&full[i % N], (i / N) & 1, err);
 }
 
-template <int BN>
+template <int BN, bool BY_EXPERT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     ckpt_dw_kernel(const __grid_constant__ DwMaps tm, const __grid_constant__ DwParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -224,6 +317,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   __shared__ uint64_t c_full[NC], c_empty[NC], a_full[NE], a_empty[NE], b_full[NB], b_empty[NB];
   __shared__ uint64_t acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_sh;
+  __shared__ std::conditional_t<BY_EXPERT, Counts, char> counts_sh;
+  Counts& counts = reinterpret_cast<Counts&>(counts_sh);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1;
@@ -252,12 +347,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tmem_alloc_pair(&tmem_sh, TMEM_COLS);
     tmem_relinquish_pair();
   }
+  if constexpr (BY_EXPERT) {
+    for (int e = threadIdx.x; e <= p.experts; e += THREADS) counts.first[e] = first_step(p, e);
+    if (warp == W_DEC) count_left(p, counts, lane);
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();   // both CTAs' barriers exist before anything signals them
   tc_fence_after();
   const uint32_t tmem = tmem_sh;
-  Walk w(p, pair);
+  Walk<BY_EXPERT> w(p, counts, pair);
   if (warp < W_DEC) reg_shrink<REG_MISC>();
 
   if (warp == 0) {
@@ -265,7 +364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       tma_prefetch_desc(&tm.dy);
       uint32_t it = 0;
       bool ok = true;
-      while (ok && w.next(p, pair)) {
+      while (ok && w.next(p, counts, pair)) {
         const int n0 = (w.t % p.n_tiles) * BN + (int)rank * HALF;
         for (int j = 0; ok && j < w.kn; ++j)
           for (int s = 0; s < p.pieces; ++s, ++it) {
@@ -295,7 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       tma_prefetch_desc(&tm.scales);
       uint32_t it = 0;
       bool ok = true;
-      while (ok && w.next(p, pair)) {
+      while (ok && w.next(p, counts, pair)) {
         const int g = (w.t / p.n_tiles) * 2 + (int)rank;
         for (int j = 0; j < w.kn; ++j, ++it) {
           const int t0 = w.step(p, j) * KT;
@@ -318,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       uint32_t ia = 0, ib = 0, ic = 0;   // v tiles, dy tiles, chains
       bool a_ready = false, b_ready = false;   // the next ones have been seen full
       bool ok = true;
-      while (ok && w.next(p, pair)) {
+      while (ok && w.next(p, counts, pair)) {
         for (int k0 = 0; ok && k0 < w.kn; k0 += p.chain, ++ic) {
           const int buf = ic & 1;
           if (ic >= 2 && !mbar_wait_cluster(&acc_empty[buf], ((ic >> 1) - 1) & 1, p.err)) {
@@ -368,7 +467,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // scope release that makes them so for the pair takes ~1000 clocks, which
     // the decoders would wait for and these two do not mind.
     if (lane == 0 && rank == 1) {
-      const uint32_t total = (uint32_t)(p.rounds * p.steps + w.left);
+      const uint32_t total = w.count(p, counts, pair);
       for (uint32_t it = warp & 1; it < total; it += 2) {
         if (!mbar_wait_each(&a_full[it % NE], (it / NE) & 1, p.err)) break;
         mbar_arrive_cluster(smem_cluster_addr(&a_full[it % NE], 0));
@@ -380,7 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int q = warp & 3, c0 = ((warp - W_EPI) >> 2) * HALF;
     uint32_t ic = 0;
     uint32_t polls = kWaitPolls;
-    while (w.next(p, pair)) {
+    while (w.next(p, counts, pair)) {
       float2 acc[HALF / 2];
 #pragma unroll
       for (int j = 0; j < HALF / 2; ++j) acc[j] = make_float2(0.f, 0.f);
@@ -406,7 +505,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (polls && row < p.d) {
         const float gain = p.gamma ? p.gamma[row] : 1.f;
         float* dst = w.frag >= 0 ? p.frag + ((long long)w.frag * 256 + r) * BN + c0
-                                 : p.dw + (long long)row * p.n + n0;
+                                 : p.dw + (w.out_row(p) + row) * p.n + n0;
         const int lim = w.frag >= 0 ? HALF : p.n - n0;           // columns that exist
         if (w.frag >= 0 || p.n % 4 == 0) {
 #pragma unroll
@@ -449,8 +548,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     uint32_t byte[N];
     uint32_t base = 0;   // steps before this piece
     uint32_t polls = kWaitPolls;
-    while (w.next(p, pair)) {
+    while (w.next(p, counts, pair)) {
       const int g = ((w.t / p.n_tiles) * 2 + (int)rank) & 15;
+      if (BY_EXPERT && w.kn == 0) continue;
       const uint32_t end = base + w.kn;
       auto fetch = [&](uint32_t it) {
         const int sc = it % NC;
@@ -545,6 +645,39 @@ __global__ void __launch_bounds__(256) dw_join_kernel(const DwParams p, int bn) 
   }
 }
 
+// The same by expert: pieces of a tile have the numbers tile + pair.
+__global__ void __launch_bounds__(256) experts_join_kernel(const DwParams p, int bn) {
+  __shared__ Counts c;
+  if (threadIdx.x < 32) count_left(p, c, threadIdx.x);
+  __syncthreads();
+  const int vecs = bn / 4;
+  const int tile = blockIdx.x / vecs;
+  const int i = (blockIdx.x % vecs) * 256 + threadIdx.x;
+  const int r = i / vecs, col = (i % vecs) * 4;
+  const int all = p.rounds * PAIRS + tile, e = all / p.tiles, t = all - e * p.tiles;
+  const int row = (t / p.n_tiles) * 256 + r, n0 = (t % p.n_tiles) * bn + col;
+  if (row >= p.d || n0 >= p.n) return;
+  const int u0 = c.left[tile], u1 = c.left[tile + 1];
+  const float* src = p.frag + (long long)r * bn + col;
+  const long long slot = 256LL * bn;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);   // an expert without rows
+  if (u1 > u0) {
+    const int pa = u0 / c.chunk, pb = (u1 - 1) / c.chunk;
+    s = *reinterpret_cast<const float4*>(src + (tile + pa) * slot);
+    for (int q = pa + 1; q <= pb; ++q) {
+      const float4 v = *reinterpret_cast<const float4*>(src + (tile + q) * slot);
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+  }
+  float* dst = p.dw + ((long long)e * p.d + row) * p.n + n0;
+  if (p.n % 4 == 0) {
+    *reinterpret_cast<float4*>(dst) = s;
+  } else {
+    const float v[4] = {s.x, s.y, s.z, s.w};
+    for (int k = 0; k < 4 && n0 + k < p.n; ++k) dst[k] = v[k];
+  }
+}
+
 // dy in bf16 with rows of np = 8 ceil(n / 8) columns: a copy (bf16) or the
 // three pieces of an fp32 value, each the rest cut to bf16's 8 significand
 // bits, so that the three hold all 24.
@@ -552,10 +685,12 @@ __global__ void __launch_bounds__(256) dw_join_kernel(const DwParams p, int bn) 
 template <typename T>
 __global__ void __launch_bounds__(256) dy_pieces_kernel(const T* __restrict__ dy,
                                                         __nv_bfloat16* __restrict__ out,
-                                                        long long rows, int n, int np) {
+                                                        long long rows, int n, int np,
+                                                        const int* __restrict__ end) {
   const int vecs = np / 8;
   const long long total = rows * vecs;
-  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
+  const long long used = end ? min((long long)*end, rows) * vecs : total;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < used; i += gridDim.x * 256LL) {
     const long long r = total <= 0x7fffffff ? (long long)((int)i / vecs) : i / vecs;
     const int c = (int)(i - r * vecs) * 8;
     float v[8];
@@ -662,14 +797,17 @@ size_t ckpt_dw_ws_bytes(int rows, int d, int n, bool fp32) {
   return pl.dy_bytes + pl.frag_bytes;
 }
 
-cudaError_t launch_ckpt_dw(int rows, int d, int n, bool fp32, const void* ck, const void* dy,
-                           const float* gamma, float* dw, unsigned char* ws, int* err,
-                           cudaStream_t st) {
-  if (rows == 0) return cudaMemsetAsync(dw, 0, (size_t)d * n * 4, st);
-  DwPlan pl = dw_plan(rows, d, n, fp32);
+namespace {
+
+// The launches of either entry point: dy's pieces, the products, their join.
+cudaError_t launch_plan(DwPlan& pl, int rows, int d, int n, bool fp32, const void* ck,
+                        const void* dy, const float* gamma, float* dw, unsigned char* ws, int* err,
+                        cudaStream_t st) {
   DwParams& p = pl.p;
   p.gamma = gamma;
   p.err = err;
+  const bool by_expert = p.experts > 0;
+  const int* end = by_expert ? p.start + p.experts : nullptr;
   cudaError_t e;
   const void* dyb = dy;
   if (pl.convert) {
@@ -679,11 +817,11 @@ cudaError_t launch_ckpt_dw(int rows, int d, int n, bool fp32, const void* ck, co
     if (fp32)
       dy_pieces_kernel<float><<<grid, 256, 0, st>>>(static_cast<const float*>(dy),
                                                     reinterpret_cast<__nv_bfloat16*>(ws), rows, n,
-                                                    pl.np);
+                                                    pl.np, end);
     else
       dy_pieces_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(
           static_cast<const __nv_bfloat16*>(dy), reinterpret_cast<__nv_bfloat16*>(ws), rows, n,
-          pl.np);
+          pl.np, end);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   p.dw = dw;
@@ -699,23 +837,74 @@ cudaError_t launch_ckpt_dw(int rows, int d, int n, bool fp32, const void* ck, co
     uint32_t box[3] = {64, KT, 1};
     if ((e = make_tmap_bf16(&tm.dy, dyb, 3, dims, str, box)) != cudaSuccess) return e;
   }
-  auto k = pl.bn == 256 ? ckpt_dw_kernel<256> : pl.bn == 192 ? ckpt_dw_kernel<192>
-                                                             : ckpt_dw_kernel<128>;
+  auto k = by_expert ? pl.bn == 256   ? ckpt_dw_kernel<256, true>
+                       : pl.bn == 192 ? ckpt_dw_kernel<192, true>
+                                      : ckpt_dw_kernel<128, true>
+           : pl.bn == 256   ? ckpt_dw_kernel<256, false>
+           : pl.bn == 192   ? ckpt_dw_kernel<192, false>
+                            : ckpt_dw_kernel<128, false>;
   if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES)) !=
       cudaSuccess)
     return e;
-  const int left = p.tiles - p.rounds * PAIRS;
-  const int pairs = p.rounds > 0 ? PAIRS : pl.frag_slots / p.max_frags;
+  const int left = std::max(p.experts, 1) * p.tiles - p.rounds * PAIRS;
+  const int pairs = p.rounds > 0 || by_expert ? PAIRS : pl.frag_slots / p.max_frags;
   {
-    LaunchScope ls_("ckpt_dw", st);
+    LaunchScope ls_(by_expert ? "experts_dw" : "ckpt_dw", st);
     k<<<2 * pairs, THREADS, SMEM_BYTES, st>>>(tm, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (left > 0) {
-    LaunchScope ls_("ckpt_dw_join", st);
-    dw_join_kernel<<<left * (pl.bn / 4), 256, 0, st>>>(p, pl.bn);
+    LaunchScope ls_(by_expert ? "experts_dw_join" : "ckpt_dw_join", st);
+    auto join = by_expert ? experts_join_kernel : dw_join_kernel;
+    join<<<left * (pl.bn / 4), 256, 0, st>>>(p, pl.bn);
   }
   return cudaGetLastError();
+}
+
+DwPlan experts_plan(int rows, int d, int n, int experts, bool fp32) {
+  // the tiles of one expert, and dy's pieces, are those of a plain product
+  DwPlan pl = dw_plan(rows, d, n, fp32);
+  DwParams& p = pl.p;
+  p.experts = experts;
+  p.rows = rows;
+  const long long tiles = (long long)experts * p.tiles;
+  p.rounds = (int)(tiles / PAIRS);
+  const int left = (int)(tiles - (long long)p.rounds * PAIRS);
+  // a pair's steps, and the steps of the left-over tiles, stay in 32 bits
+  pl.fits = ((long long)p.rounds + left) * (p.steps + 1) <= INT_MAX;
+  pl.frag_slots = left > 0 ? left + PAIRS - 1 : 0;
+  pl.frag_bytes = up1k((size_t)pl.frag_slots * 256 * pl.bn * 4);
+  if (pl.convert) pl.dy_bytes = up1k((size_t)pl.pieces * rows * pl.np * 2);
+  return pl;
+}
+
+}  // namespace
+
+cudaError_t launch_ckpt_dw(int rows, int d, int n, bool fp32, const void* ck, const void* dy,
+                           const float* gamma, float* dw, unsigned char* ws, int* err,
+                           cudaStream_t st) {
+  if (rows == 0) return cudaMemsetAsync(dw, 0, (size_t)d * n * 4, st);
+  DwPlan pl = dw_plan(rows, d, n, fp32);
+  return launch_plan(pl, rows, d, n, fp32, ck, dy, gamma, dw, ws, err, st);
+}
+
+bool experts_dw_fits(int rows, int d, int n, int experts, bool fp32) {
+  return experts_plan(rows, d, n, experts, fp32).fits;
+}
+
+size_t experts_dw_ws_bytes(int rows, int d, int n, int experts, bool fp32) {
+  if (rows == 0) return 0;
+  const DwPlan pl = experts_plan(rows, d, n, experts, fp32);
+  return pl.dy_bytes + pl.frag_bytes;
+}
+
+cudaError_t launch_experts_dw(int rows, int d, int n, int experts, bool fp32, const void* ck,
+                              const void* dy, const float* gamma, const int* start, float* dw,
+                              unsigned char* ws, int* err, cudaStream_t st) {
+  if (rows == 0) return cudaMemsetAsync(dw, 0, (size_t)experts * d * n * 4, st);
+  DwPlan pl = experts_plan(rows, d, n, experts, fp32);
+  pl.p.start = start;
+  return launch_plan(pl, rows, d, n, fp32, ck, dy, gamma, dw, ws, err, st);
 }
 
 }  // namespace laga

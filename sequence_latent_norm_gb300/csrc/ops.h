@@ -73,6 +73,7 @@ cudaError_t launch_mm8(int rows, int K, int N, int experts, bool fp32, const voi
 
 // Weight gradient by expert: the rows of expert e are start[e] .. start[e + 1],
 // multiples of 128.
+bool experts_dw_fits(int rows, int d, int n, int experts, bool fp32);
 size_t experts_dw_ws_bytes(int rows, int d, int n, int experts, bool fp32);
 cudaError_t launch_experts_dw(int rows, int d, int n, int experts, bool fp32, const void* ck,
                               const void* dy, const float* gamma, const int* start, float* dw,
