@@ -12,7 +12,8 @@ namespace laga {
 namespace {
 
 // ------------------------------------------------------------------ rows
-// A warp copies one row of codes, 16 bytes a lane.
+// A warp copies one row of codes, 16 bytes a lane and eight such loads at a
+// time (16384 rows of 7232 bytes from 2048: 35 us one at a time).
 __global__ void __launch_bounds__(256)
     spread8_kernel(const uint8_t* __restrict__ ck, const int* __restrict__ pair,
                    const int* __restrict__ end, uint8_t* __restrict__ out, int rows, int tokens,
@@ -27,7 +28,15 @@ __global__ void __launch_bounds__(256)
       continue;
     }
     const uint4* src = reinterpret_cast<const uint4*>(ck + (long long)t * pitch);
-    for (int v = lane; v < vecs; v += 32) dst[v] = src[v];
+    for (int v0 = lane; v0 < vecs; v0 += 32 * 8) {
+      uint4 q[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (v0 + 32 * k < vecs) q[k] = src[v0 + 32 * k];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (v0 + 32 * k < vecs) dst[v0 + 32 * k] = q[k];
+    }
   }
 }
 
@@ -58,108 +67,228 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// dy[row_tj] = w_tj dout_t, dw_tj = <dout_t, y[row_tj]>: a block a token, its
-// choices one after the other; then the rows that no pair has, as zeros.
-template <typename T, int V>
-__global__ void __launch_bounds__(256)
+// dy[r] = w dout_t, dw = <dout_t, y[r]> of the row's pair: a warp a row, with
+// LOADS vectors of each side under way.  It goes by rows, not by pairs: y and dy
+// stream through HBM in order then, and dout, which every choice reads, stays in
+// L2.  (16384 x 7168 rows of 2048 tokens by pairs: 135 to 183 us.)  Rows of no
+// pair get zeros, pairs without a row a dw of zero.
+constexpr int LOADS = 4;
+
+// What a row has to do with its pair.
+struct PairOf {
+  bool on;
+  int q;
+  long long token;
+  float w;
+  LAGA_DEVINL PairOf(const int* pair, const float* weight, long long r, long long pairs, int top_k) {
+    q = pair[r];
+    on = q >= 0 && q < pairs;
+    token = on ? q / top_k : 0;
+    w = on ? weight ? weight[q] : 1.f : 0.f;
+  }
+};
+
+// The pairs without a row.
+LAGA_DEVINL void zero_dweight(float* dweight, const int* row, long long pairs, int rows) {
+  for (long long q = blockIdx.x * 256LL + threadIdx.x; q < pairs; q += gridDim.x * 256LL)
+    if (row[q] < 0 || row[q] >= rows) dweight[q] = 0.f;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256, 4)
     combine_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ y,
                        const float* __restrict__ weight, const int* __restrict__ row,
                        const int* __restrict__ pair, const int* __restrict__ end,
                        T* __restrict__ dy, float* __restrict__ dweight, int tokens, int top_k,
                        int rows, int d) {
-  __shared__ float part[8];
-  const int vecs = d / V, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (long long t = blockIdx.x; t < tokens; t += gridDim.x) {
-    for (int j = 0; j < top_k; ++j) {
-      const int r = row[t * top_k + j];
-      float dot = 0.f;
-      if (r >= 0 && r < rows) {
-        const float w = weight ? weight[t * top_k + j] : 1.f;
-        for (int v = threadIdx.x; v < vecs; v += 256) {
-          float2 g[(V + 1) / 2], f[(V + 1) / 2];
-          load_vec<V>(dout + t * d + v * V, g);
-          if (y) {
-            load_vec<V>(y + (long long)r * d + v * V, f);
+  constexpr int V = vec16<T>, P = V / 2;
+  const int vecs = d / V, lane = threadIdx.x & 31;
+  const long long pairs = (long long)tokens * top_k;
+  const int n = rows > 0 ? min(rows, *end) : 0;
+  for (long long r = blockIdx.x * 8LL + (threadIdx.x >> 5); r < n; r += gridDim.x * 8LL) {
+    const PairOf o(pair, weight, r, pairs, top_k);
+    const uint4* src = reinterpret_cast<const uint4*>(dout + o.token * d);
+    const uint4* old = reinterpret_cast<const uint4*>(y + r * d);
+    uint4* dst = reinterpret_cast<uint4*>(dy + r * d);
+    float2 dot = make_float2(0.f, 0.f);
+    for (int v0 = lane; v0 < vecs; v0 += 32 * LOADS) {
+      uint4 g[LOADS], f[LOADS];
 #pragma unroll
-            for (int k = 0; k < (V + 1) / 2; ++k) dot += g[k].x * f[k].x + g[k].y * f[k].y;
-          }
-#pragma unroll
-          for (int k = 0; k < (V + 1) / 2; ++k) g[k] = __fmul2_rn(g[k], make_float2(w, w));
-          store_vec<V>(dy + (long long)r * d + v * V, g);
+      for (int i = 0; i < LOADS; ++i) {
+        const int v = v0 + 32 * i;
+        g[i] = f[i] = make_uint4(0, 0, 0, 0);
+        if (o.on && v < vecs) {
+          g[i] = __ldg(src + v);
+          if (dweight) f[i] = __ldcs(old + v);
         }
       }
-      if (!dweight) continue;
-      dot = warp_sum(dot);
-      if (lane == 0) part[warp] = dot;
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        float s = 0.f;
-        for (int k = 0; k < 8; ++k) s += part[k];
-        dweight[t * top_k + j] = s;
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        float2 a[P], b[P];
+        open16(g[i], dout, a);
+        open16(f[i], dout, b);
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          dot = __ffma2_rn(a[k], b[k], dot);
+          a[k] = __fmul2_rn(a[k], make_float2(o.w, o.w));
+        }
+        if (v0 + 32 * i < vecs) dst[v0 + 32 * i] = close16(dout, a);
       }
-      __syncthreads();
     }
+    if (!dweight || !o.on) continue;
+    const float sum = warp_sum(dot.x + dot.y);
+    if (lane == 0) dweight[o.q] = sum;
   }
+  if (dweight) zero_dweight(dweight, row, pairs, rows);
+}
+
+// Other widths, channel by channel.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    combine_bwd1_kernel(const T* __restrict__ dout, const T* __restrict__ y,
+                        const float* __restrict__ weight, const int* __restrict__ row,
+                        const int* __restrict__ pair, const int* __restrict__ end,
+                        T* __restrict__ dy, float* __restrict__ dweight, int tokens, int top_k,
+                        int rows, int d) {
+  const int lane = threadIdx.x & 31;
+  const long long pairs = (long long)tokens * top_k;
   const int n = rows > 0 ? min(rows, *end) : 0;
-  for (long long r = blockIdx.x; r < n; r += gridDim.x)
-    if (pair[r] < 0)
-      for (int c = threadIdx.x; c < d; c += 256) dy[r * d + c] = from_f32<T>(0.f);
+  for (long long r = blockIdx.x * 8LL + (threadIdx.x >> 5); r < n; r += gridDim.x * 8LL) {
+    const PairOf o(pair, weight, r, pairs, top_k);
+    float dot = 0.f;
+#pragma unroll 4
+    for (int c = lane; c < d; c += 32) {
+      const float g = o.on ? to_f32(dout[o.token * d + c]) : 0.f;
+      if (o.on && dweight) dot = fmaf(g, to_f32(y[r * d + c]), dot);
+      dy[r * d + c] = from_f32<T>(g * o.w);
+    }
+    if (!dweight || !o.on) continue;
+    dot = warp_sum(dot);
+    if (lane == 0) dweight[o.q] = dot;
+  }
+  if (dweight) zero_dweight(dweight, row, pairs, rows);
 }
 
 // ------------------------------------------------------------------ activation
-LAGA_DEVINL float sigmoid_of(float x) { return 1.f / (1.f + expf(-x)); }
+// Each kernel moves 4 to 10 bytes a channel and has some 25 instructions for it
+// at that rate, so the sigmoid is two special functions; channels come in
+// vectors of 8 where the width allows.  (16384 x 2048 bf16 with expf, a division
+// and single channels: 82 us forward.)
 
-// a = silu(g) u of 4 channels a lane, a warp one group of 128.
-template <typename T>
+// sigmoid(g) and 1 - sigmoid(g) = e^-g sigmoid(g), each within 6 units of its
+// last place: the exponent's product with log2 e is carried in two parts, since
+// what it loses moves codes across their borders.  Below -87.3 the sigmoid
+// would be subnormal: both are zero.
+LAGA_DEVINL float2 sigmoid2(float g) {
+  constexpr float C = -1.44269502f, C_LO = -1.92596303e-8f, LN2 = 0.693147182f;
+  float e, s;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(g) : "f"(g), "f"(-88.5f));
+  const float t = g * C;
+  const float lo = fmaf(g, C_LO, fmaf(g, C, -t));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  e = fmaf(e, lo * LN2, e);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return make_float2(s, e * s);
+}
+LAGA_DEVINL float sigmoid(float g) { return sigmoid2(g).x; }
+
+// Codes of a group's values, `lanes` neighbouring lanes of V each.
+template <int V>
+LAGA_DEVINL float group_max(const float (&t)[V]) {
+  float m = 0.f;
+#pragma unroll
+  for (int k = 0; k < V; ++k) m = ck_max(m, t[k]);
+#pragma unroll
+  for (int o = CK_GROUP / V / 2; o > 0; o >>= 1) m = ck_max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+// a = silu(g) u.  A thread V channels, CK_GROUP / V neighbouring threads a
+// group; widths that are no multiple of 8 go 4 channels at a time, one by one.
+template <typename T, int V>
 __global__ void __launch_bounds__(256)
     swiglu_kernel(const T* __restrict__ gu, uint8_t* __restrict__ ck, const int* __restrict__ end,
                   int rows, int f) {
-  const int cols = ck_cols(f), groups = cols / CK_GROUP, pitch = ck_pitch(f);
-  const int lane = threadIdx.x & 31;
-  const long long n = (long long)(end ? min(rows, *end) : rows) * groups;
-  for (long long w = blockIdx.x * 8LL + (threadIdx.x >> 5); w < n; w += gridDim.x * 8LL) {
-    const long long r = w / groups;
-    const int g = (int)(w % groups);
-    uint8_t* row = ck + r * pitch;
-    const T* src = gu + r * 2 * f;
-    float t[4], m = 0.f;
+  const int cols = ck_cols(f), vpr = cols / V, pitch = ck_pitch(f);
+  const int pad = pitch - cols - cols / CK_GROUP;
+  const int n_rows = end ? min(rows, *end) : rows;
+  for (long long r0 = (long long)blockIdx.x * 2; r0 < n_rows; r0 += (long long)gridDim.x * 2) {
+    const int n = (int)min(2LL, n_rows - r0) * vpr;
+    // whole warps go round, so that every lane of a group is there
+    for (int i0 = threadIdx.x & ~31; i0 < n; i0 += 256) {
+      const int i = i0 + (threadIdx.x & 31);
+      const int r = i / vpr, v = i - r * vpr;
+      const T* src = gu + (r0 + r) * 2 * f + v * V;
+      float t[V];
+      if constexpr (V == 8) {
+        float2 g[4] = {}, u[4] = {};
+        if (i < n && v * 8 < f) {
+          load_vec<8>(src, g);
+          load_vec<8>(src + f, u);
+        }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int c = g * CK_GROUP + 4 * lane + k;
-      t[k] = 0.f;
-      if (c < f) {
-        const float x = to_f32(src[c]);
-        t[k] = x * sigmoid_of(x) * to_f32(src[f + c]);
+        for (int k = 0; k < 4; ++k) {
+          t[2 * k] = g[k].x * sigmoid(g[k].x) * u[k].x;
+          t[2 * k + 1] = g[k].y * sigmoid(g[k].y) * u[k].y;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          t[k] = 0.f;
+          if (i < n && v * V + k < f) {
+            const float g = to_f32(src[k]);
+            t[k] = g * sigmoid(g) * to_f32(src[f + k]);
+          }
+        }
       }
-      m = ck_max(m, t[k]);
-    }
+      float inv;
+      const int s = ck_scale(group_max<V>(t), &inv);
+      if (i >= n) continue;
+      uint8_t* row = ck + (r0 + r) * pitch;
+      uint32_t q[V / 4];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = ck_max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float inv;
-    const int s = ck_scale(m, &inv);
-    const uint32_t q = ck_code2(make_float2(t[0], t[1]), inv) |
-                       ck_code2(make_float2(t[2], t[3]), inv) << 16;
-    *reinterpret_cast<uint32_t*>(row + g * CK_GROUP + 4 * lane) = s == CK_NAN ? 0u : q;
-    if (lane == 0) row[cols + g] = (uint8_t)s;
-    if (g == 0)
-      for (int i = cols + groups + lane; i < pitch; i += 32) row[i] = 0;
+      for (int k = 0; k < V / 4; ++k) {
+        q[k] = ck_code2(make_float2(t[4 * k], t[4 * k + 1]), inv) |
+               ck_code2(make_float2(t[4 * k + 2], t[4 * k + 3]), inv) << 16;
+        if (s == CK_NAN) q[k] = 0u;
+      }
+      if constexpr (V == 8)
+        reinterpret_cast<uint2*>(row)[v] = make_uint2(q[0], q[1]);
+      else
+        reinterpret_cast<uint32_t*>(row)[v] = q[0];
+      if (v % (CK_GROUP / V) == 0) row[cols + v / (CK_GROUP / V)] = (uint8_t)s;
+      if (v < pad) row[cols + cols / CK_GROUP + v] = 0;
+    }
   }
 }
 
-// dg = da u sigma (1 + g (1 - sigma)), du = da g sigma.
-template <typename T>
+// dg = da u sigma (1 + g (1 - sigma)), du = da g sigma: a thread V channels.
+template <typename T, int V>
 __global__ void __launch_bounds__(256)
     swiglu_bwd_kernel(const T* __restrict__ gu, const T* __restrict__ da, T* __restrict__ dgu,
                       const int* __restrict__ end, int rows, int f) {
-  const long long n = (long long)(end ? min(rows, *end) : rows) * f;
+  constexpr int P = (V + 1) / 2;
+  const int vpr = f / V;
+  const long long n = (long long)(end ? min(rows, *end) : rows) * vpr;
   for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
-    const long long r = i / f;
-    const int c = (int)(i - r * f);
+    const long long r = i / vpr;
+    const int c = (int)(i - r * vpr) * V;
     const long long o = r * 2 * f + c;
-    const float g = to_f32(gu[o]), u = to_f32(gu[o + f]), d = to_f32(da[i]);
-    const float sig = sigmoid_of(g);
-    dgu[o] = from_f32<T>(d * u * sig * (1.f + g * sigmoid_of(-g)));
-    dgu[o + f] = from_f32<T>(d * g * sig);
+    float2 g[P], u[P], d[P];
+    load_vec<V>(gu + o, g);
+    load_vec<V>(gu + o + f, u);
+    load_vec<V>(da + r * f + c, d);
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      const float2 sx = sigmoid2(g[k].x), sy = sigmoid2(g[k].y);
+      const float2 ds = __fmul2_rn(d[k], make_float2(sx.x, sy.x));
+      u[k] = __fmul2_rn(ds, u[k]);
+      u[k].x *= fmaf(g[k].x, sx.y, 1.f);
+      u[k].y *= fmaf(g[k].y, sy.y, 1.f);
+      g[k] = __fmul2_rn(ds, g[k]);
+    }
+    store_vec<V>(dgu + o, u);
+    store_vec<V>(dgu + o + f, g);
   }
 }
 
@@ -187,16 +316,12 @@ cudaError_t combine_bwd_t(int tokens, int top_k, int rows, int d, const void* do
                           const float* weight, const int* row, const int* pair, const int* end,
                           void* dy, float* dweight, cudaStream_t st) {
   LaunchScope ls_("combine_bwd", st);
-  const int grid = grid_for(std::max(tokens, 1), 152 * 8);
+  const int grid = grid_for(std::max(((long long)rows + 7) / 8, ((long long)tokens * top_k + 255) / 256),
+                            152 * 8);
   const T *g = static_cast<const T*>(dout), *f = static_cast<const T*>(y);
-  if (d % 8 == 0)
-    combine_bwd_kernel<T, 8><<<grid, 256, 0, st>>>(g, f, weight, row, pair, end,
-                                                   static_cast<T*>(dy), dweight, tokens, top_k,
-                                                   rows, d);
-  else
-    combine_bwd_kernel<T, 1><<<grid, 256, 0, st>>>(g, f, weight, row, pair, end,
-                                                   static_cast<T*>(dy), dweight, tokens, top_k,
-                                                   rows, d);
+  auto k = d % vec16<T> == 0 ? combine_bwd_kernel<T> : combine_bwd1_kernel<T>;
+  k<<<grid, 256, 0, st>>>(g, f, weight, row, pair, end, static_cast<T*>(dy), dweight, tokens,
+                          top_k, rows, d);
   return cudaGetLastError();
 }
 
@@ -229,17 +354,32 @@ cudaError_t launch_combine_bwd(int tokens, int top_k, int rows, int d, bool fp32
                                              end, dy, dweight, st);
 }
 
+namespace {
+template <typename T>
+void swiglu_t(int rows, int f, const void* gu, const int* end, void* ck, cudaStream_t st) {
+  const int grid = grid_for(((long long)rows + 1) / 2, 152 * 8);
+  auto k = f % 8 == 0 ? swiglu_kernel<T, 8> : swiglu_kernel<T, 4>;
+  k<<<grid, 256, 0, st>>>(static_cast<const T*>(gu), static_cast<uint8_t*>(ck), end, rows, f);
+}
+template <typename T>
+void swiglu_bwd_t(int rows, int f, const void* gu, const void* da, const int* end, void* dgu,
+                  cudaStream_t st) {
+  const int v = f % 8 == 0 ? 8 : 1;
+  const int grid = grid_for(((long long)rows * (f / v) + 255) / 256, 152 * 8);
+  auto k = v == 8 ? swiglu_bwd_kernel<T, 8> : swiglu_bwd_kernel<T, 1>;
+  k<<<grid, 256, 0, st>>>(static_cast<const T*>(gu), static_cast<const T*>(da),
+                          static_cast<T*>(dgu), end, rows, f);
+}
+}  // namespace
+
 cudaError_t launch_swiglu_fwd(int rows, int f, bool fp32, const void* gu, const int* end, void* ck,
                               cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
   LaunchScope ls_("swiglu", st);
-  const int grid = grid_for(((long long)rows * (ck_cols(f) / CK_GROUP) + 7) / 8, 152 * 8);
   if (fp32)
-    swiglu_kernel<float><<<grid, 256, 0, st>>>(static_cast<const float*>(gu),
-                                               static_cast<uint8_t*>(ck), end, rows, f);
+    swiglu_t<float>(rows, f, gu, end, ck, st);
   else
-    swiglu_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(gu),
-                                                       static_cast<uint8_t*>(ck), end, rows, f);
+    swiglu_t<__nv_bfloat16>(rows, f, gu, end, ck, st);
   return cudaGetLastError();
 }
 
@@ -247,15 +387,10 @@ cudaError_t launch_swiglu_bwd(int rows, int f, bool fp32, const void* gu, const 
                               const int* end, void* dgu, cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
   LaunchScope ls_("swiglu_bwd", st);
-  const int grid = grid_for(((long long)rows * f + 255) / 256, 152 * 8);
   if (fp32)
-    swiglu_bwd_kernel<float><<<grid, 256, 0, st>>>(
-        static_cast<const float*>(gu), static_cast<const float*>(da), static_cast<float*>(dgu),
-        end, rows, f);
+    swiglu_bwd_t<float>(rows, f, gu, da, end, dgu, st);
   else
-    swiglu_bwd_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(
-        static_cast<const __nv_bfloat16*>(gu), static_cast<const __nv_bfloat16*>(da),
-        static_cast<__nv_bfloat16*>(dgu), end, rows, f);
+    swiglu_bwd_t<__nv_bfloat16>(rows, f, gu, da, end, dgu, st);
   return cudaGetLastError();
 }
 

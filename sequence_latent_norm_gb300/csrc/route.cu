@@ -1,14 +1,18 @@
 // Routing to experts (include/laga.h: laga_route_fwd, laga_route_bwd).
 //
 // Forward, one warp per token, expert e = 32 i + lane in register i of a lane:
-// scores, the groups' two best, and top_k rounds of a warp-wide maximum.  The
-// order of close scores must not depend on how a score was rounded, so every
-// decision is checked: the choice runs in fp32, and where the distance between
-// two neighbours of the order is within what fp32 may have lost, the token's
-// choice runs again in fp64.  (Equal logits under equal biases are equal in
-// both, and no reason to.)  Normal logits of 256 experts take the second run
-// in about one token of 10^4; a batch of which every token takes it costs 2
-// operations a clock and SM, the fp64 rate of this part.
+// scores, the groups' two best, and top_k rounds of a warp-wide maximum (one
+// redux.sync for the value, one for the lowest expert that has it).  The order
+// of close scores must not depend on how a score was rounded, so every decision
+// is checked: the choice runs in fp32, and where the distance between two
+// neighbours of the order is within what fp32 may have lost, it
+// is settled in fp64: that of the chosen experts and of those just below them by
+// one score a lane (about a token in 1000 of random logits of 256 experts), a
+// choice of groups, or of more experts than that, by going over the token again.
+// (Equal logits under equal biases are equal in both, and no reason to.)  fp64
+// runs at 2 operations a clock and SM on this part: a second run of the whole
+// token costs 10 us of latency, and with one for every close score the kernel
+// took 78 us for 16384 x 256, and 46 us without any.
 //
 // The order of the rows: a block counts its chunk's rows by expert; the second
 // kernel (the same one, where the batch is one chunk) adds up the chunks in
@@ -43,99 +47,94 @@ template <typename F> LAGA_DEVINL F minus_inf();
 template <> LAGA_DEVINL float minus_inf<float>() { return __int_as_float(0xff800000); }
 template <> LAGA_DEVINL double minus_inf<double>() { return __longlong_as_double(0xfff0000000000000LL); }
 
-LAGA_DEVINL float exp_of(float x) { return expf(x); }
-LAGA_DEVINL double exp_of(double x) { return exp(x); }
-
-template <typename F>
-LAGA_DEVINL F warp_add(F v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(ALL, v, o);
-  return v;
-}
 LAGA_DEVINL float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(ALL, v, o));
   return v;
 }
 
-// One lane's part of a token: its experts' logits and biases.
-template <int NV>
-struct Lane {
-  float l[NV], b[NV];
-};
-
-// The best of the values that a lane still has, with what belongs to it.
-template <typename F>
-struct Best {
-  F v, s;
-  float l, b;
-  int e;
-};
-
-// Value and expert of the warp's best, the lowest expert of equal ones.
-LAGA_DEVINL void warp_best(float v, int e, float& bv, int& be) {
+// A float's bits in the order of the values.
+LAGA_DEVINL unsigned key_of(float v) {
   const unsigned u = __float_as_uint(v);
-  const unsigned key = u & 0x80000000u ? ~u : u | 0x80000000u;
-  const unsigned top = __reduce_max_sync(ALL, key);
-  bv = __uint_as_float(top & 0x80000000u ? top & 0x7fffffffu : ~top);
-  be = (int)__reduce_min_sync(ALL, key == top ? (unsigned)e : 0x7fffffffu);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-LAGA_DEVINL void warp_best(double v, int e, double& bv, int& be) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const double w = __shfl_xor_sync(ALL, v, o);
-    const int f = __shfl_xor_sync(ALL, e, o);
-    if (w > v || (w == v && f < e)) {
-      v = w;
-      e = f;
-    }
+LAGA_DEVINL float value_of(unsigned key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+constexpr unsigned KEY_OFF = 0x007fffffu;   // of -inf
+
+// The token's logit as the choice sees it, and whether it is a NaN (or as good
+// as one: a softmax with an infinity).
+template <typename T>
+LAGA_DEVINL float logit_of(const RouteParams& p, const T* l, int e, float b, bool& nan) {
+  float x = e < p.experts ? to_f32(l[e]) : minus_inf<float>();
+  if (isnan(x) || isnan(b) || (!p.sigmoid && x > 3.402823466e38f)) {
+    nan = true;
+    x = minus_inf<float>();
   }
-  bv = v;
-  be = e;
+  return x;
+}
+LAGA_DEVINL float bias_of(const RouteParams& p, int e) {
+  return p.bias && e < p.experts ? p.bias[e] : 0.f;
 }
 
-// The token's choice in F: lane j's expert (-1: none) and score.  False: the
-// fp32 order is not certain.
-template <int NV, typename F>
-LAGA_DEVINL bool choose(const RouteParams& p, const Lane<NV>& x, int lane, int& expert, F& score) {
-  constexpr bool CHECK = sizeof(F) == 4;
-  const F ninf = minus_inf<F>();
-  F s[NV], c[NV];
-  float top = 0.f;
-  if (!p.sigmoid) {
-    top = x.l[0];
+// The sum of a softmax's exponentials in 64 bits.
+template <int NV>
+LAGA_DEVINL double wide_sum(const float (&x)[NV], float top) {
+  double z = 0.0;
 #pragma unroll
-    for (int i = 1; i < NV; ++i) top = fmaxf(top, x.l[i]);
+  for (int i = 0; i < NV; ++i) z += exp((double)x[i] - (double)top);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(ALL, z, o);
+  return z;
+}
+LAGA_DEVINL double wide_score(const RouteParams& p, float x, float top, double z) {
+  return p.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - (double)top) / z;
+}
+
+// The choice in 64 bits: lane j's expert, -1 for none.
+template <int NV, typename T>
+__device__ __noinline__ int choose_wide(const RouteParams& p, const T* l, int lane) {
+  const double ninf = minus_inf<double>();
+  double c[NV], z = 1.0;
+  float x[NV], top = 0.f;
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    x[i] = logit_of(p, l, 32 * i + lane, bias_of(p, 32 * i + lane), nan);
+  if (!p.sigmoid) {
+    top = x[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) top = fmaxf(top, x[i]);
     top = warp_max(top);
     if (!(top > minus_inf<float>())) top = 0.f;
-    F z = F(0);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      s[i] = exp_of(F(x.l[i]) - F(top));
-      z += s[i];
-    }
-    z = warp_add(z);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] = z > F(0) ? s[i] / z : F(0);
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] = F(1) / (F(1) + exp_of(-F(x.l[i])));
+    z = wide_sum<NV>(x, top);
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    c[i] = s[i] + F(x.b[i]);
-    if (x.l[i] == minus_inf<float>() || !(c[i] > ninf)) c[i] = ninf;
+    c[i] = wide_score(p, x[i], top, z) + (double)bias_of(p, 32 * i + lane);
+    if (!(x[i] > minus_inf<float>()) || !(c[i] > ninf)) c[i] = ninf;
   }
-  bool sure = true;
-  if (p.top_groups < p.groups) {
-    F mine = ninf;                       // lane g: the score of group g
-    for (int g = 0; g < p.groups; ++g) {
-      const int e0 = g * p.group_size, e1 = e0 + p.group_size;
-      F a = ninf, b = ninf;
+  auto best_of = [&](double v, int e, double& bv, int& be) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int e = 32 * i + lane;
-        if (e >= e0 && e < e1) {
+    for (int o = 16; o > 0; o >>= 1) {
+      const double w = __shfl_xor_sync(ALL, v, o);
+      const int f = __shfl_xor_sync(ALL, e, o);
+      if (w > v || (w == v && f < e)) {
+        v = w;
+        e = f;
+      }
+    }
+    bv = v;
+    be = e;
+  };
+  if (p.top_groups < p.groups) {
+    double mine = ninf;                    // lane g: the score of group g
+    for (int g = 0; g < p.groups; ++g) {
+      double a = ninf, b = ninf;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if ((32 * i + lane) / p.group_size == g) {
           if (c[i] > a) {
             b = a;
             a = c[i];
@@ -143,73 +142,246 @@ LAGA_DEVINL bool choose(const RouteParams& p, const Lane<NV>& x, int lane, int& 
             b = c[i];
           }
         }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const F a2 = __shfl_xor_sync(ALL, a, o), b2 = __shfl_xor_sync(ALL, b, o);
-        b = a > a2 ? (b > a2 ? b : a2) : (a > b2 ? a : b2);
-        a = a > a2 ? a : a2;
-      }
-      if (lane == g) mine = b > ninf ? a + b : a;
+      double first, second;
+      int owner, none;
+      best_of(a, lane, first, owner);
+      best_of(lane == owner ? b : a, lane, second, none);
+      if (lane == g) mine = second > ninf ? first + second : first;
     }
     int rank = 0;
     for (int g = 0; g < p.groups; ++g) {
-      const F other = __shfl_sync(ALL, mine, g);
+      const double other = __shfl_sync(ALL, mine, g);
+      rank += other > mine || (other == mine && g < lane);
+    }
+    const unsigned keep = __ballot_sync(ALL, lane < p.groups && rank < p.top_groups);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (!(keep >> ((32 * i + lane) / p.group_size & 31) & 1u)) c[i] = ninf;
+  }
+  int expert = -1;
+  for (int j = 0; j < p.top_k; ++j) {
+    double v = ninf, bv;
+    int e = 1 << 30, be;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (c[i] > v) {
+        v = c[i];
+        e = 32 * i + lane;
+      }
+    best_of(v, e, bv, be);
+    if (!(bv > ninf)) break;
+    if (lane == j) expert = be;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (32 * i + lane == be) c[i] = ninf;
+  }
+  return expert;
+}
+
+// The lanes' experts in the order of their sums in 64 bits; the ones of `all`
+// lanes, of which the best top_k stay.
+template <int NV>
+__device__ __noinline__ int reorder_wide(const RouteParams& p, const float (&x)[NV], float top,
+                                         float l, float b, int expert, int all, int lane) {
+  const double z = p.sigmoid ? 1.0 : wide_sum<NV>(x, top);
+  const double c = expert >= 0 ? wide_score(p, l, top, z) + (double)b : minus_inf<double>();
+  int rank = 0;
+  for (int j = 0; j < all; ++j) {
+    const double other = __shfl_sync(ALL, c, j);
+    const int e = __shfl_sync(ALL, expert, j);
+    rank += other > c || (other == c && e < expert);
+  }
+  int out = -1;
+  for (int j = 0; j < all; ++j) {
+    const int r = __shfl_sync(ALL, rank, j), e = __shfl_sync(ALL, expert, j);
+    if (r == lane) out = e;
+  }
+  return out;
+}
+
+// fp32 scores of the experts that the lanes have chosen (0 for none).
+template <int NV, typename T>
+LAGA_DEVINL float score_of(const RouteParams& p, const T* l, const float (&x)[NV], int lane,
+                           int expert) {
+  float top = 0.f, z = 1.f;
+  if (!p.sigmoid) {
+    top = x[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) top = fmaxf(top, x[i]);
+    top = warp_max(top);
+    z = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) z += expf(x[i] - top);
+    z = warp_sum(z);
+  }
+  if (expert < 0) return 0.f;
+  const float v = to_f32(l[expert]);
+  return p.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - top) / z;
+}
+
+// The choice in fp32: lane j's expert.  `score`: its score.  False: the order is
+// not certain.
+template <int NV, typename T>
+LAGA_DEVINL bool choose(const RouteParams& p, const T* l, const float (&x)[NV],
+                        const float (&bias)[NV], const int (&group)[NV], int lane, int& expert,
+                        float& score) {
+  const float ninf = minus_inf<float>();
+  unsigned key[NV];
+  float top = 0.f, inv = 0.f;
+  if (!p.sigmoid) {
+    top = x[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) top = fmaxf(top, x[i]);
+    top = value_of(__reduce_max_sync(ALL, key_of(top)));
+    if (!(top > ninf)) top = 0.f;
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) z += expf(x[i] - top);
+    z = warp_sum(z);
+    inv = z > 0.f ? 1.f / z : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float s;
+    if (p.sigmoid) {
+      // within (1.25 |x| + 9) 2^-24 of itself; the weight is computed again
+      float e;
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x[i] * -1.44269504f));
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+    } else {
+      s = expf(x[i] - top) * inv;
+    }
+    const float c = s + bias[i];
+    key[i] = x[i] > ninf && c > ninf ? key_of(c) : KEY_OFF;
+  }
+  // What fp32 may have lost of a score.  Of a sigmoid s: (1 - s) (1.25 |x| + 4)
+  // units of its last place (the exponential's error) and three roundings, no
+  // more than 6 units of 2^-24 of one for any x.  Of a softmax: the rounded
+  // difference's and the exponential's, and its sum's; no score is above inv.
+  const float lost = (p.sigmoid ? 6.f : (13.f + NV) * inv) * 0x1p-24f;
+  bool sure = true;
+  if (p.top_groups < p.groups) {
+    float mine = ninf;                     // lane g: the score of group g
+    auto two_best = [&](int g, unsigned a, unsigned b) {
+      const unsigned first = __reduce_max_sync(ALL, a);
+      const int owner = __ffs(__ballot_sync(ALL, a == first)) - 1;
+      const unsigned second = __reduce_max_sync(ALL, lane == owner ? b : a);
+      if (lane == g)
+        mine = second > KEY_OFF ? value_of(first) + value_of(second) : value_of(first);
+    };
+    if (p.group_size % 32 == 0) {          // groups of whole registers
+      const int regs = p.group_size / 32;
+      unsigned a = KEY_OFF, b = KEY_OFF;
+      int left = regs, g = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        b = max(b, min(a, key[i]));
+        a = max(a, key[i]);
+        if (--left == 0) {
+          if (g < p.groups) two_best(g, a, b);
+          ++g;
+          left = regs;
+          a = b = KEY_OFF;
+        }
+      }
+    } else {
+      for (int g = 0; g < p.groups; ++g) {
+        const int e0 = g * p.group_size, e1 = e0 + p.group_size;
+        unsigned a = KEY_OFF, b = KEY_OFF;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          if (32 * i + 31 < e0 || 32 * i >= e1) continue;   // the same for all lanes
+          const int e = 32 * i + lane;
+          const unsigned k = e >= e0 && e < e1 ? key[i] : KEY_OFF;
+          b = max(b, min(a, k));
+          a = max(a, k);
+        }
+        two_best(g, a, b);
+      }
+    }
+    int rank = 0;
+    for (int g = 0; g < p.groups; ++g) {
+      const float other = __shfl_sync(ALL, mine, g);
       rank += other > mine || (other == mine && g < lane);
     }
     if (lane >= p.groups) rank = 64;
     const unsigned keep = __ballot_sync(ALL, rank < p.top_groups);
-    if (CHECK) {
-      const F in = __shfl_sync(ALL, mine, __ffs(__ballot_sync(ALL, rank == p.top_groups - 1)) - 1);
-      const F out = __shfl_sync(ALL, mine, __ffs(__ballot_sync(ALL, rank == p.top_groups)) - 1);
-      // each of the four scores is within 2^-22, each sum within 2^-24 of itself
-      const F tol = F(2.f + fabsf(float(in)) + fabsf(float(out))) * F(0x1p-20f);
-      sure = !(out > ninf) || in - out > tol;
-    }
+    const float in = __shfl_sync(ALL, mine, __ffs(__ballot_sync(ALL, rank == p.top_groups - 1)) - 1);
+    const float out = __shfl_sync(ALL, mine, __ffs(__ballot_sync(ALL, rank == p.top_groups)) - 1);
+    // four scores, their sums with the biases, and the sums of two
+    const float tol = 4.f * lost + (4.f + 4.f * (fabsf(in) + fabsf(out))) * 0x1p-24f;
+    sure = !(out > ninf) || in - out > tol;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (!(keep >> ((32 * i + lane) / p.group_size) & 1u)) c[i] = ninf;
+      if (!(keep >> group[i] & 1u)) key[i] = KEY_OFF;
   }
-  Best<F> best;
-  auto rescan = [&] {
-    best = Best<F>{c[0], s[0], x.l[0], x.b[0], lane};
-#pragma unroll
-    for (int i = 1; i < NV; ++i)
-      if (c[i] > best.v) best = Best<F>{c[i], s[i], x.l[i], x.b[i], 32 * i + lane};
-  };
-  rescan();
+  // rounds: lane j keeps the j-th best
+  float value = ninf;
   expert = -1;
-  score = F(0);
-  Best<F> last{};
-  for (int j = 0; j < p.top_k + (CHECK ? 1 : 0); ++j) {
-    Best<F> now;
-    warp_best(best.v, best.e, now.v, now.e);
-    if (!(now.v > ninf)) break;
-    const int owner = now.e & 31;
-    now.s = __shfl_sync(ALL, best.s, owner);
-    if (CHECK) {
-      now.l = __shfl_sync(ALL, best.l, owner);
-      now.b = __shfl_sync(ALL, best.b, owner);
-      if (j > 0 && !(now.l == last.l && now.b == last.b)) {
-        // a score is off by 8 units in its last place, and where it is the
-        // exponential of a rounded difference by that rounding; its sum by one
-        const float range = p.sigmoid ? 0.f : top - now.l;
-        const float tol = (float(now.s) + float(last.s)) * (16.f + 2.f * range) * 0x1p-24f +
-                          (fabsf(float(now.v)) + fabsf(float(last.v))) * 0x1p-22f;
-        sure = sure && float(last.v) - float(now.v) > tol;
-      }
-      last = now;
-    }
-    if (j < p.top_k && lane == j) {
-      expert = now.e;
-      score = now.s;
-    }
-    if (lane == owner) {
+  int found = 0;
+  auto round = [&](float least) {
+    unsigned best = key[0];
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (32 * i + lane == now.e) c[i] = ninf;
-      rescan();
+    for (int i = 1; i < NV; ++i) best = max(best, key[i]);
+    const unsigned first = __reduce_max_sync(ALL, best);
+    if (first <= KEY_OFF || !(value_of(first) >= least)) return false;
+    unsigned e = 0x7fffffffu;
+#pragma unroll
+    for (int i = NV - 1; i >= 0; --i)
+      if (key[i] == first) e = 32 * i + lane;
+    e = __reduce_min_sync(ALL, e);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (32 * i + lane == (int)e) key[i] = KEY_OFF;
+    if (lane == found) {
+      expert = (int)e;
+      value = value_of(first);
     }
+    ++found;
+    return true;
+  };
+  while (found < min(p.top_k + 1, 32) && round(ninf)) {
+  }
+  // the chosen ones' scores, and the distance of each from the next (of the last
+  // one from the best that was not chosen)
+  float mine = 0.f, b = 0.f;
+  auto look = [&] {
+    score = 0.f;
+    if (expert >= 0) {
+      bool nan;
+      mine = logit_of(p, l, expert, 0.f, nan);
+      b = bias_of(p, expert);
+      score = p.sigmoid ? 1.f / (1.f + expf(-mine)) : expf(mine - top) * inv;
+    }
+  };
+  look();
+  const unsigned next = min(lane + 1, 31);
+  const float v1 = __shfl_sync(ALL, value, next), l1 = __shfl_sync(ALL, mine, next);
+  const float b1 = __shfl_sync(ALL, b, next);
+  const int e1 = __shfl_sync(ALL, expert, next);
+  // (equal ones at the end may have others next to them that were not looked at)
+  const bool equal = mine == l1 && b == b1 && lane + 1 < p.top_k;
+  const bool close = lane < min(p.top_k, 31) && expert >= 0 && e1 >= 0 && !equal &&
+                     !(value - v1 > 2.f * lost + (fabsf(value) + fabsf(v1)) * 0x1p-24f);
+  if (__any_sync(ALL, close) || p.top_k == 32) {
+    // everything that may belong to the best top_k, whose last one may have lost
+    // as much as what is below it
+    const int last = min(p.top_k, found) - 1;
+    if (last >= 0) {
+      const float least = __shfl_sync(ALL, value - 2.5f * lost - fabsf(value) * 0x1p-22f, last);
+      while (found < 32 && round(least)) {
+      }
+      // a full warp may have left some out; infinities have no distance
+      if (found == 32 || !(fabsf(least) <= 3.402823466e38f)) return false;
+      look();
+      expert = reorder_wide<NV>(p, x, top, mine, b, expert, found, lane);
+      if (lane >= p.top_k) expert = -1;
+      look();
+    }
+  }
+  if (lane >= p.top_k) {
+    expert = -1;
+    score = 0.f;
   }
   return sure;
 }
@@ -316,30 +488,24 @@ __global__ void __launch_bounds__(route_threads<NV>())
   const int t0 = blockIdx.x * p.chunk, t1 = min(p.tokens, t0 + p.chunk);
   for (int e = threadIdx.x; e < p.local; e += blockDim.x) smem[e] = 0;
   __syncthreads();
-  Lane<NV> x;
+  float bias[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = 32 * i + lane;
-    x.b[i] = p.bias && e < p.experts ? p.bias[e] : 0.f;
-  }
+  for (int i = 0; i < NV; ++i) bias[i] = bias_of(p, 32 * i + lane);
+  int group[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) group[i] = min((32 * i + lane) / p.group_size, 31);
   for (int t = t0 + warp; t < t1; t += warps) {
+    const T* l = logits + (long long)t * p.experts;
     bool nan = false;
+    float x[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = 32 * i + lane;
-      x.l[i] = e < p.experts ? to_f32(logits[(long long)t * p.experts + e]) : minus_inf<float>();
-      if (isnan(x.l[i]) || isnan(x.b[i]) || (!p.sigmoid && x.l[i] > 3.402823466e38f)) {
-        nan = true;                       // (a softmax with an infinity is one, too)
-        x.l[i] = minus_inf<float>();
-      }
-    }
+    for (int i = 0; i < NV; ++i) x[i] = logit_of(p, l, 32 * i + lane, bias[i], nan);
     nan = __any_sync(ALL, nan);
     int expert;
     float score;
-    if (!choose<NV, float>(p, x, lane, expert, score)) {
-      double wide;
-      choose<NV, double>(p, x, lane, expert, wide);
-      score = (float)wide;
+    if (!choose<NV, T>(p, l, x, bias, group, lane, expert, score)) {
+      expert = choose_wide<NV, T>(p, l, lane);
+      score = score_of(p, l, x, lane, expert);
     }
     const float total = warp_sum(score) + TINY;
     float w = p.scale * (p.renormalise ? score / total : score);

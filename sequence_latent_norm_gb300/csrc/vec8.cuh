@@ -52,4 +52,31 @@ LAGA_DEVINL void store_vec(__nv_bfloat16* p, const float2 (&f)[(V + 1) / 2]) {
   }
 }
 
+// Vectors of 16 bytes (8 bf16 or 4 fp32) that stay packed until they are used.
+template <typename T>
+constexpr int vec16 = 16 / (int)sizeof(T);
+LAGA_DEVINL void open16(const uint4& w, const float*, float2 (&f)[2]) {
+  f[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+  f[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
+}
+LAGA_DEVINL void open16(const uint4& w, const __nv_bfloat16*, float2 (&f)[4]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    f[k] = make_float2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xffff0000u));
+}
+LAGA_DEVINL uint4 close16(const float*, const float2 (&f)[2]) {
+  return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x),
+                    __float_as_uint(f[1].y));
+}
+LAGA_DEVINL uint4 close16(const __nv_bfloat16*, const float2 (&f)[4]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f[k].x, f[k].y);
+    u[k] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
 }  // namespace laga

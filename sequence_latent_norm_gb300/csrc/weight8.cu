@@ -3,32 +3,49 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "ops.h"
+#include "vec8.cuh"
 
 namespace laga {
 namespace {
 
-// ------------------------------------------------------------------ weights
 // A block takes one 128 x 128 block of W: its maximum, its codes, and these as
-// 128-byte pieces of the rows of W^T (fwd) and of W (bwd).
-constexpr int WB = CK_GROUP, W_LD = WB + 4;
+// 128-byte pieces of the rows of W^T (fwd) and of W (bwd).  A thread loads 8
+// columns of 8 rows.  The codes are turned in shared memory in words of 4: word w
+// of row r sits at w ^ (r / 4), so that reading rows 4 l .. 4 l + 3 of one word by
+// lane l, like writing, meets every bank once.
+constexpr int WB = CK_GROUP;
 
-template <typename T>
+template <typename T, int V>
 __global__ void __launch_bounds__(256)
     weight_pack_kernel(const T* __restrict__ w, uint8_t* __restrict__ fwd,
                        uint8_t* __restrict__ bwd, int K, int N) {
-  __shared__ uint8_t tile[WB * W_LD];
+  __shared__ uint32_t tile[WB][WB / 4];
   __shared__ float part[8];
   const int nb = blockIdx.x, kb = blockIdx.y, e = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31;
   const T* src = w + (long long)e * K * N;
-  const int c = tid & 127, r0 = tid >> 7;
-  const bool in = nb * WB + c < N;
-  float v[WB / 2], m = 0.f;
+  const int c = (tid & 15) * 8, r0 = tid >> 4;
+  float2 v[8][4];
+  float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < WB / 2; ++i) {
-    const int k = kb * WB + r0 + 2 * i;
-    v[i] = in && k < K ? to_f32(src[(long long)k * N + nb * WB + c]) : 0.f;
-    m = ck_max(m, v[i]);
+  for (int i = 0; i < 8; ++i) {
+    const int k = kb * WB + r0 + 16 * i, n = nb * WB + c;
+    const T* p = src + (long long)k * N + n;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[i][j] = make_float2(0.f, 0.f);
+    if (k < K) {
+      if constexpr (V == 8) {
+        if (n < N) load_vec<8>(p, v[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (n + 2 * j < N) v[i][j].x = to_f32(p[2 * j]);
+          if (n + 2 * j + 1 < N) v[i][j].y = to_f32(p[2 * j + 1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = ck_max(ck_max(m, v[i][j].x), v[i][j].y);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = ck_max(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -40,10 +57,13 @@ __global__ void __launch_bounds__(256)
   float inv;
   const int s = ck_scale(m, &inv);
 #pragma unroll
-  for (int i = 0; i < WB / 2; i += 2) {
-    const uint32_t q = s == CK_NAN ? 0u : ck_code2(make_float2(v[i], v[i + 1]), inv);
-    tile[(r0 + 2 * i) * W_LD + c] = (uint8_t)q;
-    tile[(r0 + 2 * i + 2) * W_LD + c] = (uint8_t)(q >> 8);
+  for (int i = 0; i < 8; ++i) {
+    const int r = r0 + 16 * i, x = r >> 2;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t q = ck_code2(v[i][2 * h], inv) | ck_code2(v[i][2 * h + 1], inv) << 16;
+      tile[r][(c / 4 + h) ^ x] = s == CK_NAN ? 0u : q;
+    }
   }
   __syncthreads();
   // what a row gets: a word of codes a lane, its scale byte, and behind the
@@ -54,19 +74,32 @@ __global__ void __launch_bounds__(256)
     if (b == cols / WB - 1)
       for (int i = cols + cols / WB + lane; i < pitch; i += 32) row[i] = 0;
   };
-  for (int n = tid >> 5; n < WB && nb * WB + n < N; n += 8) {
-    uint8_t* row = fwd + ((long long)e * N + nb * WB + n) * pk;
-    uint32_t q = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) q |= (uint32_t)tile[(4 * lane + j) * W_LD + n] << (8 * j);
-    reinterpret_cast<uint32_t*>(row + kb * WB)[lane] = q;
-    finish(row, ck, kb, pk);
+  for (int i = 0; i < 4; ++i) {
+    // 4 rows x 4 columns of codes, turned
+    const int cw = (tid >> 5) + 8 * i;
+    uint32_t q[4], o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] = tile[4 * lane + j][cw ^ lane];
+    const uint32_t a = __byte_perm(q[0], q[1], 0x5140), b = __byte_perm(q[2], q[3], 0x5140);
+    const uint32_t d = __byte_perm(q[0], q[1], 0x7362), g = __byte_perm(q[2], q[3], 0x7362);
+    o[0] = __byte_perm(a, b, 0x5410);
+    o[1] = __byte_perm(a, b, 0x7632);
+    o[2] = __byte_perm(d, g, 0x5410);
+    o[3] = __byte_perm(d, g, 0x7632);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = nb * WB + 4 * cw + j;
+      if (n >= N) break;
+      uint8_t* row = fwd + ((long long)e * N + n) * pk;
+      reinterpret_cast<uint32_t*>(row + kb * WB)[lane] = o[j];
+      finish(row, ck, kb, pk);
+    }
   }
   if (!bwd) return;
   for (int k = tid >> 5; k < WB && kb * WB + k < K; k += 8) {
     uint8_t* row = bwd + ((long long)e * K + kb * WB + k) * pn;
-    reinterpret_cast<uint32_t*>(row + nb * WB)[lane] =
-        *reinterpret_cast<const uint32_t*>(tile + k * W_LD + 4 * lane);
+    reinterpret_cast<uint32_t*>(row + nb * WB)[lane] = tile[k][lane ^ (k >> 2)];
     finish(row, cn, nb, pn);
   }
 }
@@ -76,15 +109,16 @@ __global__ void __launch_bounds__(256)
 cudaError_t launch_weight_pack(int experts, int K, int N, bool fp32, const void* w, void* fwd,
                                void* bwd, cudaStream_t st) {
   const dim3 grid((N + WB - 1) / WB, (K + WB - 1) / WB, experts);
+  uint8_t *f = static_cast<uint8_t*>(fwd), *b = static_cast<uint8_t*>(bwd);
   LaunchScope ls_("weight_pack", st);
-  if (fp32)
-    weight_pack_kernel<<<grid, 256, 0, st>>>(static_cast<const float*>(w),
-                                             static_cast<uint8_t*>(fwd),
-                                             static_cast<uint8_t*>(bwd), K, N);
-  else
-    weight_pack_kernel<<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(w),
-                                             static_cast<uint8_t*>(fwd),
-                                             static_cast<uint8_t*>(bwd), K, N);
+  if (fp32) {
+    auto k = N % 8 == 0 ? weight_pack_kernel<float, 8> : weight_pack_kernel<float, 1>;
+    k<<<grid, 256, 0, st>>>(static_cast<const float*>(w), f, b, K, N);
+  } else {
+    auto k = N % 8 == 0 ? weight_pack_kernel<__nv_bfloat16, 8>
+                        : weight_pack_kernel<__nv_bfloat16, 1>;
+    k<<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(w), f, b, K, N);
+  }
   return cudaGetLastError();
 }
 
