@@ -199,6 +199,61 @@ __device__ __noinline__ int reorder_wide(const RouteParams& p, const float (&x)[
   return out;
 }
 
+// The choice of groups where the last one in and the first one out are close:
+// the two best of every group about there, settled in 64 bits, a group a lane.
+// 0 where it is not certain which two these are.
+template <int NV, typename T>
+__device__ __noinline__ unsigned regroup_wide(const RouteParams& p, const unsigned (&key)[NV],
+                                              const float (&x)[NV], float top, const T* l,
+                                              float mine, float in, float out, float tol,
+                                              float lost, int lane) {
+  const bool in_range = lane < p.groups;
+  const unsigned above = __ballot_sync(ALL, in_range && mine > in + tol);
+  const bool about = in_range && mine <= in + tol && mine >= out - tol;
+  int e1 = -1, e2 = -1;
+  for (unsigned left = __ballot_sync(ALL, about); left; left &= left - 1) {
+    const int g = __ffs(left) - 1;
+    int e[3] = {-1, -1, -1};
+    float v[3];
+    for (int n = 0; n < 3; ++n) {
+      unsigned best = KEY_OFF;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int f = 32 * i + lane;
+        if (f / p.group_size == g && f != e[0] && f != e[1]) best = max(best, key[i]);
+      }
+      const unsigned first = __reduce_max_sync(ALL, best);
+      v[n] = value_of(first);
+      if (first == KEY_OFF) break;
+      unsigned f0 = 0x7fffffffu;
+#pragma unroll
+      for (int i = NV - 1; i >= 0; --i) {
+        const int f = 32 * i + lane;
+        if (f / p.group_size == g && f != e[0] && f != e[1] && key[i] == first) f0 = f;
+      }
+      e[n] = (int)__reduce_min_sync(ALL, f0);
+    }
+    if (e[2] >= 0 && !(v[1] - v[2] > 2.f * lost + (fabsf(v[1]) + fabsf(v[2])) * 0x1p-23f)) return 0u;
+    if (lane == g) {
+      e1 = e[0];
+      e2 = e[1];
+    }
+  }
+  const double z = p.sigmoid ? 1.0 : wide_sum<NV>(x, top);
+  double c = minus_inf<double>();
+  if (e1 >= 0) {
+    c = wide_score(p, to_f32(l[e1]), top, z) + (double)bias_of(p, e1);
+    if (e2 >= 0) c += wide_score(p, to_f32(l[e2]), top, z) + (double)bias_of(p, e2);
+  }
+  int rank = __popc(above);
+  for (int g = 0; g < p.groups; ++g) {
+    const double other = __shfl_sync(ALL, c, g);
+    const bool rival = __shfl_sync(ALL, (int)about, g);
+    rank += rival && (other > c || (other == c && g < lane));
+  }
+  return above | __ballot_sync(ALL, about && rank < p.top_groups);
+}
+
 // fp32 scores of the experts that the lanes have chosen (0 for none).
 template <int NV, typename T>
 LAGA_DEVINL float score_of(const RouteParams& p, const T* l, const float (&x)[NV], int lane,
@@ -259,7 +314,6 @@ LAGA_DEVINL bool choose(const RouteParams& p, const T* l, const float (&x)[NV],
   // more than 6 units of 2^-24 of one for any x.  Of a softmax: the rounded
   // difference's and the exponential's, and its sum's; no score is above inv.
   const float lost = (p.sigmoid ? 6.f : (13.f + NV) * inv) * 0x1p-24f;
-  bool sure = true;
   if (p.top_groups < p.groups) {
     float mine = ninf;                     // lane g: the score of group g
     auto two_best = [&](int g, unsigned a, unsigned b) {
@@ -305,12 +359,17 @@ LAGA_DEVINL bool choose(const RouteParams& p, const T* l, const float (&x)[NV],
       rank += other > mine || (other == mine && g < lane);
     }
     if (lane >= p.groups) rank = 64;
-    const unsigned keep = __ballot_sync(ALL, rank < p.top_groups);
+    unsigned keep = __ballot_sync(ALL, rank < p.top_groups);
     const float in = __shfl_sync(ALL, mine, __ffs(__ballot_sync(ALL, rank == p.top_groups - 1)) - 1);
     const float out = __shfl_sync(ALL, mine, __ffs(__ballot_sync(ALL, rank == p.top_groups)) - 1);
     // four scores, their sums with the biases, and the sums of two
     const float tol = 4.f * lost + (4.f + 4.f * (fabsf(in) + fabsf(out))) * 0x1p-24f;
-    sure = !(out > ninf) || in - out > tol;
+    if (out > ninf && !(in - out > tol)) {
+      // (an infinite sum has no distance)
+      keep = fabsf(in) <= 3.402823466e38f
+                 ? regroup_wide<NV, T>(p, key, x, top, l, mine, in, out, tol, lost, lane) : 0u;
+      if (keep == 0u) return false;
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (!(keep >> group[i] & 1u)) key[i] = KEY_OFF;
@@ -383,7 +442,7 @@ LAGA_DEVINL bool choose(const RouteParams& p, const T* l, const float (&x)[NV],
     expert = -1;
     score = 0.f;
   }
-  return sure;
+  return true;
 }
 
 // Numbers the pairs of this block's chunk.  counts: the chunks' rows by local
@@ -401,7 +460,7 @@ LAGA_DEVINL void place(const RouteParams& p, unsigned* smem) {
   for (int i = threadIdx.x; i < EL * parts; i += blockDim.x) {
     const int e = i % EL;
     unsigned before = 0, all = 0;
-#pragma unroll 8
+#pragma unroll 16
     for (int c = i / EL; c < p.chunks; c += parts) {
       const unsigned n = p.counts[(size_t)c * EL + e];
       all += n;
@@ -440,7 +499,8 @@ LAGA_DEVINL void place(const RouteParams& p, unsigned* smem) {
   }
   const int t0 = blockIdx.x * p.chunk, t1 = min(p.tokens, t0 + p.chunk);
   const int n = (t1 - t0) * p.top_k;
-  const int share = ((n + warps - 1) / warps + 31) / 32 * 32;
+  const int share = max(((n + warps - 1) / warps + 31) / 32 * 32, 64);
+  const int busy = min(warps, (n + share - 1) / share);
   const int i0 = warp * share, i1 = min(n, i0 + share);
   const long long off = (long long)t0 * p.top_k;
   unsigned* h = hist + warp * EL;
@@ -454,7 +514,8 @@ LAGA_DEVINL void place(const RouteParams& p, unsigned* smem) {
   __syncthreads();
   for (int e = threadIdx.x; e < EL; e += blockDim.x) {
     unsigned at = base[e];
-    for (int w = 0; w < warps; ++w) {
+#pragma unroll 4
+    for (int w = 0; w < busy; ++w) {
       const unsigned c = hist[w * EL + e];
       hist[w * EL + e] = at;
       at += c;
@@ -491,16 +552,30 @@ __global__ void __launch_bounds__(route_threads<NV>())
   float bias[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) bias[i] = bias_of(p, 32 * i + lane);
+  bool bad_bias = false;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) bad_bias = bad_bias || isnan(bias[i]);
   int group[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) group[i] = min((32 * i + lane) / p.group_size, 31);
   for (int t = t0 + warp; t < t1; t += warps) {
     const T* l = logits + (long long)t * p.experts;
-    bool nan = false;
-    float x[NV];
+    float x[NV], most = minus_inf<float>();   // the largest, or a NaN
 #pragma unroll
-    for (int i = 0; i < NV; ++i) x[i] = logit_of(p, l, 32 * i + lane, bias[i], nan);
-    nan = __any_sync(ALL, nan);
+    for (int i = 0; i < NV; ++i) {
+      const int e = 32 * i + lane;
+      x[i] = e < p.experts ? to_f32(l[e]) : minus_inf<float>();
+      asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(x[i]));
+    }
+    bool nan = __any_sync(ALL, isnan(most) || bad_bias ||
+                                   (!p.sigmoid && most > 3.402823466e38f));
+    if (nan) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        bool off = false;
+        x[i] = logit_of(p, l, 32 * i + lane, bias[i], off);
+      }
+    }
     int expert;
     float score;
     if (!choose<NV, T>(p, l, x, bias, group, lane, expert, score)) {
