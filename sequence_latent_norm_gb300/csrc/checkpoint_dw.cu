@@ -116,6 +116,7 @@ struct DwParams {
   const float* gamma;
   float *dw, *frag;
   int* err;
+  int wide;                // dw and frag start on 32 bytes
   // by expert; `tiles` is one expert's, and rounds are of all experts'
   int experts, rows;
   const int* start;        // first row of each expert, whole steps
@@ -280,6 +281,14 @@ LAGA_DEVINL void decode16(const uint4& q, uint32_t byte, uint4& a, uint4& b) {
     a = make_uint4(mul_bf16x2(a.x, n), mul_bf16x2(a.y, n), mul_bf16x2(a.z, n), mul_bf16x2(a.w, n));
     b = make_uint4(mul_bf16x2(b.x, n), mul_bf16x2(b.y, n), mul_bf16x2(b.z, n), mul_bf16x2(b.w, n));
   }
+}
+
+// Eight floats to a 32-byte boundary.
+LAGA_DEVINL void store32(float* p, const float2* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0].x),
+               "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x),
+               "f"(v[3].y)
+               : "memory");
 }
 
 // Whether a phase has completed, without waiting for it.
@@ -500,25 +509,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane == 0 && polls) mbar_arrive_cluster(smem_cluster_addr(&acc_empty[buf], 0));
       }
-      const int r = (int)rank * CK_GROUP + channel_of(q * 32 + lane);   // row of the pair's tile
-      const int row = (w.t / p.n_tiles) * 256 + r, n0 = (w.t % p.n_tiles) * BN + c0;
-      if (polls && row < p.d) {
-        const float gain = p.gamma ? p.gamma[row] : 1.f;
-        float* dst = w.frag >= 0 ? p.frag + ((long long)w.frag * 256 + r) * BN + c0
-                                 : p.dw + (w.out_row(p) + row) * p.n + n0;
-        const int lim = w.frag >= 0 ? HALF : p.n - n0;           // columns that exist
-        if (w.frag >= 0 || p.n % 4 == 0) {
+      const int m0 = (w.t / p.n_tiles) * 256 + (int)rank * CK_GROUP;   // first channel
+      const int r = channel_of(q * 32 + lane), n0 = (w.t % p.n_tiles) * BN + c0;
+      const bool piece = w.frag >= 0;
+      const float gain = p.gamma && m0 + r < p.d ? p.gamma[m0 + r] : 1.f;
+#pragma unroll
+      for (int j = 0; j < HALF / 2; ++j) acc[j] = __fmul2_rn(acc[j], make_float2(gain, gain));
+      float* out = piece ? p.frag + ((long long)w.frag * 256 + (int)rank * CK_GROUP) * BN + c0
+                         : p.dw + (w.out_row(p) + m0) * p.n + n0;
+      const long long ld = piece ? BN : p.n;
+      const int lim = piece ? HALF : p.n - n0;            // columns that exist
+      const int rows = piece ? CK_GROUP : p.d - m0;       // channels that exist
+      if (!polls) continue;
+      if (p.wide && (piece || p.n % 8 == 0)) {
+        // 32 columns at a time: four neighbouring lanes turn 4 rows x 32 columns
+        // into 8 columns of all four rows each, so that a store of 32 bytes a lane
+        // covers 128 of a row.  (8 experts of 2048 rows, 2048 x 7168: 580 us with
+        // 16-byte stores of a row a lane, 489 us with 32-byte ones.)
+#pragma unroll
+        for (int g = 0; g < HALF / 32; ++g) {
+          float2 (&v)[16] = *reinterpret_cast<float2(*)[16]>(acc + 16 * g);
+          const bool hi = lane & 2, odd = lane & 1;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {      // columns 0-15 against 16-31
+            const float2 send = hi ? v[k] : v[8 + k];
+            float2 got;
+            got.x = __shfl_xor_sync(0xffffffffu, send.x, 2);
+            got.y = __shfl_xor_sync(0xffffffffu, send.y, 2);
+            if (hi) v[k] = v[8 + k];
+            v[8 + k] = got;                  // the own row first, then the other's
+          }
+#pragma unroll
+          for (int k = 0; k < 16; k += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {    // columns 0-7 against 8-15 of either
+              const float2 send = odd ? v[k + e] : v[k + 4 + e];
+              float2 got;
+              got.x = __shfl_xor_sync(0xffffffffu, send.x, 1);
+              got.y = __shfl_xor_sync(0xffffffffu, send.y, 1);
+              if (odd) v[k + e] = v[k + 4 + e];
+              v[k + 4 + e] = got;
+            }
+          const int col = 32 * g + 8 * (lane & 3);
+          if (col < lim) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {    // the row of lane ^ {0, 1, 2, 3}
+              const int row = channel_of(q * 32 + (lane ^ e));
+              if (row < rows) store32(out + row * ld + col, &v[4 * e]);
+            }
+          }
+        }
+      } else if (r < rows) {
+        float* dst = out + r * ld;
+        if (piece || p.n % 4 == 0) {
 #pragma unroll
           for (int j = 0; j < HALF / 4; ++j)
             if (4 * j < lim)
               reinterpret_cast<float4*>(dst)[j] =
-                  make_float4(acc[2 * j].x * gain, acc[2 * j].y * gain, acc[2 * j + 1].x * gain,
-                              acc[2 * j + 1].y * gain);
+                  make_float4(acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x, acc[2 * j + 1].y);
         } else {
 #pragma unroll
           for (int j = 0; j < HALF / 2; ++j) {
-            if (2 * j < lim) dst[2 * j] = acc[j].x * gain;
-            if (2 * j + 1 < lim) dst[2 * j + 1] = acc[j].y * gain;
+            if (2 * j < lim) dst[2 * j] = acc[j].x;
+            if (2 * j + 1 < lim) dst[2 * j + 1] = acc[j].y;
           }
         }
       }
@@ -826,6 +879,7 @@ cudaError_t launch_plan(DwPlan& pl, int rows, int d, int n, bool fp32, const voi
   }
   p.dw = dw;
   p.frag = reinterpret_cast<float*>(ws + pl.dy_bytes);
+  p.wide = (reinterpret_cast<uintptr_t>(dw) | reinterpret_cast<uintptr_t>(p.frag)) % 32 == 0;
   DwMaps tm{};
   const uint64_t pitch = ck_pitch(d);
   if ((e = byte_map(&tm.codes, ck, p.cols, rows, pitch, CK_GROUP)) != cudaSuccess) return e;
