@@ -468,13 +468,15 @@ laga_status laga_weight_pack(int experts, int k, int n, laga_dtype dtype, const 
 /* y[r, j] = sum_i a[r, i] b[e n + j, i] of 8-bit rows
  *   a [rows, laga_ckpt_row_bytes(k)]; b [max(experts, 1) n, laga_ckpt_row_bytes(k)]
  *   start [experts + 1] (device): row r is expert e's (see above); experts 0:
- *   one matrix b for all rows, start ignored
+ *   one matrix b for all rows, start and pair ignored
+ *   pair [rows] (device) or NULL: rows of no pair, fewer than 128 and an
+ *   expert's last ones, are zero in y; without it they are computed like the others
  *   y [rows, n] (output, out_dtype), 1 <= n <= 16384
  * Products are exact, sums in fp32, in an order that the sizes fix. */
 size_t laga_mm8_workspace_bytes(int rows, int k, int n, int experts, laga_dtype out_dtype);
 laga_status laga_mm8(int rows, int k, int n, int experts, laga_dtype out_dtype, const void* a,
-                     const void* b, const int* start, void* y, void* ws, size_t ws_bytes,
-                     void* stream);
+                     const void* b, const int* start, const int* pair, void* y, void* ws,
+                     size_t ws_bytes, void* stream);
 
 /* laga_ckpt_dw by expert: dw [experts, d, n], expert e over its rows of v and
  * dy; start[e] are multiples of 128, and rows that belong to no pair are zero

@@ -132,7 +132,7 @@ def load(path: str = LIB_PATH):
     lib.laga_ckpt_dw_workspace_bytes.restype = S
     Q = ctypes.POINTER(LagaRouteDims)
     for name, args in (("route_fwd", [Q] + [P] * 8 + [S, P]), ("route_bwd", [Q] + [P] * 5),
-                       ("weight_pack", [I] * 4 + [P] * 4), ("mm8", [I] * 5 + [P] * 5 + [S, P]),
+                       ("weight_pack", [I] * 4 + [P] * 4), ("mm8", [I] * 5 + [P] * 6 + [S, P]),
                        ("experts_dw", [I] * 5 + [P] * 6 + [S, P]), ("spread8", [I] * 4 + [P] * 5),
                        ("combine_fwd", [I] * 5 + [P] * 5), ("combine_bwd", [I] * 5 + [P] * 9),
                        ("swiglu_fwd", [I] * 3 + [P] * 4), ("swiglu_bwd", [I] * 3 + [P] * 5)):
@@ -349,10 +349,10 @@ def mm8_workspace_bytes(rows, k, n, experts, out_dtype) -> int:
     return int(load().laga_mm8_workspace_bytes(rows, k, n, experts, DTYPES[out_dtype]))
 
 
-def mm8(rows, k, n, experts, out_dtype, a, b, start, y, ws, ws_bytes, stream=0):
-    """laga_mm8 with raw device addresses (ints; experts 0: one matrix b)."""
-    _check(load().laga_mm8(rows, k, n, experts, DTYPES[out_dtype], a, b, start, y, ws, ws_bytes,
-                           stream), "laga_mm8")
+def mm8(rows, k, n, experts, out_dtype, a, b, start, pair, y, ws, ws_bytes, stream=0):
+    """laga_mm8 with raw device addresses (ints; experts 0: one matrix b; pair 0: none)."""
+    _check(load().laga_mm8(rows, k, n, experts, DTYPES[out_dtype], a, b, start, pair, y, ws,
+                           ws_bytes, stream), "laga_mm8")
 
 
 def experts_dw_workspace_bytes(rows, d, n, experts, dy_dtype) -> int:

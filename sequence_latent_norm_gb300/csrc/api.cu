@@ -579,8 +579,8 @@ size_t laga_mm8_workspace_bytes(int rows, int k, int n, int experts, laga_dtype 
 }
 
 laga_status laga_mm8(int rows, int k, int n, int experts, laga_dtype out_dtype, const void* a,
-                     const void* b, const int* start, void* y, void* ws, size_t ws_bytes,
-                     void* stream) {
+                     const void* b, const int* start, const int* pair, void* y, void* ws,
+                     size_t ws_bytes, void* stream) {
   t_launches = 0;
   if (!mm8_sizes_ok(rows, k, n, experts, out_dtype)) return LAGA_ERR_ARG;
   const bool fp32 = out_dtype == LAGA_FP32;
@@ -589,6 +589,7 @@ laga_status laga_mm8(int rows, int k, int n, int experts, laga_dtype out_dtype, 
   c.need(rows > 0, a);
   c.need(rows > 0, b);
   c.need(rows > 0 && experts > 0, start);
+  c.need(experts > 0 && pair, pair);
   c.need(rows > 0, y);
   c.need(need_bytes > 0 && ws, ws);
   if (c.status() != LAGA_OK) return c.status();
@@ -597,7 +598,7 @@ laga_status laga_mm8(int rows, int k, int n, int experts, laga_dtype out_dtype, 
     int* err = nullptr;
     const laga_status e = err_word(&err);
     return e != LAGA_OK ? e
-                        : cuda_status(launch_mm8(rows, k, n, experts, fp32, a, b, start, y,
+                        : cuda_status(launch_mm8(rows, k, n, experts, fp32, a, b, start, pair, y,
                                                  static_cast<unsigned char*>(ws), err,
                                                  static_cast<cudaStream_t>(stream)));
   });

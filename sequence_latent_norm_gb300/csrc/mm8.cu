@@ -40,22 +40,32 @@ constexpr int KS = CK_GROUP;                 // codes of i per step, the swizzle
 constexpr int HALVES = 2;                    // steps per stage
 constexpr int FT = 256;                      // rows of b per tile
 constexpr int TN_MAX = 224;                  // rows of a per tile
-constexpr int STAGES = 3;
-constexpr int W_BYTES = 128 * KS, X_BYTES = TN_MAX / 2 * KS;
-constexpr int X_OFF = HALVES * W_BYTES, STAGE_BYTES = X_OFF + HALVES * X_BYTES;
+constexpr int W_BYTES = 128 * KS, X_OFF = HALVES * W_BYTES;
 constexpr int SF_BYTES = 3 * 512;            // 4 steps' words of 128 rows of b, 2 x 128 of a
 constexpr int SF_WORDS = 4, SF_SLOTS = 2;    // such words in a slot of the ring
 constexpr int SF_STEPS = 4 * SF_WORDS;
-constexpr int SF_OFF = STAGES * STAGE_BYTES;
-constexpr int SLOT_BYTES = 2048, OUT_OFF = SF_OFF + SF_SLOTS * SF_WORDS * SF_BYTES;
-constexpr int EPI_WARPS = 8;
-constexpr int SMEM_BYTES = OUT_OFF + EPI_WARPS * SLOT_BYTES + 1024;
+constexpr int SF_SETS = 4;                   // sets of scales in tensor memory
+constexpr int SLOT_BYTES = 2048, EPI_WARPS = 8;
+// Shared memory for tiles of up to TN rows of a.  With few rows, where b's bytes
+// are all that counts, the ring is deeper (16 rows of 32 experts x 7168 x 4096:
+// 72 us with three stages).
+template <int TN>
+struct Ring {
+  static constexpr int STAGES = TN > 32 ? 3 : 5;
+  static constexpr int X_BYTES = TN / 2 * KS, STAGE_BYTES = X_OFF + HALVES * X_BYTES;
+  static constexpr int SF_OFF = STAGES * STAGE_BYTES;
+  static constexpr int OUT_OFF = SF_OFF + SF_SLOTS * SF_WORDS * SF_BYTES;
+  static constexpr int SMEM_BYTES = OUT_OFF + EPI_WARPS * SLOT_BYTES + 1024;
+  static_assert(SMEM_BYTES + (int)sizeof(int) * 3 * (ROUTE_MAX_EXPERTS + 1) + 1024 + 256 <=
+                    228 * 1024,
+                "shared memory, with the segments and the barriers");
+  // A set of scales is written again SF_SETS groups of 4 steps later.  By then
+  // the MMAs that read it are done: the ring lets STAGES stages be in flight.
+  static_assert((SF_SETS - 1) * 4 >= STAGES * HALVES, "scales outlive the MMAs that read them");
+};
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
-constexpr int TMEM_COLS = 512, SF_COL = 2 * TN_MAX, SF_SETS = 4, SF_COLS = 16;
+constexpr int TMEM_COLS = 512, SF_COL = 2 * TN_MAX, SF_COLS = 16;
 static_assert(SF_COL + SF_SETS * SF_COLS <= TMEM_COLS, "tensor memory");
-// A set of scales is written again SF_SETS groups of 4 steps later.  By then the
-// MMAs that read it are done: the ring lets STAGES stages be in flight.
-static_assert((SF_SETS - 1) * 4 >= STAGES * HALVES, "scales outlive the MMAs that read them");
 static_assert(4 % HALVES == 0, "whole stages under a word of scales");
 constexpr int PAIRS = 76;                    // one pair per two SMs
 constexpr int BAND = 8;                      // column tiles that run side by side
@@ -74,20 +84,21 @@ struct Params {
   int bf16;
   int mapped;              // y has a tensor map
   const uint8_t *a, *b;
-  const int* start;
+  const int *start, *pair;
   void* y;                 // or the partial sums [splits, rows, n]
   int* err;
 };
 
-// The experts' first rows, and the row tiles in front of each.
+// The experts' first rows, the ends of those that belong to pairs, and the row
+// tiles in front of each.
 struct Segments {
-  int start[WMAX + 1], tiles[WMAX + 1];
+  int start[WMAX + 1], end[WMAX], tiles[WMAX + 1];
 };
 
 // A pair's tiles in turn: rows r0 .. r1 of expert e, column tile f, steps k0 ..
 struct Walk {
   int t, e;                // next tile, and the expert of the last one
-  int r0, r1, f, k0, kn, z;
+  int r0, r1, r2, f, k0, kn, z;   // rows r1 .. r2: of no pair, zeros
 
   LAGA_DEVINL explicit Walk(int pair) : t(pair), e(0) {}
   LAGA_DEVINL bool next(const Params& p, const Segments& s) {
@@ -101,14 +112,15 @@ struct Walk {
     const int v = u - band * BAND * tt;
     f = band * BAND + v % fb;
     r0 = s.start[e] + v / fb * p.tn;
-    r1 = min(s.start[e + 1], r0 + p.tn);
+    r1 = min(s.end[e], r0 + p.tn);
+    r2 = r1 == s.end[e] ? s.start[e + 1] : r1;
     k0 = z * p.split_steps;
     kn = min(p.split_steps, p.steps - k0);
     t += gridDim.x >> 1;
     return true;
   }
   // N of the tile's MMAs
-  LAGA_DEVINL int width() const { return (r1 - r0 + 31) / 32 * 32; }
+  LAGA_DEVINL int width() const { return max((r1 - r0 + 31) / 32 * 32, 32); }
 };
 
 // Block-scaled MMA: D (+)= (A scaleA) (B scaleB)^T, both CTAs of the pair.
@@ -192,10 +204,15 @@ LAGA_DEVINL void store_tile(const Params& p, const CUtensorMap* ym, const Walk& 
       }
     }
   }
+  if (first == 0 && j < p.n)
+    for (int r = n; r < w.r2 - w.r0; ++r) dst[(long long)r * p.n] = from_f32<T>(0.f);
 }
 
+template <int TN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     mm8_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Params p) {
+  constexpr int STAGES = Ring<TN>::STAGES, STAGE_BYTES = Ring<TN>::STAGE_BYTES;
+  constexpr int X_BYTES = Ring<TN>::X_BYTES, SF_OFF = Ring<TN>::SF_OFF;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
@@ -238,7 +255,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         s = p.experts ? min(p.start[e], p.rows) : 0;
         t = p.experts ? min(p.start[e + 1], p.rows) : p.rows;
       }
-      const int own = e < E && t > s ? (t - s + p.tn - 1) / p.tn : 0;
+      int end = t;
+      if (p.pair) {
+        // the rows of no pair are the last ones, fewer than 128
+        for (int lo = max(s, t - 127); lo < end;) {
+          const int mid = (lo + end) >> 1;
+          if (p.pair[mid] < 0)
+            end = mid;
+          else
+            lo = mid + 1;
+        }
+      }
+      const int own = e < E && t > s ? max((end - s + p.tn - 1) / p.tn, 1) : 0;
       int sum = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -247,6 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       if (e < E) {
         seg.start[e] = s;
+        seg.end[e] = end;
         seg.tiles[e] = carry + sum - own;
         if (e == E - 1) {
           seg.start[E] = t;
@@ -399,7 +428,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   } else if (warp >= 4) {
     const int q = warp & 3;
     uint32_t polls = kWaitPolls;
-    uint8_t* slot = sm + OUT_OFF + (warp - 4) * SLOT_BYTES;
+    uint8_t* slot = sm + Ring<TN>::OUT_OFF + (warp - 4) * SLOT_BYTES;
     const int first = (warp - 4) / 4 * 32;
     if (lane == 0) tma_prefetch_desc(&tm.y);
     for (uint32_t tile = 0; w.next(p, seg); ++tile) {
@@ -515,7 +544,7 @@ size_t mm8_ws_bytes(int rows, int K, int N, int experts, bool fp32) {
 }
 
 cudaError_t launch_mm8(int rows, int K, int N, int experts, bool fp32, const void* a,
-                       const void* b, const int* start, void* y, unsigned char* ws, int* err,
+                       const void* b, const int* start, const int* pair, void* y, unsigned char* ws, int* err,
                        cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
   const Mm8Plan pl = mm8_plan(rows, K, N, experts);
@@ -528,6 +557,7 @@ cudaError_t launch_mm8(int rows, int K, int N, int experts, bool fp32, const voi
   p.a = static_cast<const uint8_t*>(a);
   p.b = static_cast<const uint8_t*>(b);
   p.start = start;
+  p.pair = experts ? pair : nullptr;
   p.y = pl.splits > 1 ? static_cast<void*>(ws) : y;
   p.err = err;
   const int blocks = std::max(experts, 1);
@@ -541,13 +571,15 @@ cudaError_t launch_mm8(int rows, int K, int N, int experts, bool fp32, const voi
   if (p.mapped &&
       (e = out_map(&tm.y, p.y, N, (uint64_t)pl.splits * rows, p.bf16)) != cudaSuccess)
     return e;
-  if ((e = cudaFuncSetAttribute(mm8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                SMEM_BYTES)) != cudaSuccess)
+  auto k = pl.tn > 32 ? mm8_kernel<TN_MAX> : mm8_kernel<32>;
+  const int smem = pl.tn > 32 ? Ring<TN_MAX>::SMEM_BYTES : Ring<32>::SMEM_BYTES;
+  if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) !=
+      cudaSuccess)
     return e;
   const long long most = ((long long)rows / pl.tn + std::min(blocks, rows)) * pl.f_tiles * pl.splits;
   {
     LaunchScope ls_("mm8", st);
-    mm8_kernel<<<2 * (int)std::min<long long>(PAIRS, most), THREADS, SMEM_BYTES, st>>>(tm, p);
+    k<<<2 * (int)std::min<long long>(PAIRS, most), THREADS, smem, st>>>(tm, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (pl.splits > 1) {

@@ -68,8 +68,8 @@ cudaError_t launch_weight_pack(int experts, int K, int N, bool fp32, const void*
                                void* bwd, cudaStream_t st);
 size_t mm8_ws_bytes(int rows, int K, int N, int experts, bool fp32);
 cudaError_t launch_mm8(int rows, int K, int N, int experts, bool fp32, const void* a,
-                       const void* b, const int* start, void* y, unsigned char* ws, int* err,
-                       cudaStream_t st);
+                       const void* b, const int* start, const int* pair, void* y,
+                       unsigned char* ws, int* err, cudaStream_t st);
 
 // Weight gradient by expert: the rows of expert e are start[e] .. start[e + 1],
 // multiples of 128.

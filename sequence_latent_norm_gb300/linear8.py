@@ -92,26 +92,29 @@ def _product(x, w, routes, dtype, stream, matrix, k, n, what):
         raise ValueError(f"{what}: the weight on {w.device}, expected {dev}")
     if (routes is None) != (w.experts == 0):
         raise ValueError(f"{what}: routes go with the weights of experts, and these with routes")
-    start, lead = 0, x.shape[:-1]
+    start = pair = 0
+    lead = x.shape[:-1]
     if routes is not None:
         if routes.experts != w.experts:
             raise ValueError(f"{what}: routes to {routes.experts} experts, weights of {w.experts}")
-        start = routes.check(dev)[2]
+        pair, start = routes.check(dev)[1:3]
+        if routes.align == 1:            # every row in use has a pair
+            pair = 0
         if x.rows != routes.rows:
             raise ValueError(f"{what}: {x.rows} rows, expected the routes' {routes.rows}")
-    with on_stream(dev, stream, x.data, matrix, routes and routes.start) as st:
+    with on_stream(dev, stream, x.data, matrix, *(routes[3:5] if routes is not None else ())) as st:
         y = torch.empty(*lead, n, dtype=dtype, device=dev)
         nb = _lib.mm8_workspace_bytes(x.rows, k, n, w.experts, IO_NAME[dtype])
         ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
         _lib.mm8(x.rows, k, n, w.experts, IO_NAME[dtype], x.data.data_ptr(), matrix.data_ptr(),
-                 start, y.data_ptr(), ws.data_ptr() if nb else 0, nb, st)
+                 start, pair, y.data_ptr(), ws.data_ptr() if nb else 0, nb, st)
     return y
 
 
 def linear8(x: Checkpoint8, w: Weight8, *, routes=None, dtype=torch.bfloat16, stream=None):
     """x W [..., n] in ``dtype`` (bf16 or fp32); with ``routes`` (a Routes; x
     has its rows, as :func:`spread8` makes them) row by row with its
-    expert's W."""
+    expert's W; rows of no pair are zero."""
     if not isinstance(w, Weight8):
         raise TypeError("linear8 takes a Weight8")
     k, n = w.shape[-2:]

@@ -317,19 +317,22 @@ def test_linear_by_expert(counts, align, io, K, N):
     nb = laga._lib.mm8_workspace_bytes(rows, K, N, E, io)
     ws = torch.empty(max(nb, 16), dtype=torch.uint8, device=DEV)
     d_x, d_w = _dev(x), _dev(fwd)
-    laga._lib.mm8(rows, K, N, E, io, d_x.data_ptr(), d_w.data_ptr(), r.start.data_ptr(),
+    laga._lib.mm8(rows, K, N, E, io, d_x.data_ptr(), d_w.data_ptr(), r.start.data_ptr(), 0,
                   y.data_ptr(), ws.data_ptr(), nb, torch.cuda.current_stream().cuda_stream)
     _sync()
     want, mag = oex.mm8(x, fwd, K, N, start)
     _check_sum(y[:start[-1]], want[:start[-1]], mag[:start[-1]], K, io, "y")
     assert (y[start[-1]:] == 7.0).all()
     w8 = laga.Weight8((E, K, N), d_w, _dev(bwd))
-    assert torch.equal(laga.linear8(laga.Checkpoint8(d_x, K), w8, routes=r, dtype=DT[io])
-                       [:start[-1]], y[:start[-1]])
+    live = (r.pair >= 0)[:, None]
+    by_routes = laga.linear8(laga.Checkpoint8(d_x, K), w8, routes=r, dtype=DT[io])
+    _sync()
+    assert torch.equal(by_routes[:start[-1]], torch.where(live, y, 0.0)[:start[-1]])
     dy = _codes(rows, N, g)
     dx = laga.linear8_dx(laga.Checkpoint8(_dev(dy), N), w8, routes=r, dtype=DT[io])
     _sync()
     want, mag = oex.mm8(dy, bwd, N, K, start)
+    want = np.where(live.cpu().numpy(), want, 0.0)
     _check_sum(dx[:start[-1]], want[:start[-1]], mag[:start[-1]], N, io, "dx")
 
 
