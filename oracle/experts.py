@@ -196,3 +196,61 @@ def swiglu_bwd(gu, da):
     with np.errstate(over="ignore"):
         s, r = 1.0 / (1.0 + np.exp(-g)), 1.0 / (1.0 + np.exp(g))
     return np.concatenate([da * u * s * (1.0 + g * r), da * g * s], axis=1)
+
+
+# ------------------------------------------------------------------ the block
+def bf16(v):
+    """fp64 values rounded to bf16 (8 significand bits, nearest even)."""
+    m, e = np.frexp(v)
+    return np.ldexp(np.rint(m * 256.0) / 256.0, e)
+
+
+def quantised(v):
+    return unpack(pack(v), v.shape[1])
+
+
+def quantised_weight(w):
+    """[E, K, N] as its 128 x 128 blocks' codes hold it."""
+    _, bwd = pack_weight(w)
+    return unpack(bwd, w.shape[2]).reshape(w.shape)
+
+
+def block_fwd(h, w_router, bias, w_in, w_out, *, exact=False, io="bf16", **route):
+    """(y, state) of routed experts over tokens h [T, d]: the block's 8-bit
+    roundings and those of bf16 (``io``), or none with ``exact``."""
+    q, qw, r = ((lambda v: v,) * 3) if exact else (quantised, quantised_weight, bf16)
+    if io == "fp32":
+        r = lambda v: v      # noqa: E731  (fp32's roundings are far below the others)
+    logits = h @ w_router
+    expert, weight = choose(logits, bias, **route)
+    row, pair, start = order(expert, local=w_in.shape[0], align=1, rows=int((expert >= 0).sum()))
+    h8, wi, wo = q(h), qw(w_in), qw(w_out)
+    x = h8[pair // expert.shape[1]]
+    seg = [(e, start[e], start[e + 1]) for e in range(len(wi)) if start[e + 1] > start[e]]
+    gu = np.concatenate([r(x[a:b] @ wi[e]) for e, a, b in seg])
+    act = q(swiglu(gu))
+    rows = np.concatenate([r(act[a:b] @ wo[e]) for e, a, b in seg])
+    y, _ = combine(rows, weight, row)
+    return r(y), dict(h=h, h8=h8, x=x, wi=wi, wo=wo, gu=gu, act=act, rows=rows, logits=logits,
+                      expert=expert, weight=weight, row=row, seg=seg, w_router=w_router,
+                      fns=(q, r), route=route)
+
+
+def block_bwd(st, dy):
+    q, r = st["fns"]
+    d_rows, dweight, _ = combine_bwd(dy, st["rows"], st["weight"], st["row"])
+    d_rows = r(d_rows)
+    d8 = q(d_rows)
+    n, d = len(st["wi"]), dy.shape[1]
+    da = np.concatenate([r(d8[a:b] @ st["wo"][e].T) for e, a, b in st["seg"]])
+    dgu = r(swiglu_bwd(st["gu"], da))
+    dgu8 = q(dgu)
+    dx = np.concatenate([r(dgu8[a:b] @ st["wi"][e].T) for e, a, b in st["seg"]])
+    dw_in, dw_out = np.zeros(st["wi"].shape), np.zeros(st["wo"].shape)
+    for e, a, b in st["seg"]:
+        dw_in[e], dw_out[e] = st["x"][a:b].T @ dgu[a:b], st["act"][a:b].T @ d_rows[a:b]
+    kw = {k: v for k, v in st["route"].items() if k in ("score", "renormalise", "scale")}
+    dlogits = route_bwd(st["logits"], st["expert"], dweight, **kw)
+    back, _ = combine(dx, np.ones_like(st["weight"]), st["row"])
+    return dict(dh=r(r(back) + r(dlogits @ st["w_router"].T)), dw_router=st["h8"].T @ dlogits,
+                dw_in=dw_in, dw_out=dw_out)

@@ -9,7 +9,7 @@ build script and a thin binding.
 
 from .api import Laga, Shard, attention_flops, upproj_flops  # noqa: F401
 from .checkpoint import Checkpoint8, pack8, weight_grad8  # noqa: F401
-from .experts import combine, combine_grad, spread8, swiglu8, swiglu8_grad  # noqa: F401
+from .experts import RoutedExperts, combine, combine_grad, spread8, swiglu8, swiglu8_grad  # noqa: F401
 from .linear8 import Weight8, linear8, linear8_dx, pack_weight8  # noqa: F401
 from .routing import Router, Routes  # noqa: F401
 from .residual import ResidualGrads, ResidualNorm, ResidualOut, ResidualSaved  # noqa: F401

@@ -29,6 +29,12 @@ What the block holds of h between the passes serves dW_q and dW_kv_a alone.
 ``checkpoint="fp8"`` holds it in 8 bits (``checkpoint.py``) and takes both
 gradients, in fp32, straight from the codes.
 
+``projections="fp8"`` takes the three projections and their input gradients as
+8-bit products (``linear8.py``): h, the attention's output and the gradients
+that meet a weight are packed on the way, the weights in every call.  The weight
+gradients come from the codes that were multiplied (h's from ``kept`` where it is
+given), in fp32.
+
 ``LagaResidualStack`` puts blocks on a residual stream, each with its norm in
 front, and its norm, gate and residual scale behind (``residual.py``); between
 two blocks both run in one kernel.  The paper leaves this part of the
@@ -44,6 +50,8 @@ import torch.distributed as dist
 from .sp import LibraryCompute, SequenceParallelLaga
 from .api import Shard
 from .checkpoint import Checkpoint8, pack8, weight_grad8
+from .experts import RoutedExperts
+from .linear8 import linear8, linear8_dx, pack_weight8
 from .residual import ResidualNorm
 
 
@@ -58,13 +66,19 @@ class LagaAttentionBlock:
     ``backward(d_out) -> (dq, dc, dw_kvb, dgamma)``); ``group`` is the
     process group whose ranks share the weights (None: one rank, no
     collective); ``checkpoint`` how h is held between the passes ("none": as
-    given, "fp8": in 8 bits, on a CUDA device)."""
+    given, "fp8": in 8 bits, on a CUDA device); ``projections`` how W_q, W_kv_a
+    and W_o are multiplied ("io": in the I/O type, "fp8": in 8 bits, widths up to
+    16384, on a CUDA device; h is then held in 8 bits whatever ``checkpoint``
+    says)."""
 
     def __init__(self, attn, n_h: int, group=None, distributed: bool = False,
-                 checkpoint: str = "none"):
+                 checkpoint: str = "none", projections: str = "io"):
         if checkpoint not in ("none", "fp8"):
             raise ValueError(f"checkpoint={checkpoint!r}: one of none, fp8")
+        if projections not in ("io", "fp8"):
+            raise ValueError(f"projections={projections!r}: one of io, fp8")
         self.checkpoint = checkpoint
+        self.projections = projections
         self.attn = attn
         self.n_h = n_h
         self.group = group
@@ -74,20 +88,21 @@ class LagaAttentionBlock:
 
     @classmethod
     def sequence_parallel(cls, n_h: int, S: int, *, group=None, device=None,
-                          checkpoint: str = "none", **dims):
+                          checkpoint: str = "none", projections: str = "io", **dims):
         """A rank of a sequence-parallel group (torch.distributed must be
         initialised): the library on its n_h/P heads behind sp.py's
         exchanges."""
         return cls(SequenceParallelLaga(n_h, S, group=group, device=device, **dims), n_h, group,
-                   distributed=True, checkpoint=checkpoint)
+                   distributed=True, checkpoint=checkpoint, projections=projections)
 
     @classmethod
     def single(cls, n_h: int, S: int, *, device=None, B: int = 1, checkpoint: str = "none",
-               **dims):
+               projections: str = "io", **dims):
         """All n_h heads and the whole sequence on one device, no process
         group: the library directly."""
         shard = Shard(S=S, H=n_h, n_h_total=n_h, B=B, **dims)
-        return cls(LibraryCompute(shard, device), n_h, checkpoint=checkpoint)
+        return cls(LibraryCompute(shard, device), n_h, checkpoint=checkpoint,
+                   projections=projections)
 
     def forward(self, h, w_q, w_kva, gamma, w_kvb, w_o, cos, sin, *, kept=None, kept_gain=None):
         """h [B, S_r, d_model] (this rank's chunk); w_q [d_model, n_h (d_nope
@@ -106,16 +121,33 @@ class LagaAttentionBlock:
             raise ValueError(f"kept: a checkpoint of {kept.rows} rows of {kept.d}, expected "
                              f"{B * S_r} of {d_model}")
         h_flat = h.reshape(B * S_r, d_model)
-        q = (h_flat @ w_q).reshape(B, S_r, self.n_h, -1)
-        c = (h_flat @ w_kva).reshape(B, S_r, -1)
+        fp8 = self.projections == "fp8"
+        if fp8:
+            w_q, w_kva, w_o = (pack_weight8(w) for w in (w_q, w_kva, w_o))
+            h8 = pack8(h_flat.contiguous())
+            q, c = (linear8(h8, w, dtype=h.dtype) for w in (w_q, w_kva))
+        else:
+            q, c = h_flat @ w_q, h_flat @ w_kva
+        q = q.reshape(B, S_r, self.n_h, -1)
+        c = c.reshape(B, S_r, -1)
         out, _ = self.attn.forward(q, c, w_kvb, gamma, cos, sin)
         out_flat = out.reshape(B * S_r, -1)
-        if kept is None and self.checkpoint == "fp8":
+        if kept is None and fp8:
+            kept = h8
+        elif kept is None and self.checkpoint == "fp8":
             kept = pack8(h_flat.contiguous())
         elif kept is None:
             kept = h_flat
+        if fp8:
+            out_flat = pack8(out_flat.contiguous())
         self._saved = (kept, kept_gain, w_q, w_kva, w_o, out_flat, out.shape, h.shape)
-        return (out_flat @ w_o).reshape(B, S_r, d_model)
+        y = linear8(out_flat, w_o, dtype=h.dtype) if fp8 else out_flat @ w_o
+        return y.reshape(B, S_r, d_model)
+
+    def _layer(self, h, w, cos, sin, **kept):
+        """forward with a layer's dict of weights."""
+        return self.forward(h, w["w_q"], w["w_kva"], w["gamma"], w["w_kvb"], w["w_o"], cos, sin,
+                            **kept)
 
     def _all_reduce(self, t, what):
         if not self.distributed:
@@ -133,13 +165,23 @@ class LagaAttentionBlock:
         kept, gain, w_q, w_kva, w_o, out_flat, out_shape, h_shape = self._saved
         rows = out_flat.shape[0]
         dy_flat = dy.reshape(rows, -1)
-        dw_o = _wide(out_flat.t() @ dy_flat)
-        d_out = (dy_flat @ w_o.t()).reshape(out_shape)
+        fp8 = self.projections == "fp8"
+        if fp8:
+            dy_flat = dy_flat.contiguous()
+            dw_o = weight_grad8(out_flat, dy_flat)
+            d_out = linear8_dx(pack8(dy_flat), w_o, dtype=dy.dtype).reshape(out_shape)
+        else:
+            dw_o = _wide(out_flat.t() @ dy_flat)
+            d_out = (dy_flat @ w_o.t()).reshape(out_shape)
         dq, dc, dw_kvb, dgamma = self.attn.backward(d_out)
         dq_flat = dq.reshape(rows, -1)
         dc_flat = dc.reshape(rows, -1)
-        dc_io = dc_flat.to(dq.dtype)
-        dh = (dq_flat @ w_q.t() + dc_io @ w_kva.t()).reshape(h_shape)
+        if fp8:
+            dh = (linear8_dx(pack8(dq_flat), w_q, dtype=dq.dtype) +
+                  linear8_dx(pack8(dc_flat), w_kva, dtype=dq.dtype)).reshape(h_shape)
+        else:
+            dc_io = dc_flat.to(dq.dtype)
+            dh = (dq_flat @ w_q.t() + dc_io @ w_kva.t()).reshape(h_shape)
         if isinstance(kept, Checkpoint8):
             dw_q = weight_grad8(kept, dq_flat, gain)
             dw_kva = weight_grad8(kept, dc_flat, gain)
@@ -153,12 +195,13 @@ class LagaAttentionBlock:
 
 
 class LagaResidualStack:
-    """Attention blocks on a residual stream x [B, S_r, d_model] (contiguous):
+    """Blocks on a residual stream x [B, S_r, d_model] (contiguous):
 
         h_l = N_pre(x_l) gamma_pre,  y_l = block_l(h_l),
         x_{l+1} = x_l + alpha s N_post(y_l) gamma_post
 
-    ``blocks``: one LagaAttentionBlock a layer.  norm_pre, norm_post ("none":
+    ``blocks``: one LagaAttentionBlock or RoutedExperts a layer (the latter on one
+    rank only).  norm_pre, norm_post ("none":
     a plain gated residual add) and gate as for ResidualNorm.  ``ckpt`` holds
     the normalised x and y of every layer as 8-bit checkpoints; the one of x
     also serves the layer's dW_q and dW_kv_a, so neither x nor h is held in
@@ -171,6 +214,9 @@ class LagaResidualStack:
                  device="cuda"):
         if not blocks:
             raise ValueError("at least one block")
+        if any(isinstance(b, RoutedExperts) for b in blocks) and any(
+                getattr(b, "distributed", False) for b in blocks):
+            raise ValueError("RoutedExperts in a stack over several ranks")
         kw = dict(norm_pre=norm_pre, norm_post=norm_post, gate=gate, ckpt=ckpt, io_dtype=io_dtype,
                   eps=eps, device=device)
         self.blocks = list(blocks)
@@ -181,7 +227,8 @@ class LagaResidualStack:
 
     def forward(self, x, layers, cos, sin):
         """``layers``: per block a dict of w_q, w_kva, gamma, w_kvb, w_o (see
-        LagaAttentionBlock.forward), gamma_pre [d_model] and alpha [1] fp32,
+        LagaAttentionBlock.forward), or w_router, w_in, w_out and bias (see
+        RoutedExperts.forward; no bias: None or left out), and gamma_pre [d_model] and alpha [1] fp32,
         and, where they apply, gamma_post [d_model] fp32 and gate logits [B,
         S_r, d_model or 1].  Returns x behind the last block."""
         if len(layers) != len(self.blocks):
@@ -191,9 +238,8 @@ class LagaResidualStack:
         behind = []                           # of the residual half behind block l
         for i, (block, w) in enumerate(zip(self.blocks, layers)):
             in_bits = self.first.ckpt
-            y = block.forward(r.h, w["w_q"], w["w_kva"], w["gamma"], w["w_kvb"], w["w_o"], cos, sin,
-                              kept=kept[i].x if in_bits else None,
-                              kept_gain=w["gamma_pre"] if in_bits else None)
+            y = block._layer(r.h, w, cos, sin, kept=kept[i].x if in_bits else None,
+                             kept_gain=w["gamma_pre"] if in_bits else None)
             ends = i + 1 == len(layers)
             step = self.last if ends else self.between
             r = step.forward(r.x, y, gate=w.get("gate"), alpha=w["alpha"],

@@ -594,6 +594,7 @@ laga_status laga_mm8(int rows, int k, int n, int experts, laga_dtype out_dtype, 
   c.need(need_bytes > 0 && ws, ws);
   if (c.status() != LAGA_OK) return c.status();
   if (need_bytes > 0 && (!ws || ws_bytes < need_bytes)) return LAGA_ERR_WORKSPACE;
+  if (rows == 0) return LAGA_OK;
   return run_launches("laga_mm8", [&] {
     int* err = nullptr;
     const laga_status e = err_word(&err);

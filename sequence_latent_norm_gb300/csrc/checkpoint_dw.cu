@@ -897,9 +897,7 @@ cudaError_t launch_plan(DwPlan& pl, int rows, int d, int n, bool fp32, const voi
            : pl.bn == 256   ? ckpt_dw_kernel<256, false>
            : pl.bn == 192   ? ckpt_dw_kernel<192, false>
                             : ckpt_dw_kernel<128, false>;
-  if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES)) !=
-      cudaSuccess)
-    return e;
+  if ((e = allow_smem(k, SMEM_BYTES)) != cudaSuccess) return e;
   const int left = std::max(p.experts, 1) * p.tiles - p.rounds * PAIRS;
   const int pairs = p.rounds > 0 || by_expert ? PAIRS : pl.frag_slots / p.max_frags;
   {

@@ -4,6 +4,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "plan.h"
 
 namespace laga {
@@ -82,5 +84,27 @@ struct Views {
   const __nv_bfloat16* dO;                      // [R, 128] canonical dO
 };
 Views make_views(const Plan& p, const Ptrs& x);
+
+// Allows a kernel more shared memory than 48 KB, once per device: the limit of a
+// kernel is the same in every call.
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes) {
+  static std::atomic<const void*> done[64][8];   // kernels of this type, per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const void* k = reinterpret_cast<const void*>(kernel);
+  std::atomic<const void*>* set = dev >= 0 && dev < 64 ? done[dev] : nullptr;
+  if (set)
+    for (int i = 0; i < 8; ++i)
+      if (set[i].load(std::memory_order_acquire) == k) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess || !set) return e;
+  for (int i = 0; i < 8; ++i) {
+    const void* free_slot = nullptr;
+    if (set[i].compare_exchange_strong(free_slot, k) || free_slot == k) break;
+  }
+  return cudaSuccess;
+}
 
 }  // namespace laga

@@ -573,9 +573,7 @@ cudaError_t launch_mm8(int rows, int K, int N, int experts, bool fp32, const voi
     return e;
   auto k = pl.tn > 32 ? mm8_kernel<TN_MAX> : mm8_kernel<32>;
   const int smem = pl.tn > 32 ? Ring<TN_MAX>::SMEM_BYTES : Ring<32>::SMEM_BYTES;
-  if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) !=
-      cudaSuccess)
-    return e;
+  if ((e = allow_smem(k, smem)) != cudaSuccess) return e;
   const long long most = ((long long)rows / pl.tn + std::min(blocks, rows)) * pl.f_tiles * pl.splits;
   {
     LaunchScope ls_("mm8", st);

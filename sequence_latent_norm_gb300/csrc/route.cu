@@ -445,29 +445,37 @@ LAGA_DEVINL bool choose(const RouteParams& p, const T* l, const float (&x)[NV],
   return true;
 }
 
-// Numbers the pairs of this block's chunk.  counts: the chunks' rows by local
-// expert; smem: [experts' bases | next starts | warps x local 16-bit counts].
+// Numbers the pairs of this block's chunk.  smem: [bases | counts | warps x counts]
+// by local expert.
 LAGA_DEVINL void place(const RouteParams& p, unsigned* smem) {
   const int EL = p.local, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int warps = blockDim.x >> 5;
   unsigned* base = smem;
   unsigned* next = smem + EL;
   unsigned* hist = smem + 2 * EL;        // [warps, EL]
-  for (int i = threadIdx.x; i < EL * (warps + 2); i += blockDim.x) smem[i] = 0;
-  __syncthreads();
-  // chunks in front of this one, and all of them; `parts` threads an expert
-  const int parts = max(1, (int)blockDim.x / EL);
-  for (int i = threadIdx.x; i < EL * parts; i += blockDim.x) {
-    const int e = i % EL;
-    unsigned before = 0, all = 0;
-#pragma unroll 16
-    for (int c = i / EL; c < p.chunks; c += parts) {
-      const unsigned n = p.counts[(size_t)c * EL + e];
-      all += n;
-      before += c < (int)blockIdx.x ? n : 0;
+  if (p.chunks == 1) {                   // the counts are where `base` will be
+    for (int e = threadIdx.x; e < EL; e += blockDim.x) {
+      next[e] = base[e];
+      base[e] = 0;
     }
-    atomicAdd(&base[e], before);
-    atomicAdd(&next[e], all);
+    for (int i = threadIdx.x; i < EL * warps; i += blockDim.x) hist[i] = 0;
+  } else {
+    for (int i = threadIdx.x; i < EL * (warps + 2); i += blockDim.x) smem[i] = 0;
+    __syncthreads();
+    // chunks in front of this one, and all of them; `parts` threads an expert
+    const int parts = max(1, (int)blockDim.x / EL);
+    for (int i = threadIdx.x; i < EL * parts; i += blockDim.x) {
+      const int e = i % EL;
+      unsigned before = 0, all = 0;
+#pragma unroll 16
+      for (int c = i / EL; c < p.chunks; c += parts) {
+        const unsigned n = p.counts[(size_t)c * EL + e];
+        all += n;
+        before += c < (int)blockIdx.x ? n : 0;
+      }
+      atomicAdd(&base[e], before);
+      atomicAdd(&next[e], all);
+    }
   }
   __syncthreads();
   if (warp == 0) {                       // segment starts: a scan over the experts
@@ -593,11 +601,11 @@ __global__ void __launch_bounds__(route_threads<NV>())
     }
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.local; e += blockDim.x)
-    p.counts[(size_t)blockIdx.x * p.local + e] = smem[e];
   if (p.chunks == 1) {
-    __syncthreads();
     place(p, smem);
+  } else {
+    for (int e = threadIdx.x; e < p.local; e += blockDim.x)
+      p.counts[(size_t)blockIdx.x * p.local + e] = smem[e];
   }
 }
 
@@ -685,36 +693,29 @@ RouteParams make_params(const laga_route_dims& d) {
   return p;
 }
 
+// Words of shared memory that place needs.
+constexpr size_t place_words(int local, int warps) { return (size_t)local * (warps + 2); }
+
 template <int NV>
 cudaError_t launch_fwd(const RouteParams& p, bool fp32, const void* logits, cudaStream_t st) {
   constexpr int threads = route_threads<NV>();
-  const size_t place_smem = (size_t)p.local * (threads / 32 + 2) * 4;
-  const size_t smem = p.chunks == 1 ? place_smem : (size_t)p.local * 4;
+  // (at most 40 KB: 1024 experts come with 8 warps)
+  const size_t smem = (p.chunks == 1 ? place_words(p.local, threads / 32) : p.local) * 4;
   cudaError_t e;
   {
     LaunchScope ls_("route", st);
-    if (fp32) {
-      if ((e = cudaFuncSetAttribute(route_kernel<NV, float>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024)) !=
-          cudaSuccess)
-        return e;
+    if (fp32)
       route_kernel<NV, float><<<p.chunks, threads, smem, st>>>(static_cast<const float*>(logits), p);
-    } else {
-      if ((e = cudaFuncSetAttribute(route_kernel<NV, __nv_bfloat16>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024)) !=
-          cudaSuccess)
-        return e;
+    else
       route_kernel<NV, __nv_bfloat16><<<p.chunks, threads, smem, st>>>(
           static_cast<const __nv_bfloat16*>(logits), p);
-    }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (p.chunks > 1) {
-    if ((e = cudaFuncSetAttribute(route_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  200 * 1024)) != cudaSuccess)
+    if ((e = allow_smem(route_place_kernel, place_words(ROUTE_MAX_EXPERTS, 32) * 4)) != cudaSuccess)
       return e;
     LaunchScope ls_("route_place", st);
-    route_place_kernel<<<p.chunks, 1024, (size_t)p.local * 34 * 4, st>>>(p);
+    route_place_kernel<<<p.chunks, 1024, place_words(p.local, 32) * 4, st>>>(p);
   }
   return cudaGetLastError();
 }
@@ -747,6 +748,7 @@ long long route_rows(const laga_route_dims& d) {
 size_t route_ws_bytes(const laga_route_dims& d) {
   if (d.tokens == 0) return 0;
   const RouteParams p = make_params(d);
+  if (p.chunks == 1) return 0;
   return ((size_t)p.chunks * p.local * 4 + 255) / 256 * 256;
 }
 

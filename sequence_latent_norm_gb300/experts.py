@@ -3,6 +3,9 @@
     h_t -> rows of its experts (spread8) -> [g | u] = row W_in[e] (linear8)
         -> a = silu(g) u in 8 bits (swiglu8) -> a W_out[e] (linear8)
         -> y_t = sum_j weight_tj row_tj (combine)
+
+:class:`RoutedExperts` runs all of it, forward and backward, as a block of
+``LagaResidualStack``.
 """
 
 from __future__ import annotations
@@ -10,7 +13,11 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .checkpoint import IO_NAME, Checkpoint8, empty_checkpoint, need, on_stream, rows_of
+from .api import _TORCH_DT
+from .checkpoint import (IO_NAME, Checkpoint8, empty_checkpoint, need, on_stream, pack8, rows_of,
+                         weight_grad8)
+from .linear8 import Weight8, linear8, linear8_dx, pack_weight8
+from .routing import Router
 
 
 def _matrix(t, name, device=None, shape=None):
@@ -116,3 +123,82 @@ def swiglu8_grad(gu: torch.Tensor, da: torch.Tensor, *, routes=None, stream=None
         dgu = torch.empty_like(gu)
         _lib.swiglu_bwd(rows, f, IO_NAME[gu.dtype], p, pa, end, dgu.data_ptr(), st)
     return dgu
+
+
+class RoutedExperts:
+    """Feed-forward experts behind a router, all on this device:
+
+        logits = h W_router (fp32),  routes = Router(logits, bias),
+        y_t = sum_j weight_tj W_out[e]^T (silu(g) u),  [g | u] = W_in[e]^T h_t
+
+    with the experts' products in 8 bits.  Options of the router as for
+    Router (score, groups, top_groups, renormalise, scale).  What is held
+    between the passes: h in 8 bits (or ``kept``), [g | u], logits and routes;
+    the activation and the experts' outputs are computed again."""
+
+    distributed = False
+
+    def __init__(self, n_experts: int, top_k: int, *, io_dtype: str = "bf16", device="cuda",
+                 **router):
+        for k in ("shard", "align"):
+            if k in router:
+                raise ValueError(f"RoutedExperts sets {k} itself")
+        if io_dtype not in _TORCH_DT:
+            raise ValueError(f"io_dtype={io_dtype!r}: one of {', '.join(_TORCH_DT)}")
+        self.router = Router(n_experts, top_k, device=device, **router)
+        self.dtype = _TORCH_DT[io_dtype]
+        self._saved = None
+
+    def forward(self, h, w_router, w_in, w_out, *, bias=None, kept=None, kept_gain=None):
+        """h [..., d]; w_router [d, n_experts] fp32; w_in [n_experts, d, 2 f] and
+        w_out [n_experts, f, d], in the I/O dtype or as Weight8; bias
+        [n_experts] fp32 or None.  Returns y [..., d].  ``kept`` and
+        ``kept_gain`` as for LagaAttentionBlock.forward."""
+        if h.dtype != self.dtype:
+            raise ValueError(f"h: dtype {h.dtype} != {self.dtype}")
+        rows, d = rows_of(h.shape)
+        if kept is None:
+            if kept_gain is not None:
+                raise ValueError("kept_gain without kept: h is held as given")
+        elif not isinstance(kept, Checkpoint8):
+            raise TypeError("kept must be a Checkpoint8")
+        elif (kept.rows, kept.d) != (rows, d):
+            raise ValueError(f"kept: a checkpoint of {kept.rows} rows of {kept.d}, expected "
+                             f"{rows} of {d}")
+        w_in, w_out = (w if isinstance(w, Weight8) else pack_weight8(w) for w in (w_in, w_out))
+        h_flat = h.reshape(rows, d).contiguous()
+        logits = h_flat.float() @ w_router
+        routes = self.router.forward(logits, bias)
+        h8 = pack8(h_flat)
+        gu = linear8(spread8(h8, routes), w_in, routes=routes, dtype=self.dtype)
+        y = self._outputs(swiglu8(gu, routes=routes), w_out, routes)
+        self._saved = (h8 if kept is None else kept, kept_gain, logits, routes, gu, w_router, w_in,
+                       w_out, h.shape)
+        return combine(y, routes).reshape(h.shape)
+
+    def _outputs(self, a8, w_out, routes):
+        return linear8(a8, w_out, routes=routes, dtype=self.dtype)
+
+    def _layer(self, h, w, cos, sin, **kept):
+        """forward with a layer's dict of weights (cos and sin are attention's)."""
+        return self.forward(h, w["w_router"], w["w_in"], w["w_out"], bias=w.get("bias"), **kept)
+
+    def _all_reduce(self, t, what):
+        return t
+
+    def backward(self, dy):
+        """dy [..., d].  Returns a dict: dh [..., d]; dw_router [d, n_experts],
+        dw_in and dw_out of their weights' shapes, fp32."""
+        kept, gain, logits, routes, gu, w_router, w_in, w_out, shape = self._saved
+        dy_flat = dy.reshape(-1, shape[-1]).contiguous()
+        a8 = swiglu8(gu, routes=routes)
+        d_rows, dweight = combine_grad(dy_flat, routes, y=self._outputs(a8, w_out, routes))
+        dw_out = weight_grad8(a8, d_rows, routes=routes)
+        da = linear8_dx(pack8(d_rows), w_out, routes=routes, dtype=self.dtype)
+        dgu = swiglu8_grad(gu, da, routes=routes)
+        dw_in = weight_grad8(spread8(kept, routes), dgu, gain, routes=routes)
+        dx = linear8_dx(pack8(dgu), w_in, routes=routes, dtype=self.dtype)
+        dlogits = self.router.backward(logits, routes, dweight)
+        dh = combine(dx, routes, weighted=False) + (dlogits @ w_router.t()).to(self.dtype)
+        return dict(dh=dh.reshape(shape), dw_router=weight_grad8(kept, dlogits, gain), dw_in=dw_in,
+                    dw_out=dw_out)
