@@ -68,7 +68,7 @@ constexpr int TMEM_COLS = 512, SF_COL = 2 * TN_MAX, SF_COLS = 16;
 static_assert(SF_COL + SF_SETS * SF_COLS <= TMEM_COLS, "tensor memory");
 static_assert(4 % HALVES == 0, "whole stages under a word of scales");
 constexpr int PAIRS = 76;                    // one pair per two SMs
-constexpr int BAND = 8;                      // column tiles that run side by side
+constexpr int BAND = 16;                     // column tiles that run side by side
 constexpr int WMAX = ROUTE_MAX_EXPERTS;
 
 struct Maps {

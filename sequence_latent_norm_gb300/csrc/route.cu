@@ -40,7 +40,8 @@ struct RouteParams {
   const float* bias;
   int *expert, *row, *pair, *start;
   float* weight;
-  unsigned* counts;                      // [chunks, local]
+  unsigned* counts;                      // [chunks, stride]
+  int stride;                            // local, rounded up to 4
 };
 
 template <typename F> LAGA_DEVINL F minus_inf();
@@ -323,7 +324,11 @@ LAGA_DEVINL bool choose(const RouteParams& p, const T* l, const float (&x)[NV],
       if (lane == g)
         mine = second > KEY_OFF ? value_of(first) + value_of(second) : value_of(first);
     };
-    if (p.group_size % 32 == 0) {          // groups of whole registers
+    if (p.group_size == 32) {              // a register each
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (i < p.groups) two_best(i, key[i], KEY_OFF);
+    } else if (p.group_size % 32 == 0) {   // whole registers
       const int regs = p.group_size / 32;
       unsigned a = KEY_OFF, b = KEY_OFF;
       int left = regs, g = 0;
@@ -450,6 +455,16 @@ LAGA_DEVINL bool choose(const RouteParams& p, const T* l, const float (&x)[NV],
 LAGA_DEVINL void place(const RouteParams& p, unsigned* smem) {
   const int EL = p.local, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int warps = blockDim.x >> 5;
+  const int t0 = blockIdx.x * p.chunk, t1 = min(p.tokens, t0 + p.chunk);
+  const int n = (t1 - t0) * p.top_k;
+  const int share = max(((n + warps - 1) / warps + 31) / 32 * 32, 64);
+  const int busy = min(warps, (n + share - 1) / share);
+  const int i0 = warp * share, i1 = min(n, i0 + share);
+  const int* chosen = p.expert + (long long)t0 * p.top_k;
+  int early[2];                          // its loads overlap the counting
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    early[k] = i0 + 32 * k + lane < i1 ? chosen[i0 + 32 * k + lane] - p.first : -1;
   unsigned* base = smem;
   unsigned* next = smem + EL;
   unsigned* hist = smem + 2 * EL;        // [warps, EL]
@@ -458,23 +473,39 @@ LAGA_DEVINL void place(const RouteParams& p, unsigned* smem) {
       next[e] = base[e];
       base[e] = 0;
     }
-    for (int i = threadIdx.x; i < EL * warps; i += blockDim.x) hist[i] = 0;
+    for (int i = threadIdx.x; i < EL * busy; i += blockDim.x) hist[i] = 0;
   } else {
-    for (int i = threadIdx.x; i < EL * (warps + 2); i += blockDim.x) smem[i] = 0;
+    for (int i = threadIdx.x; i < EL * (busy + 2); i += blockDim.x) smem[i] = 0;
     __syncthreads();
-    // chunks in front of this one, and all of them; `parts` threads an expert
-    const int parts = max(1, (int)blockDim.x / EL);
-    for (int i = threadIdx.x; i < EL * parts; i += blockDim.x) {
-      const int e = i % EL;
-      unsigned before = 0, all = 0;
-#pragma unroll 16
-      for (int c = i / EL; c < p.chunks; c += parts) {
-        const unsigned n = p.counts[(size_t)c * EL + e];
-        all += n;
-        before += c < (int)blockIdx.x ? n : 0;
+    // chunks in front of this one, and all of them: a thread 4 experts of every
+    // `parts`-th chunk, ten loads at a time
+    const int quads = p.stride / 4, parts = max(1, (int)blockDim.x / quads);
+    for (int i = threadIdx.x; i < quads * parts; i += blockDim.x) {
+      const int q = i % quads;
+      const uint4* src = reinterpret_cast<const uint4*>(p.counts) + q;
+      uint4 before = make_uint4(0, 0, 0, 0), all = before;
+      for (int c0 = i / quads; c0 < p.chunks; c0 += 10 * parts) {
+        uint4 n[10];
+#pragma unroll
+        for (int k = 0; k < 10; ++k)
+          n[k] = c0 + k * parts < p.chunks ? src[(size_t)(c0 + k * parts) * quads]
+                                           : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 10; ++k) {
+          all.x += n[k].x; all.y += n[k].y; all.z += n[k].z; all.w += n[k].w;
+          if (c0 + k * parts < (int)blockIdx.x) {
+            before.x += n[k].x; before.y += n[k].y; before.z += n[k].z; before.w += n[k].w;
+          }
+        }
       }
-      atomicAdd(&base[e], before);
-      atomicAdd(&next[e], all);
+      const unsigned b4[4] = {before.x, before.y, before.z, before.w};
+      const unsigned a4[4] = {all.x, all.y, all.z, all.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (4 * q + k < EL) {
+          atomicAdd(&base[4 * q + k], b4[k]);
+          atomicAdd(&next[4 * q + k], a4[k]);
+        }
     }
   }
   __syncthreads();
@@ -505,15 +536,15 @@ LAGA_DEVINL void place(const RouteParams& p, unsigned* smem) {
       next[0] = carry;
     }
   }
-  const int t0 = blockIdx.x * p.chunk, t1 = min(p.tokens, t0 + p.chunk);
-  const int n = (t1 - t0) * p.top_k;
-  const int share = max(((n + warps - 1) / warps + 31) / 32 * 32, 64);
-  const int busy = min(warps, (n + share - 1) / share);
-  const int i0 = warp * share, i1 = min(n, i0 + share);
   const long long off = (long long)t0 * p.top_k;
+  auto expert_at = [&](int i) {          // of pair i + lane of the chunk
+    const int k = (i - i0) / 32;
+    if (k < 2) return k == 0 ? early[0] : early[1];
+    return i + lane < i1 ? chosen[i + lane] - p.first : -1;
+  };
   unsigned* h = hist + warp * EL;
   for (int i = i0; i < i1; i += 32) {
-    const int e = i + lane < i1 ? p.expert[off + i + lane] - p.first : -1;
+    const int e = expert_at(i);
     const bool on = e >= 0 && e < EL;
     const unsigned same = __match_any_sync(ALL, on ? e : -1);
     if (on && lane == __ffs(same) - 1) h[e] += __popc(same);
@@ -535,7 +566,7 @@ LAGA_DEVINL void place(const RouteParams& p, unsigned* smem) {
   __syncthreads();
   for (int i = i0; i < i1; i += 32) {
     const bool in = i + lane < i1;
-    const int e = in ? p.expert[off + i + lane] - p.first : -1;
+    const int e = expert_at(i);
     const bool on = e >= 0 && e < EL;
     const unsigned same = __match_any_sync(ALL, on ? e : -1);
     const unsigned at = on ? h[e] + __popc(same & ((1u << lane) - 1)) : 0;
@@ -605,7 +636,7 @@ __global__ void __launch_bounds__(route_threads<NV>())
     place(p, smem);
   } else {
     for (int e = threadIdx.x; e < p.local; e += blockDim.x)
-      p.counts[(size_t)blockIdx.x * p.local + e] = smem[e];
+      p.counts[(size_t)blockIdx.x * p.stride + e] = smem[e];
   }
 }
 
@@ -690,6 +721,7 @@ RouteParams make_params(const laga_route_dims& d) {
   p.chunk = route_chunk(d.tokens, route_warps(d.experts));
   p.chunks = (d.tokens + p.chunk - 1) / p.chunk;
   p.cap = (int)route_rows(d);
+  p.stride = (d.local + 3) / 4 * 4;
   return p;
 }
 
@@ -749,7 +781,7 @@ size_t route_ws_bytes(const laga_route_dims& d) {
   if (d.tokens == 0) return 0;
   const RouteParams p = make_params(d);
   if (p.chunks == 1) return 0;
-  return ((size_t)p.chunks * p.local * 4 + 255) / 256 * 256;
+  return ((size_t)p.chunks * p.stride * 4 + 255) / 256 * 256;
 }
 
 cudaError_t launch_route_fwd(const laga_route_dims& d, const void* logits, const float* bias,
