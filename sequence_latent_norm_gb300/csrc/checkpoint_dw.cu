@@ -128,7 +128,9 @@ struct Counts {
   int first[ROUTE_MAX_EXPERTS + 1];
   int left[PAIRS + 1], total_left, chunk;
 };
-LAGA_DEVINL int first_step(const DwParams& p, int e) { return min(p.start[e], p.rows) / KT; }
+LAGA_DEVINL int first_step(const DwParams& p, int e) {
+  return min(max(p.start[e], 0), p.rows) / KT;
+}
 // By one whole warp; left-over tile i is tile rounds * PAIRS + i of all.
 LAGA_DEVINL void count_left(const DwParams& p, Counts& c, int lane) {
   const int t0 = p.rounds * PAIRS, n = p.experts * p.tiles - t0;

@@ -23,6 +23,16 @@
 //         partial sums, which mm8_join adds up in order)
 // TMEM: two accumulators of up to 224 columns, so that one drains while the
 // other fills, and four sets of scales.
+//
+// What bounds it (16384 x 7168 x 7168, bf16 out: 533 us, 3158 TFLOP/s, 0.82 of
+// twice the measured bf16 rate): the issuing thread and shared memory.  MMAs alone
+// run at 4500 TFLOP/s.  Every wait, commit and copy of scales that stands
+// between them takes 60 to 150 clocks of the one thread that issues: with a wait
+// per 128 of i instead of 256, not asked for ahead, and scales fetched 4 steps at
+// a time, it took 690 us.  Without its loads it takes 468 us: they write 67 bytes a
+// clock into a shared memory that the MMAs read at the same time.  Short K
+// (16384 x 2048 x 7168: 214 us) adds the output's 235 MB; a few rows are bound by
+// b's bytes.
 #include <algorithm>
 
 #include "ckpt8.cuh"
@@ -167,48 +177,56 @@ LAGA_DEVINL void wait_landed(uint64_t (&full)[N], uint32_t it, int* err) {
     mbar_wait_each(&full[i % N], (i / N) & 1, err);
 }
 
-// This warp's 32 columns of y, from the accumulator's lanes, which are columns
-// here, to rows: through a slot of [rows][32 columns] in shared memory and a
-// tensor store, or (a tile's last rows, widths that no tensor map takes) lane
-// by lane.  Of the two warps of these columns each takes every other 32 rows.
+// This warp's 32 columns x 32 rows of y, from the accumulator's lanes, which are
+// columns here, to rows: through a slot of [rows][32 columns] in shared memory
+// and a tensor store, or (a tile's last rows, widths that no tensor map takes)
+// lane by lane.
 template <typename T>
-LAGA_DEVINL void store_tile(const Params& p, const CUtensorMap* ym, const Walk& w, uint32_t acc,
-                            int q, int lane, int first, int col0, uint8_t* out) {
+LAGA_DEVINL void store_rows(const Params& p, const CUtensorMap* ym, const Walk& w,
+                            const float (&v)[32], int lane, int c0, int col0, uint8_t* out) {
   constexpr int R = SLOT_BYTES / (32 * sizeof(T));   // rows of a slot
-  const int j = col0 + lane;
-  const int n = w.r1 - w.r0;
+  const int j = col0 + lane, n = w.r1 - w.r0;
   const long long row0 = (long long)w.z * p.rows + w.r0;
   T* dst = static_cast<T*>(p.y) + row0 * p.n + j;
-  for (int c0 = first; c0 < n; c0 += 64) {
-    uint32_t u[32];
-    tmem_ld32(tmem_addr(acc, q, c0), u);
 #pragma unroll
-    for (int h = 0; h < 32; h += R) {
-      if (p.mapped && c0 + h + R <= n) {
-        T* slot = reinterpret_cast<T*>(out);
-        if (lane == 0) bulk_wait_read0();     // the store that last read the slot
-        __syncwarp();
+  for (int h = 0; h < 32; h += R) {
+    if (p.mapped && c0 + h + R <= n) {
+      T* slot = reinterpret_cast<T*>(out);
+      if (lane == 0) bulk_wait_read0();     // the store that last read the slot
+      __syncwarp();
 #pragma unroll
-        for (int c = 0; c < R; ++c) slot[c * 32 + lane] = from_f32<T>(__uint_as_float(u[h + c]));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (col0 < p.n) tma_store_2d(ym, slot, col0, (int)row0 + c0 + h);
-          bulk_commit();
-        }
-      } else if (j < p.n) {
-#pragma unroll
-        for (int c = 0; c < R; ++c)
-          if (c0 + h + c < n)
-            dst[(long long)(c0 + h + c) * p.n] = from_f32<T>(__uint_as_float(u[h + c]));
+      for (int c = 0; c < R; ++c) slot[c * 32 + lane] = from_f32<T>(v[h + c]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (col0 < p.n) tma_store_2d(ym, slot, col0, (int)row0 + c0 + h);
+        bulk_commit();
       }
+    } else if (j < p.n) {
+#pragma unroll
+      for (int c = 0; c < R; ++c)
+        if (c0 + h + c < n) dst[(long long)(c0 + h + c) * p.n] = from_f32<T>(v[h + c]);
     }
   }
-  if (first == 0 && j < p.n)
-    for (int r = n; r < w.r2 - w.r0; ++r) dst[(long long)r * p.n] = from_f32<T>(0.f);
 }
 
-template <int TN>
+// The tile's rows of no pair.
+template <typename T>
+LAGA_DEVINL void store_zeros(const Params& p, const Walk& w, int j) {
+  T* dst = static_cast<T*>(p.y) + ((long long)w.z * p.rows + w.r1) * p.n + j;
+  if (j < p.n)
+    for (int r = 0; r < w.r2 - w.r1; ++r) dst[(long long)r * p.n] = from_f32<T>(0.f);
+}
+
+LAGA_DEVINL void load_rows(uint32_t taddr, float (&v)[32]) {
+  uint32_t u[32];
+  tmem_ld32(taddr, u);
+#pragma unroll
+  for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(u[c]);
+}
+
+// CHAINS: y in fp32, added up in registers over chains of SF_STEPS steps.
+template <int TN, bool CHAINS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     mm8_kernel(const __grid_constant__ Maps tm, const __grid_constant__ Params p) {
   constexpr int STAGES = Ring<TN>::STAGES, STAGE_BYTES = Ring<TN>::STAGE_BYTES;
@@ -252,8 +270,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int e = e0 + lane;
       int s = 0, t = 0;
       if (e < E) {
-        s = p.experts ? min(p.start[e], p.rows) : 0;
-        t = p.experts ? min(p.start[e + 1], p.rows) : p.rows;
+        s = p.experts ? min(max(p.start[e], 0), p.rows) : 0;
+        t = p.experts ? min(max(p.start[e + 1], 0), p.rows) : p.rows;
       }
       int end = t;
       if (p.pair) {
@@ -329,16 +347,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       bool ok = true;
       const uint32_t ring = sdesc_lo(smem_u32(sm), 16);
       uint32_t alo = ring;
-      while (ok && w.next(p, seg)) {
+      uint32_t d = 0;
+      auto next_accumulator = [&] {
         const int buf = tile & 1;
-        if (tile >= 2 && !mbar_wait_cluster(&acc_empty[buf], ((tile >> 1) - 1) & 1, p.err)) break;
+        if (tile >= 2 && !mbar_wait_cluster(&acc_empty[buf], ((tile >> 1) - 1) & 1, p.err))
+          return false;
         tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(buf * TN_MAX);
+        d = tmem + (uint32_t)(buf * TN_MAX);
+        return true;
+      };
+      while (ok && w.next(p, seg)) {
+        if (!CHAINS && !next_accumulator()) break;
         const int n = w.width();
         const bool wide = n > 128;
         const uint32_t idesc0 = idesc_mx(n, 0);
         uint32_t more = 0;
         for (int left = w.kn; ok && left > 0; left -= SF_STEPS, ++group) {
+          if (CHAINS) {
+            if (!next_accumulator()) {
+              ok = false;
+              break;
+            }
+            more = 0;
+          }
           const int slot = group % SF_SLOTS;
           if (!mbar_wait_cluster(&sf_full[slot], (group / SF_SLOTS) & 1, p.err)) {
             ok = false;
@@ -382,9 +413,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             }
           }
           mma_commit_pair(&sf_empty[slot]);
+          if (CHAINS) mma_commit_pair(&acc_full[tile++ & 1]);
         }
-        mma_commit_pair(&acc_full[buf]);
-        ++tile;
+        if (!CHAINS) mma_commit_pair(&acc_full[tile++ & 1]);
       }
       // the MMAs are done before the pair's shared memory and TMEM are left
       if (tile > 0) mbar_wait_each(&acc_full[(tile - 1) & 1], ((tile - 1) >> 1) & 1, p.err);
@@ -431,19 +462,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     uint8_t* slot = sm + Ring<TN>::OUT_OFF + (warp - 4) * SLOT_BYTES;
     const int first = (warp - 4) / 4 * 32;
     if (lane == 0) tma_prefetch_desc(&tm.y);
-    for (uint32_t tile = 0; w.next(p, seg); ++tile) {
-      const int buf = tile & 1;
-      mbar_wait_or_pass(&acc_full[buf], (tile >> 1) & 1, polls, p.err);
+    uint32_t tile = 0;
+    uint32_t acc = 0;
+    auto full_accumulator = [&] {
+      mbar_wait_or_pass(&acc_full[tile & 1], (tile >> 1) & 1, polls, p.err);
       tc_fence_after();
-      const uint32_t acc = tmem + (uint32_t)(buf * TN_MAX);
-      const int col0 = w.f * FT + (int)rank * 128 + q * 32;
-      if (p.bf16)
-        store_tile<__nv_bfloat16>(p, &tm.y, w, acc, q, lane, first, col0, slot);
-      else
-        store_tile<float>(p, &tm.y, w, acc, q, lane, first, col0, slot);
+      acc = tmem + (uint32_t)((tile & 1) * TN_MAX);
+    };
+    auto release_accumulator = [&] {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0 && polls) mbar_arrive_cluster(smem_cluster_addr(&acc_empty[buf], 0));
+      if (lane == 0 && polls) mbar_arrive_cluster(smem_cluster_addr(&acc_empty[tile & 1], 0));
+      ++tile;
+    };
+    while (w.next(p, seg)) {
+      const int col0 = w.f * FT + (int)rank * 128 + q * 32, n = w.r1 - w.r0;
+      if constexpr (CHAINS) {
+        // The tensor core drops what does not fit below the accumulator's last
+        // place: sums of 7168 positive terms came out 1.1e-6 short, of 16384
+        // 3.9e-6; as chains of 2048 that are added here, 3.7e-7 and 5.1e-7
+        // (16384 x 7168 x 1536: 142 us, 134 us in one chain).
+        constexpr int PARTS = (TN + 63) / 64;
+        float v[PARTS][32];
+        for (int k = 0; k < w.kn; k += SF_STEPS) {
+          full_accumulator();
+#pragma unroll
+          for (int i = 0; i < PARTS; ++i) {
+            if (first + 64 * i >= n) break;
+            if (k == 0) {
+              load_rows(tmem_addr(acc, q, first + 64 * i), v[i]);
+            } else {
+              float more[32];
+              load_rows(tmem_addr(acc, q, first + 64 * i), more);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) v[i][c] += more[c];
+            }
+          }
+          release_accumulator();
+        }
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) {
+          if (first + 64 * i >= n) break;
+          store_rows<float>(p, &tm.y, w, v[i], lane, first + 64 * i, col0, slot);
+        }
+        if (first == 0) store_zeros<float>(p, w, col0 + lane);
+      } else {
+        full_accumulator();
+        for (int c0 = first; c0 < n; c0 += 64) {
+          float v[32];
+          load_rows(tmem_addr(acc, q, c0), v);
+          if (p.bf16)
+            store_rows<__nv_bfloat16>(p, &tm.y, w, v, lane, c0, col0, slot);
+          else
+            store_rows<float>(p, &tm.y, w, v, lane, c0, col0, slot);
+        }
+        release_accumulator();
+        if (first == 0) {
+          if (p.bf16)
+            store_zeros<__nv_bfloat16>(p, w, col0 + lane);
+          else
+            store_zeros<float>(p, w, col0 + lane);
+        }
+      }
     }
     if (lane == 0) bulk_wait_read0();
     __syncwarp();
@@ -571,7 +651,8 @@ cudaError_t launch_mm8(int rows, int K, int N, int experts, bool fp32, const voi
   if (p.mapped &&
       (e = out_map(&tm.y, p.y, N, (uint64_t)pl.splits * rows, p.bf16)) != cudaSuccess)
     return e;
-  auto k = pl.tn > 32 ? mm8_kernel<TN_MAX> : mm8_kernel<32>;
+  auto k = pl.tn > 32 ? fp32 ? mm8_kernel<TN_MAX, true> : mm8_kernel<TN_MAX, false>
+                      : fp32 ? mm8_kernel<32, true> : mm8_kernel<32, false>;
   const int smem = pl.tn > 32 ? Ring<TN_MAX>::SMEM_BYTES : Ring<32>::SMEM_BYTES;
   if ((e = allow_smem(k, smem)) != cudaSuccess) return e;
   const long long most = ((long long)rows / pl.tn + std::min(blocks, rows)) * pl.f_tiles * pl.splits;

@@ -443,3 +443,38 @@ def test_values_at_the_ends_of_the_scales():
     assert np.isinf(y[big]).all() and (np.abs(y[small]) <= 2.0 ** -119).all()
     rest = ~small & ~big
     assert (y[rest] == want[rest]).all() and (y[3] == 0).all()
+
+
+def test_more_than_2_31_elements():
+    """Outputs, rows and codes whose offsets do not fit 32 bits; values that tell
+    the rows apart."""
+    laga = _laga()
+    T, n = 140000, 16384                               # 2.3e9 elements
+    x = torch.zeros(T, 128, device=DEV)
+    r = torch.arange(T, device=DEV)
+    for c in range(18):                                # the row number in bits: exact codes
+        x[:, c] = (r >> c & 1).float()
+    w = torch.zeros(128, n, device=DEV)
+    w[:18, -1] = w[:18, 5] = 1.0
+    w[:18, -2] = torch.arange(1, 19, device=DEV).float().clamp(max=16)
+    y = laga.linear8(laga.pack8(x), laga.pack_weight8(w, backward=False))
+    laga._lib.sync_check()
+    ones, weighted = x.sum(dim=1), x[:, :18] @ w[:18, -2]
+    assert torch.equal(y[:, -1].float(), ones) and torch.equal(y[:, 5].float(), ones)
+    assert torch.equal(y[:, -2].float(), weighted.to(torch.bfloat16).float())
+    assert not y[:, 6:-2].any()
+    a8 = laga.swiglu8(y)                               # u = silu's partner: columns 8192 on
+    laga._lib.sync_check()
+    assert a8.shape == (T, n // 2) and not a8.data[:, :n // 2].any()
+    routes = laga.Routes(torch.zeros(T, 1, dtype=torch.int32, device=DEV), torch.ones(T, 1, device=DEV),
+                         r.flip(0)[:, None].int().contiguous(), r.flip(0).int().contiguous(),
+                         torch.tensor([0, T], dtype=torch.int32, device=DEV), 1)
+    out = laga.combine(y, routes)
+    dy, dw = laga.combine_grad(out, routes, y=y)
+    laga._lib.sync_check()
+    assert torch.equal(out[:, -1], y[:, -1].flip(0)) and torch.equal(dy, y)
+    want = 2 * ones.flip(0).double() ** 2 + weighted.to(torch.bfloat16).flip(0).double() ** 2
+    assert ((dw[:, 0].double() - want).abs() <= 2.0 ** -22 * want).all()
+    back = laga.spread8(a8, routes)
+    laga._lib.sync_check()
+    assert back.data.shape == a8.data.shape and torch.equal(back.data[-1], a8.data[0])
