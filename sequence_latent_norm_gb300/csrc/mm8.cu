@@ -24,14 +24,15 @@
 // TMEM: two accumulators of up to 224 columns, so that one drains while the
 // other fills, and four sets of scales.
 //
-// What bounds it (16384 x 7168 x 7168, bf16 out: 533 us, 3158 TFLOP/s, 0.82 of
-// twice the measured bf16 rate): the issuing thread and shared memory.  MMAs alone
-// run at 4500 TFLOP/s.  Every wait, commit and copy of scales that stands
-// between them takes 60 to 150 clocks of the one thread that issues: with a wait
-// per 128 of i instead of 256, not asked for ahead, and scales fetched 4 steps at
-// a time, it took 690 us.  Without its loads it takes 468 us: they write 67 bytes a
-// clock into a shared memory that the MMAs read at the same time.  Short K
-// (16384 x 2048 x 7168: 214 us) adds the output's 235 MB; a few rows are bound by
+// What bounds it (16384 x 7168 x 7168, bf16 out: 531 us, 3170 TFLOP/s, 0.83 of
+// twice the measured bf16 rate): the supply of operands, next to the issuing
+// thread.  MMAs alone run at 4500 TFLOP/s.  Every wait, commit and copy of
+// scales that stands between them takes 60 to 150 clocks of the one thread that
+// issues: with a wait per 128 of i instead of 256 and scales fetched 4 steps at a
+// time it took 690 us.  Without its loads it takes 468 us, and 508 us where all of
+// them hit the same lines of L2: they write 45 bytes a clock into a shared
+// memory that the MMAs read at the same time.  Short K
+// (16384 x 2048 x 7168: 216 us) adds the output's 235 MB; a few rows are bound by
 // b's bytes.
 #include <algorithm>
 
@@ -155,19 +156,6 @@ LAGA_DEVINL void copy_scales_pair(uint32_t taddr, uint32_t saddr) {
   const uint64_t desc = (uint64_t)(8u | 1u << 14) << 32 | ((saddr >> 4) & 0x3fffu);
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
                : "memory");
-}
-
-// Whether a phase has completed, without waiting for it.
-LAGA_DEVINL bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 
 // A thread that copies leaves when its last copies have landed.
@@ -343,7 +331,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // This thread's own instructions set the pace (MMAs of 112 clocks): everything that can is carried along instead of computed.
       uint32_t group = 0, set = 0, tile = 0;
       uint32_t st = 0, parity = 0;         // the next stage and its phase
-      bool ready = false;                  // it has been seen full
       bool ok = true;
       const uint32_t ring = sdesc_lo(smem_u32(sm), 16);
       uint32_t alo = ring;
@@ -386,7 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             const int m = min(4, words - i0);
             uint32_t idesc = idesc0;
             for (int i = 0; i < m; i += HALVES) {
-              if (!ready && !mbar_wait_each(&full[st], parity, p.err)) {
+              if (!mbar_wait_each(&full[st], parity, p.err)) {
                 ok = false;
                 break;
               }
@@ -395,9 +382,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               st = st + 1 == STAGES ? 0 : st + 1;
               parity ^= st == 0;
               alo = st == 0 ? ring : alo + (STAGE_BYTES >> 4);
-              // ask for the next stage now: the answer arrives while these MMAs
-              // are issued
-              ready = mbar_test(&full[st], parity);
 #pragma unroll
               for (int h = 0; h < HALVES; ++h) {
                 if (h > 0 && i + h >= m) break;
