@@ -177,6 +177,7 @@ class LagaAttentionBlock:
         dq_flat = dq.reshape(rows, -1)
         dc_flat = dc.reshape(rows, -1)
         if fp8:
+            dc_flat = dc_flat.to(dq.dtype)   # (in fp32 its weight gradient would take three products)
             dh = (linear8_dx(pack8(dq_flat), w_q, dtype=dq.dtype) +
                   linear8_dx(pack8(dc_flat), w_kva, dtype=dq.dtype)).reshape(h_shape)
         else:

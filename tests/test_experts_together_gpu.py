@@ -254,7 +254,7 @@ def test_projections_in_8_bits(io):
     check(seen["c"], codes(b["h"]), weight(b["w_kva"]))
     check(y, codes(seen["out"]), weight(b["w_o"]))
     check(seen["d_out"], codes(b["dy"]), weight(b["w_o"]).T)
-    dq, dc = seen["grads"][:2]
+    dq, dc = seen["grads"][0], seen["grads"][1].to(dt)
     one, two = (codes(t) @ weight(w).T for t, w in ((dq, b["w_q"]), (dc, b["w_kva"])))
     mags = [np.abs(codes(t)) @ np.abs(weight(w)).T for t, w in ((dq, b["w_q"]), (dc, b["w_kva"]))]
     lim = sum(700 * 2.0 ** -23 * m for m in mags) + 2 * half * (np.abs(one) + np.abs(two))
