@@ -13,7 +13,7 @@ namespace {
 
 // ------------------------------------------------------------------ rows
 // A warp copies one row of codes, 16 bytes a lane and eight such loads at a
-// time (16384 rows of 7232 bytes from 2048: 35 us one at a time).
+// time (16384 rows of 7232 bytes from 2048: 27 us, 35 us one at a time).
 __global__ void __launch_bounds__(256)
     spread8_kernel(const uint8_t* __restrict__ ck, const int* __restrict__ pair,
                    const int* __restrict__ end, uint8_t* __restrict__ out, int rows, int tokens,
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(256)
 // dy[r] = w dout_t, dw = <dout_t, y[r]> of the row's pair: a warp a row, with
 // LOADS vectors of each side under way.  It goes by rows, not by pairs: y and dy
 // stream through HBM in order then, and dout, which every choice reads, stays in
-// L2.  (16384 x 7168 rows of 2048 tokens by pairs: 135 to 183 us.)  Rows of no
+// L2.  (16384 x 7168 rows of 2048 tokens: 91 us, by pairs 131 to 183 us.)  Rows of no
 // pair get zeros, pairs without a row a dw of zero.
 constexpr int LOADS = 4;
 
@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------ activation
 // Each kernel moves 4 to 10 bytes a channel and has some 25 instructions for it
 // at that rate, so the sigmoid is two special functions; channels come in
-// vectors of 8 where the width allows.  (16384 x 2048 bf16 with expf, a division
-// and single channels: 82 us forward.)
+// vectors of 8 where the width allows.  (16384 x 2048 bf16: 36 us forward, and 82 us
+// with expf, a division and single channels.)
 
 // sigmoid(g) and 1 - sigmoid(g) = e^-g sigmoid(g), each within 6 units of its
 // last place: the exponent's product with log2 e is carried in two parts, since
