@@ -6,7 +6,7 @@ with the CUDA path.  Test infrastructure only.
 
 import numpy as np
 
-from .residual import GROUP, E_MAX, E_MIN, pack, row_layout, unpack
+from .residual import E_MAX, E_MIN, GROUP, e4m3_values, pack, row_layout, unpack
 
 TINY = 1e-20
 
@@ -108,27 +108,26 @@ def pack_weight(w):
     cn, pn = row_layout(N)
     g = np.zeros((E, ck, cn))
     g[:, :K, :N] = w
+    blocks = g.reshape(E, ck // GROUP, GROUP, cn // GROUP, GROUP)
+    bad = ~np.isfinite(blocks).all(axis=(2, 4))
+    m, x = np.frexp(np.where(bad[:, :, None, :, None], 0.0, np.abs(blocks)).max(axis=(2, 4)))
+    x = np.where(m <= 448.0 / 512.0, x - 9, x - 8)          # m 2^x <= 448 2^e
+    x = np.where(m == 0, E_MIN, np.clip(x, E_MIN, E_MAX))
+    t = np.where(bad[:, :, None, :, None], 0.0, blocks) / 2.0 ** x[:, :, None, :, None]
+    t = np.clip(t, -448.0, 448.0).reshape(E, ck, cn)
+    size = np.abs(t)
+    step = 2.0 ** (np.maximum(np.floor(np.log2(np.maximum(size, 2.0 ** -7))), -6.0) - 3.0)
+    size = np.rint(size / step) * step                      # ties to even
+    table = e4m3_values()[:0x7f]
+    code = np.searchsorted(table, size)
+    assert (table[code] == size).all()
+    code = (code + np.where(np.signbit(t), 128, 0)).astype(np.uint8)
+    byte = np.where(bad, 255, x + 127).astype(np.uint8)
     fwd, bwd = np.zeros((E, N, pk), np.uint8), np.zeros((E, K, pn), np.uint8)
-    for e in range(E):
-        for i in range(0, ck, GROUP):
-            for j in range(0, cn, GROUP):
-                b = g[e, i:i + GROUP, j:j + GROUP]
-                # one group of 128 x 128 values: the row format's rule for a scale
-                m, x = np.frexp(np.abs(b).max()) if np.isfinite(b).all() else (0.0, 0)
-                x = x - 9 if m <= 448.0 / 512.0 else x - 8
-                x = E_MIN if m == 0 else min(max(x, E_MIN), E_MAX)
-                byte = x + 127 if np.isfinite(b).all() else 255
-                # codes: each value as a row of its own under that scale
-                unit = np.zeros((b.size, 2))
-                unit[:, 0] = np.where(np.isfinite(b), np.clip(b, -448.0 * 2.0 ** x, 448.0 * 2.0 ** x),
-                                      0.0).reshape(-1)
-                unit[:, 1] = 448.0 * 2.0 ** x
-                code = pack(unit)[:, 0].reshape(b.shape) if byte != 255 else np.zeros(b.shape, np.uint8)
-                ni, nj = min(GROUP, K - i), min(GROUP, N - j)
-                fwd[e, j:j + nj, i:i + GROUP] = code[:, :nj].T
-                fwd[e, j:j + nj, ck + i // GROUP] = byte
-                bwd[e, i:i + ni, j:j + GROUP] = code[:ni]
-                bwd[e, i:i + ni, cn + j // GROUP] = byte
+    fwd[:, :, :ck] = code[:, :, :N].transpose(0, 2, 1)
+    fwd[:, :, ck:ck + ck // GROUP] = np.repeat(byte.transpose(0, 2, 1), GROUP, axis=1)[:, :N]
+    bwd[:, :, :cn] = code[:, :K]
+    bwd[:, :, cn:cn + cn // GROUP] = np.repeat(byte, GROUP, axis=1)[:, :K]
     return fwd.reshape(E * N, pk), bwd.reshape(E * K, pn)
 
 

@@ -5,10 +5,10 @@
 // redux.sync for the value, one for the lowest expert that has it).  The order
 // of close scores must not depend on how a score was rounded, so every decision
 // is checked: the choice runs in fp32, and where the distance between two
-// neighbours of the order is within what fp32 may have lost, it
-// is settled in fp64: that of the chosen experts and of those just below them by
-// one score a lane (about a token in 1000 of random logits of 256 experts), a
-// choice of groups, or of more experts than that, by going over the token again.
+// neighbours of the order is within what fp32 may have lost, it is settled in
+// fp64: that of the chosen experts and of those just below them by one score a
+// lane (about a token in 1000 of random logits of 256 experts), that of groups by
+// one group a lane, and what is left by going over the whole token again.
 // (Equal logits under equal biases are equal in both, and no reason to.)  fp64
 // runs at 2 operations a clock and SM on this part: a second run of the whole
 // token costs 10 us of latency, and with one for every close score the kernel
@@ -276,12 +276,12 @@ LAGA_DEVINL float score_of(const RouteParams& p, const T* l, const float (&x)[NV
   return p.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - top) / z;
 }
 
-// The choice in fp32: lane j's expert.  `score`: its score.  False: the order is
-// not certain.
+// The choice in fp32: lane j's expert.  `score`: its score.  `reach`: no sum of
+// a score and a finite bias is larger.  False: the order is not certain.
 template <int NV, typename T>
 LAGA_DEVINL bool choose(const RouteParams& p, const T* l, const float (&x)[NV],
-                        const float (&bias)[NV], const int (&group)[NV], int lane, int& expert,
-                        float& score) {
+                        const float (&bias)[NV], const int (&group)[NV], float reach, int lane,
+                        int& expert, float& score) {
   const float ninf = minus_inf<float>();
   unsigned key[NV];
   float top = 0.f, inv = 0.f;
@@ -314,8 +314,9 @@ LAGA_DEVINL bool choose(const RouteParams& p, const T* l, const float (&x)[NV],
   // What fp32 may have lost of a score.  Of a sigmoid s: (1 - s) (1.25 |x| + 4)
   // units of its last place (the exponential's error) and three roundings, no
   // more than 6 units of 2^-24 of one for any x.  Of a softmax: the rounded
-  // difference's and the exponential's, and its sum's; no score is above inv.
-  const float lost = (p.sigmoid ? 6.f : (13.f + NV) * inv) * 0x1p-24f;
+  // difference's and the exponential's, and its sum's (weighted by the terms, no
+  // more than log E + 2 units, and NV + 5 additions); no score is above inv.
+  const float lost = (p.sigmoid ? 6.f : (20.f + NV) * inv) * 0x1p-24f;
   if (p.top_groups < p.groups) {
     float mine = ninf;                     // lane g: the score of group g
     auto two_best = [&](int g, unsigned a, unsigned b) {
@@ -369,7 +370,7 @@ LAGA_DEVINL bool choose(const RouteParams& p, const T* l, const float (&x)[NV],
     const float in = __shfl_sync(ALL, mine, __ffs(__ballot_sync(ALL, rank == p.top_groups - 1)) - 1);
     const float out = __shfl_sync(ALL, mine, __ffs(__ballot_sync(ALL, rank == p.top_groups)) - 1);
     // four scores, their sums with the biases, and the sums of two
-    const float tol = 4.f * lost + (4.f + 4.f * (fabsf(in) + fabsf(out))) * 0x1p-24f;
+    const float tol = 4.f * lost + (4.f * reach + 4.f * (fabsf(in) + fabsf(out))) * 0x1p-24f;
     if (out > ninf && !(in - out > tol)) {
       // (an infinite sum has no distance)
       keep = fabsf(in) <= 3.402823466e38f
@@ -593,8 +594,13 @@ __global__ void __launch_bounds__(route_threads<NV>())
 #pragma unroll
   for (int i = 0; i < NV; ++i) bias[i] = bias_of(p, 32 * i + lane);
   bool bad_bias = false;
+  float reach = 0.f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) bad_bias = bad_bias || isnan(bias[i]);
+  for (int i = 0; i < NV; ++i) {
+    bad_bias = bad_bias || isnan(bias[i]);
+    if (fabsf(bias[i]) <= 3.402823466e38f) reach = fmaxf(reach, fabsf(bias[i]));
+  }
+  reach = 1.f + warp_max(reach);
   int group[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) group[i] = min((32 * i + lane) / p.group_size, 31);
@@ -618,7 +624,7 @@ __global__ void __launch_bounds__(route_threads<NV>())
     }
     int expert;
     float score;
-    if (!choose<NV, T>(p, l, x, bias, group, lane, expert, score)) {
+    if (!choose<NV, T>(p, l, x, bias, group, reach, lane, expert, score)) {
       expert = choose_wide<NV, T>(p, l, lane);
       score = score_of(p, l, x, lane, expert);
     }

@@ -141,6 +141,20 @@ def test_route_close_scores_in_64_bits():
     _route(T, E, 8, logits=l, bias=b)
 
 
+def test_route_close_groups_in_64_bits():
+    """Groups whose two best sums differ by less than fp32 shows: large biases
+    of both signs that cancel within a group, and equal groups."""
+    g = _gen(12)
+    T, E, G = 600, 64, 8
+    l = torch.randn(T, 1, 8, generator=g).repeat(1, G, 1)      # every group the same logits
+    l[:, 1::2] += 1e-6 * torch.randn(T, G // 2, 8, generator=g)
+    b = torch.zeros(G, 8)
+    b[:, 0], b[:, 1] = 100.0, -90.0 + torch.arange(8) * 2.0 ** -17
+    for bias in (b.reshape(-1), None):
+        for score in ("sigmoid", "softmax"):
+            _route(T, E, 4, logits=l.reshape(T, E), bias=bias, groups=G, top_groups=3, score=score)
+
+
 def test_route_masked_experts_and_tokens():
     g = _gen(7)
     l = torch.randn(300, 48, generator=g)
