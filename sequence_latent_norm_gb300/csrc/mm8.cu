@@ -70,9 +70,13 @@ struct Ring {
   static_assert(SMEM_BYTES + (int)sizeof(int) * 3 * (ROUTE_MAX_EXPERTS + 1) + 1024 + 256 <=
                     228 * 1024,
                 "shared memory, with the segments and the barriers");
-  // A set of scales is written again SF_SETS groups of 4 steps later.  By then
-  // the MMAs that read it are done: the ring lets STAGES stages be in flight.
-  static_assert((SF_SETS - 1) * 4 >= STAGES * HALVES, "scales outlive the MMAs that read them");
+  // A set of scales is written again SF_SETS words later, and the MMAs that read
+  // it must be done by then.  Words of one tile or two have at least SF_SETS - 1
+  // others between them, of two stages each but for a tile's last one, which may
+  // have one: no fewer stages than the ring lets be in flight.  (Words of tiles
+  // further apart have a wait for an accumulator between them.)
+  static_assert((SF_SETS - 1) * (4 / HALVES) - 1 >= STAGES,
+                "scales outlive the MMAs that read them");
 };
 constexpr int THREADS = 128 + 32 * EPI_WARPS;
 constexpr int TMEM_COLS = 512, SF_COL = 2 * TN_MAX, SF_COLS = 16;
@@ -330,7 +334,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      // This thread's own instructions set the pace (MMAs of 112 clocks): everything that can is carried along instead of computed.
+      // This thread's own instructions are a good part of the pace (MMAs take 112
+      // clocks): what can be is carried along instead of computed.
       uint32_t group = 0, set = 0, tile = 0;
       uint32_t st = 0, parity = 0;         // the next stage and its phase
       bool ok = true;
@@ -549,7 +554,7 @@ Mm8Plan mm8_plan(int rows, int K, int N, int experts) {
   Mm8Plan pl{};
   pl.f_tiles = (N + FT - 1) / FT;
   pl.steps = ck_cols(K) / KS;
-  // Rows of a tile: the fewest clocks of the fullest pair, a stage costing its
+  // Rows of a tile: the fewest clocks of the fullest pair, a step costing its
   // MMAs, or the bytes that it loads at about 45 a clock, or its issue.
   const int used = experts ? std::min(experts, rows) : 1;
   const int each = (rows + used - 1) / used;
@@ -557,8 +562,8 @@ Mm8Plan mm8_plan(int rows, int K, int N, int experts) {
   for (int tn = 32; tn <= TN_MAX; tn += 32) {
     const long long tiles = (long long)used * ((each + tn - 1) / tn) * pl.f_tiles;
     const long long turns = (tiles + PAIRS - 1) / PAIRS;
-    const double stage = std::max({2.0 * tn, (W_BYTES + tn / 2 * KS) / 45.0, 220.0});
-    const double cost = turns * (pl.steps * stage + 600.0);
+    const double step = std::max({2.0 * tn, (W_BYTES + tn / 2 * KS) / 45.0, 220.0});
+    const double cost = turns * (pl.steps * step + 600.0);
     if (best < 0 || cost < best) {
       best = cost;
       pl.tn = tn;
@@ -566,7 +571,7 @@ Mm8Plan mm8_plan(int rows, int K, int N, int experts) {
   }
   const long long tiles = (long long)used * ((each + pl.tn - 1) / pl.tn) * pl.f_tiles;
   // Pieces of K where the tiles leave half of the pairs without work: whole
-  // words of scale bytes, 4 stages, at least
+  // words of scale bytes, 4 steps, at least
   const int words = (pl.steps + 3) / 4;
   int splits = 1;
   if (2 * tiles <= PAIRS) splits = (int)std::min<long long>(PAIRS / tiles, words);
@@ -610,8 +615,8 @@ size_t mm8_ws_bytes(int rows, int K, int N, int experts, bool fp32) {
 }
 
 cudaError_t launch_mm8(int rows, int K, int N, int experts, bool fp32, const void* a,
-                       const void* b, const int* start, const int* pair, void* y, unsigned char* ws, int* err,
-                       cudaStream_t st) {
+                       const void* b, const int* start, const int* pair, void* y,
+                       unsigned char* ws, int* err, cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
   const Mm8Plan pl = mm8_plan(rows, K, N, experts);
   Params p{};
@@ -641,7 +646,8 @@ cudaError_t launch_mm8(int rows, int K, int N, int experts, bool fp32, const voi
                       : fp32 ? mm8_kernel<32, true> : mm8_kernel<32, false>;
   const int smem = pl.tn > 32 ? Ring<TN_MAX>::SMEM_BYTES : Ring<32>::SMEM_BYTES;
   if ((e = allow_smem(k, smem)) != cudaSuccess) return e;
-  const long long most = ((long long)rows / pl.tn + std::min(blocks, rows)) * pl.f_tiles * pl.splits;
+  const long long most =
+      ((long long)rows / pl.tn + std::min(blocks, rows)) * pl.f_tiles * pl.splits;
   {
     LaunchScope ls_("mm8", st);
     k<<<2 * (int)std::min<long long>(PAIRS, most), THREADS, smem, st>>>(tm, p);

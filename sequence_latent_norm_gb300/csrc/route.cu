@@ -47,7 +47,9 @@ struct RouteParams {
 
 template <typename F> LAGA_DEVINL F minus_inf();
 template <> LAGA_DEVINL float minus_inf<float>() { return __int_as_float(0xff800000); }
-template <> LAGA_DEVINL double minus_inf<double>() { return __longlong_as_double(0xfff0000000000000LL); }
+template <> LAGA_DEVINL double minus_inf<double>() {
+  return __longlong_as_double(0xfff0000000000000LL);
+}
 
 LAGA_DEVINL float warp_max(float v) {
 #pragma unroll
@@ -235,7 +237,8 @@ __device__ __noinline__ unsigned regroup_wide(const RouteParams& p, const unsign
       }
       e[n] = (int)__reduce_min_sync(ALL, f0);
     }
-    if (e[2] >= 0 && !(v[1] - v[2] > 2.f * lost + (fabsf(v[1]) + fabsf(v[2])) * 0x1p-23f)) return 0u;
+    if (e[2] >= 0 && !(v[1] - v[2] > 2.f * lost + (fabsf(v[1]) + fabsf(v[2])) * 0x1p-23f))
+      return 0u;
     if (lane == g) {
       e1 = e[0];
       e2 = e[1];
@@ -367,8 +370,9 @@ LAGA_DEVINL bool choose(const RouteParams& p, const T* l, const float (&x)[NV],
     }
     if (lane >= p.groups) rank = 64;
     unsigned keep = __ballot_sync(ALL, rank < p.top_groups);
-    const float in = __shfl_sync(ALL, mine, __ffs(__ballot_sync(ALL, rank == p.top_groups - 1)) - 1);
-    const float out = __shfl_sync(ALL, mine, __ffs(__ballot_sync(ALL, rank == p.top_groups)) - 1);
+    const int last = __ffs(__ballot_sync(ALL, rank == p.top_groups - 1)) - 1;
+    const int first_out = __ffs(__ballot_sync(ALL, rank == p.top_groups)) - 1;
+    const float in = __shfl_sync(ALL, mine, last), out = __shfl_sync(ALL, mine, first_out);
     // four scores, their sums with the biases, and the sums of two
     const float tol = 4.f * lost + (4.f * reach + 4.f * (fabsf(in) + fabsf(out))) * 0x1p-24f;
     if (out > ninf && !(in - out > tol)) {
@@ -744,7 +748,8 @@ cudaError_t launch_fwd(const RouteParams& p, bool fp32, const void* logits, cuda
   {
     LaunchScope ls_("route", st);
     if (fp32)
-      route_kernel<NV, float><<<p.chunks, threads, smem, st>>>(static_cast<const float*>(logits), p);
+      route_kernel<NV, float><<<p.chunks, threads, smem, st>>>(static_cast<const float*>(logits),
+                                                               p);
     else
       route_kernel<NV, __nv_bfloat16><<<p.chunks, threads, smem, st>>>(
           static_cast<const __nv_bfloat16*>(logits), p);

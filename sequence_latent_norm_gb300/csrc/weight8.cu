@@ -12,8 +12,8 @@ namespace {
 // 128-byte pieces of the rows of W^T (fwd) and of W (bwd).  A thread loads 8
 // columns of 8 rows.  The codes are turned in shared memory in words of 4: word w
 // of row r sits at w ^ (r / 4), so that reading rows 4 l .. 4 l + 3 of one word by
-// lane l, like writing, meets every bank once.  Bound by HBM from some 10^7 values on (7168 x 1536 bf16: 10 us
-// within a graph).
+// lane l, like writing, meets every bank once.  Bound by HBM from some 10^7 values
+// on (7168 x 1536 bf16: 10 us within a graph).
 constexpr int WB = CK_GROUP;
 
 template <typename T, int V>
