@@ -203,6 +203,43 @@ def test_route_many_tokens_twice_the_same():
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("T,E,k,groups,score,io", [(200003, 64, 6, 4, "sigmoid", "fp32"),
+                                                   (70001, 1000, 32, 1, "softmax", "fp32"),
+                                                   (40000, 256, 8, 8, "sigmoid", "bf16")])
+def test_route_a_long_batch(T, E, k, groups, score, io):
+    """Chunks of more pairs than a block has threads, against torch in 64 bits."""
+    laga = _laga()
+    l = torch.randn(T, E, generator=torch.Generator(DEV).manual_seed(T), device=DEV).to(DT[io])
+    b = 0.05 * torch.randn(E, generator=torch.Generator(DEV).manual_seed(E), device=DEV)
+    top_groups = max(1, groups // 2)
+    r = laga.Router(E, k, score=score, groups=groups, top_groups=top_groups, io_dtype=io, device=DEV)
+    out = r.forward(l, b)
+    _sync()
+    s = torch.sigmoid(l.double()) if score == "sigmoid" else torch.softmax(l.double(), dim=1)
+    c = s + b.double()
+    if top_groups < groups:
+        two = c.view(T, groups, -1).sort(dim=2, descending=True).values[:, :, :2].sum(dim=2)
+        best = two.sort(dim=1, descending=True, stable=True).indices[:, :top_groups]
+        keep = torch.zeros(T, groups, dtype=torch.bool, device=DEV).scatter_(1, best, True)
+        c = c.masked_fill(~keep.repeat_interleave(E // groups, dim=1), -float("inf"))
+    expert = c.sort(dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(out.expert.long(), expert)
+    w = s.gather(1, expert)
+    w = w / w.sum(dim=1, keepdim=True)
+    assert ((out.weight.double() - w).abs() <= (24 + 4 * k + 4 * 8) * 2.0 ** -24 * w).all()
+    flat = expert.reshape(-1)
+    count = torch.bincount(flat, minlength=E)
+    start = torch.cat([count.new_zeros(1), ((count + 127) // 128 * 128).cumsum(0)])
+    assert torch.equal(out.start.long(), start)
+    by = torch.argsort(flat, stable=True)
+    before = torch.cat([count.new_zeros(1), count.cumsum(0)])[:-1]
+    at = start[flat[by]] + torch.arange(len(by), device=DEV) - before[flat[by]]
+    pair = torch.full((out.rows,), -1, dtype=torch.long, device=DEV)
+    pair[at] = by
+    assert torch.equal(out.pair.long(), pair)
+    assert torch.equal(out.row.reshape(-1)[by].long(), at)
+
+
 def test_route_no_tokens():
     r = _laga().Router(16, 2, device=DEV)
     out = r.forward(torch.zeros(0, 16, device=DEV))
