@@ -12,8 +12,8 @@
 // (Equal logits under equal biases are equal in both, and no reason to.)  fp64
 // runs at 2 operations a clock and SM on this part: a second run of the whole
 // token costs 10 us of latency, and with one for every close score the kernel
-// took 78 us for 16384 x 256, and 46 us without any; it takes 37 us now, bound
-// by its instructions, some 1550 a token and warp.
+// took 78 us for 16384 x 256, and 46 us without any; it takes some 30 us now,
+// bound by its instructions, 1330 a token and warp.
 //
 // The order of the rows: a block counts its chunk's rows by expert; the second
 // kernel (the same one, where the batch is one chunk) adds up the chunks in
@@ -182,13 +182,29 @@ __device__ __noinline__ int choose_wide(const RouteParams& p, const T* l, int la
   return expert;
 }
 
+// (The functions that settle what is close read the token's logits again: what is
+// handed to them stays in registers, and they hardly ever run.)
+template <int NV, typename T>
+LAGA_DEVINL void logits_of(const RouteParams& p, const T* l, int lane, float (&x)[NV]) {
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    x[i] = logit_of(p, l, 32 * i + lane, bias_of(p, 32 * i + lane), nan);
+}
+
 // The lanes' experts in the order of their sums in 64 bits; the ones of `all`
 // lanes, of which the best top_k stay.
-template <int NV>
-__device__ __noinline__ int reorder_wide(const RouteParams& p, const float (&x)[NV], float top,
-                                         float l, float b, int expert, int all, int lane) {
-  const double z = p.sigmoid ? 1.0 : wide_sum<NV>(x, top);
-  const double c = expert >= 0 ? wide_score(p, l, top, z) + (double)b : minus_inf<double>();
+template <int NV, typename T>
+__device__ __noinline__ int reorder_wide(const RouteParams& p, const T* l, float top, int expert,
+                                         int all, int lane) {
+  double z = 1.0;
+  if (!p.sigmoid) {
+    float x[NV];
+    logits_of<NV>(p, l, lane, x);
+    z = wide_sum<NV>(x, top);
+  }
+  double c = minus_inf<double>();
+  if (expert >= 0) c = wide_score(p, to_f32(l[expert]), top, z) + (double)bias_of(p, expert);
   int rank = 0;
   for (int j = 0; j < all; ++j) {
     const double other = __shfl_sync(ALL, c, j);
@@ -203,14 +219,40 @@ __device__ __noinline__ int reorder_wide(const RouteParams& p, const float (&x)[
   return out;
 }
 
+// fp32 sums of score and bias, as keys.  (Explicit roundings: the same bits
+// wherever it is inlined.)
+template <int NV>
+LAGA_DEVINL void keys_of(const RouteParams& p, const float (&x)[NV], const float (&bias)[NV],
+                         float top, float inv, unsigned (&key)[NV]) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float s;
+    if (p.sigmoid) {
+      // within (1.25 |x| + 9) 2^-24 of itself; the weight is computed again
+      float e;
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(x[i], -1.44269504f)));
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(__fadd_rn(1.f, e)));
+    } else {
+      s = __fmul_rn(expf(x[i] - top), inv);
+    }
+    const float c = __fadd_rn(s, bias[i]);
+    key[i] = x[i] > minus_inf<float>() && c > minus_inf<float>() ? key_of(c) : KEY_OFF;
+  }
+}
+
 // The choice of groups where the last one in and the first one out are close:
 // the two best of every group about there, settled in 64 bits, a group a lane.
 // 0 where it is not certain which two these are.
 template <int NV, typename T>
-__device__ __noinline__ unsigned regroup_wide(const RouteParams& p, const unsigned (&key)[NV],
-                                              const float (&x)[NV], float top, const T* l,
-                                              float mine, float in, float out, float tol,
-                                              float lost, int lane) {
+__device__ __noinline__ unsigned regroup_wide(const RouteParams& p, const T* l, float top,
+                                              float inv, float mine, float in, float out,
+                                              float tol, float lost, int lane) {
+  float x[NV], bias[NV];
+  unsigned key[NV];
+  logits_of<NV>(p, l, lane, x);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) bias[i] = bias_of(p, 32 * i + lane);
+  keys_of<NV>(p, x, bias, top, inv, key);
   const bool in_range = lane < p.groups;
   const unsigned above = __ballot_sync(ALL, in_range && mine > in + tol);
   const bool about = in_range && mine <= in + tol && mine >= out - tol;
@@ -279,6 +321,83 @@ LAGA_DEVINL float score_of(const RouteParams& p, const T* l, const float (&x)[NV
   return p.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - top) / z;
 }
 
+// The choice among the keys of this lane's experts `index` (ascending), in fp32:
+// lane j's expert.  `score`: its score.  False: the order is not certain.
+template <int NV, int M, typename T>
+LAGA_DEVINL bool pick(const RouteParams& p, const T* l, unsigned (&key)[M], const int (&index)[M],
+                      float top, float inv, float lost, int lane, int& expert, float& score) {
+  const float ninf = minus_inf<float>();
+  // rounds: lane j keeps the j-th best
+  float value = ninf;
+  expert = -1;
+  int found = 0;
+  auto round = [&](float least) {
+    unsigned best = key[0];
+#pragma unroll
+    for (int i = 1; i < M; ++i) best = max(best, key[i]);
+    const unsigned first = __reduce_max_sync(ALL, best);
+    if (first <= KEY_OFF || !(value_of(first) >= least)) return false;
+    unsigned e = 0x7fffffffu;
+#pragma unroll
+    for (int i = M - 1; i >= 0; --i)
+      if (key[i] == first) e = index[i];
+    e = __reduce_min_sync(ALL, e);
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+      if (index[i] == (int)e) key[i] = KEY_OFF;
+    if (lane == found) {
+      expert = (int)e;
+      value = value_of(first);
+    }
+    ++found;
+    return true;
+  };
+  while (found < min(p.top_k + 1, 32) && round(ninf)) {
+  }
+  // the chosen ones' scores, and the distance of each from the next (of the last
+  // one from the best that was not chosen)
+  float mine = 0.f, b = 0.f;
+  auto look = [&] {
+    score = 0.f;
+    if (expert >= 0) {
+      bool nan;
+      mine = logit_of(p, l, expert, 0.f, nan);
+      b = bias_of(p, expert);
+      score = p.sigmoid ? 1.f / (1.f + expf(-mine)) : expf(mine - top) * inv;
+    }
+  };
+  look();
+  const unsigned next = min(lane + 1, 31);
+  const float v1 = __shfl_sync(ALL, value, next), l1 = __shfl_sync(ALL, mine, next);
+  const float b1 = __shfl_sync(ALL, b, next);
+  const int e1 = __shfl_sync(ALL, expert, next);
+  // (equal ones at the end may have others next to them that were not looked at)
+  const bool equal = mine == l1 && b == b1 && lane + 1 < p.top_k;
+  const bool close = lane < min(p.top_k, 31) && expert >= 0 && e1 >= 0 && !equal &&
+                     !(value - v1 > 2.f * lost + (fabsf(value) + fabsf(v1)) * 0x1p-24f);
+  if (__any_sync(ALL, close) || p.top_k == 32) {
+    // everything that may belong to the best top_k, whose last one may have lost
+    // as much as what is below it
+    const int last = min(p.top_k, found) - 1;
+    if (last >= 0) {
+      const float least = __shfl_sync(ALL, value - 2.5f * lost - fabsf(value) * 0x1p-22f, last);
+      while (found < 32 && round(least)) {
+      }
+      // a full warp may have left some out; infinities have no distance
+      if (found == 32 || !(fabsf(least) <= 3.402823466e38f)) return false;
+      look();
+      expert = reorder_wide<NV, T>(p, l, top, expert, found, lane);
+      if (lane >= p.top_k) expert = -1;
+      look();
+    }
+  }
+  if (lane >= p.top_k) {
+    expert = -1;
+    score = 0.f;
+  }
+  return true;
+}
+
 // The choice in fp32: lane j's expert.  `score`: its score.  `reach`: no sum of
 // a score and a finite bias is larger.  False: the order is not certain.
 template <int NV, typename T>
@@ -300,20 +419,7 @@ LAGA_DEVINL bool choose(const RouteParams& p, const T* l, const float (&x)[NV],
     z = warp_sum(z);
     inv = z > 0.f ? 1.f / z : 0.f;
   }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float s;
-    if (p.sigmoid) {
-      // within (1.25 |x| + 9) 2^-24 of itself; the weight is computed again
-      float e;
-      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x[i] * -1.44269504f));
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
-    } else {
-      s = expf(x[i] - top) * inv;
-    }
-    const float c = s + bias[i];
-    key[i] = x[i] > ninf && c > ninf ? key_of(c) : KEY_OFF;
-  }
+  keys_of<NV>(p, x, bias, top, inv, key);
   // What fp32 may have lost of a score.  Of a sigmoid s: (1 - s) (1.25 |x| + 4)
   // units of its last place (the exponential's error) and three roundings, no
   // more than 6 units of 2^-24 of one for any x.  Of a softmax: the rounded
@@ -378,82 +484,37 @@ LAGA_DEVINL bool choose(const RouteParams& p, const T* l, const float (&x)[NV],
     if (out > ninf && !(in - out > tol)) {
       // (an infinite sum has no distance)
       keep = fabsf(in) <= 3.402823466e38f
-                 ? regroup_wide<NV, T>(p, key, x, top, l, mine, in, out, tol, lost, lane) : 0u;
+                 ? regroup_wide<NV, T>(p, l, top, inv, mine, in, out, tol, lost, lane) : 0u;
       if (keep == 0u) return false;
+    }
+    if constexpr (NV == 8) {
+      // groups of a register, four of them at most: what is left in four, which
+      // the rounds go over (16384 x 256, 4 of 8 groups: 47 us -> 41 us)
+      if (p.group_size == 32 && p.top_groups <= 4) {
+        unsigned live[4];
+        int first[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = keep ? __ffs(keep) - 1 : 0;   // the same for all lanes
+          const bool b0 = i & 1, b1 = i & 2, b2 = i & 4;
+          const unsigned k01 = b0 ? key[1] : key[0], k23 = b0 ? key[3] : key[2];
+          const unsigned k45 = b0 ? key[5] : key[4], k67 = b0 ? key[7] : key[6];
+          const unsigned low = b1 ? k23 : k01, high = b1 ? k67 : k45;
+          live[j] = keep ? b2 ? high : low : KEY_OFF;
+          first[j] = 32 * i + lane;
+          keep &= keep - 1;
+        }
+        return pick<NV, 4, T>(p, l, live, first, top, inv, lost, lane, expert, score);
+      }
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (!(keep >> group[i] & 1u)) key[i] = KEY_OFF;
   }
-  // rounds: lane j keeps the j-th best
-  float value = ninf;
-  expert = -1;
-  int found = 0;
-  auto round = [&](float least) {
-    unsigned best = key[0];
+  int index[NV];
 #pragma unroll
-    for (int i = 1; i < NV; ++i) best = max(best, key[i]);
-    const unsigned first = __reduce_max_sync(ALL, best);
-    if (first <= KEY_OFF || !(value_of(first) >= least)) return false;
-    unsigned e = 0x7fffffffu;
-#pragma unroll
-    for (int i = NV - 1; i >= 0; --i)
-      if (key[i] == first) e = 32 * i + lane;
-    e = __reduce_min_sync(ALL, e);
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (32 * i + lane == (int)e) key[i] = KEY_OFF;
-    if (lane == found) {
-      expert = (int)e;
-      value = value_of(first);
-    }
-    ++found;
-    return true;
-  };
-  while (found < min(p.top_k + 1, 32) && round(ninf)) {
-  }
-  // the chosen ones' scores, and the distance of each from the next (of the last
-  // one from the best that was not chosen)
-  float mine = 0.f, b = 0.f;
-  auto look = [&] {
-    score = 0.f;
-    if (expert >= 0) {
-      bool nan;
-      mine = logit_of(p, l, expert, 0.f, nan);
-      b = bias_of(p, expert);
-      score = p.sigmoid ? 1.f / (1.f + expf(-mine)) : expf(mine - top) * inv;
-    }
-  };
-  look();
-  const unsigned next = min(lane + 1, 31);
-  const float v1 = __shfl_sync(ALL, value, next), l1 = __shfl_sync(ALL, mine, next);
-  const float b1 = __shfl_sync(ALL, b, next);
-  const int e1 = __shfl_sync(ALL, expert, next);
-  // (equal ones at the end may have others next to them that were not looked at)
-  const bool equal = mine == l1 && b == b1 && lane + 1 < p.top_k;
-  const bool close = lane < min(p.top_k, 31) && expert >= 0 && e1 >= 0 && !equal &&
-                     !(value - v1 > 2.f * lost + (fabsf(value) + fabsf(v1)) * 0x1p-24f);
-  if (__any_sync(ALL, close) || p.top_k == 32) {
-    // everything that may belong to the best top_k, whose last one may have lost
-    // as much as what is below it
-    const int last = min(p.top_k, found) - 1;
-    if (last >= 0) {
-      const float least = __shfl_sync(ALL, value - 2.5f * lost - fabsf(value) * 0x1p-22f, last);
-      while (found < 32 && round(least)) {
-      }
-      // a full warp may have left some out; infinities have no distance
-      if (found == 32 || !(fabsf(least) <= 3.402823466e38f)) return false;
-      look();
-      expert = reorder_wide<NV>(p, x, top, mine, b, expert, found, lane);
-      if (lane >= p.top_k) expert = -1;
-      look();
-    }
-  }
-  if (lane >= p.top_k) {
-    expert = -1;
-    score = 0.f;
-  }
-  return true;
+  for (int i = 0; i < NV; ++i) index[i] = 32 * i + lane;
+  return pick<NV, NV, T>(p, l, key, index, top, inv, lost, lane, expert, score);
 }
 
 // Numbers the pairs of this block's chunk.  smem: [bases | counts | warps x counts]
