@@ -14,10 +14,36 @@ namespace {
 // of row r sits at w ^ (r / 4), so that reading rows 4 l .. 4 l + 3 of one word by
 // lane l, like writing, meets every bank once.  Bound by HBM from some 10^7 values
 // on (7168 x 1536 bf16: 10 us within a graph).
+// The values stay as they were loaded until they are coded, so that four blocks of
+// bf16 weights fit an SM (32 x 7168 x 4096: 881 us as floats, three blocks).
 constexpr int WB = CK_GROUP;
 
+template <typename T>
+struct Eight;   // eight neighbouring values
+template <>
+struct Eight<float> {
+  float2 v[4];
+  LAGA_DEVINL float2 at(int j) const { return v[j]; }
+  LAGA_DEVINL void load(const float* p) { load_vec<8>(p, v); }
+  LAGA_DEVINL void set(int j, float a, float b) { v[j] = make_float2(a, b); }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  uint32_t v[4];
+  LAGA_DEVINL float2 at(int j) const {
+    return make_float2(__uint_as_float(v[j] << 16), __uint_as_float(v[j] & 0xffff0000u));
+  }
+  LAGA_DEVINL void load(const __nv_bfloat16* p) {
+    const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p));
+    v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+  }
+  LAGA_DEVINL void set(int j, float a, float b) {   // (bf16 values: nothing is rounded)
+    v[j] = __float_as_uint(a) >> 16 | (__float_as_uint(b) & 0xffff0000u);
+  }
+};
+
 template <typename T, int V>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3)
     weight_pack_kernel(const T* __restrict__ w, uint8_t* __restrict__ fwd,
                        uint8_t* __restrict__ bwd, int K, int N) {
   __shared__ uint32_t tile[WB][WB / 4];
@@ -26,28 +52,32 @@ __global__ void __launch_bounds__(256)
   const int tid = threadIdx.x, lane = tid & 31;
   const T* src = w + (long long)e * K * N;
   const int c = (tid & 15) * 8, r0 = tid >> 4;
-  float2 v[8][4];
+  Eight<T> v[8];
   float m = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int k = kb * WB + r0 + 16 * i, n = nb * WB + c;
     const T* p = src + (long long)k * N + n;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[i][j] = make_float2(0.f, 0.f);
+    for (int j = 0; j < 4; ++j) v[i].set(j, 0.f, 0.f);
     if (k < K) {
       if constexpr (V == 8) {
-        if (n < N) load_vec<8>(p, v[i]);
+        if (n < N) v[i].load(p);
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (n + 2 * j < N) v[i][j].x = to_f32(p[2 * j]);
-          if (n + 2 * j + 1 < N) v[i][j].y = to_f32(p[2 * j + 1]);
-        }
+        for (int j = 0; j < 4; ++j)
+          v[i].set(j, n + 2 * j < N ? to_f32(p[2 * j]) : 0.f,
+                   n + 2 * j + 1 < N ? to_f32(p[2 * j + 1]) : 0.f);
       }
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m = ck_max(ck_max(m, v[i][j].x), v[i][j].y);
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = v[i].at(j);
+      m = ck_max(ck_max(m, f.x), f.y);
+    }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = ck_max(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) part[tid >> 5] = m;
@@ -62,7 +92,7 @@ __global__ void __launch_bounds__(256)
     const int r = r0 + 16 * i, x = r >> 2;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t q = ck_code2(v[i][2 * h], inv) | ck_code2(v[i][2 * h + 1], inv) << 16;
+      const uint32_t q = ck_code2(v[i].at(2 * h), inv) | ck_code2(v[i].at(2 * h + 1), inv) << 16;
       tile[r][(c / 4 + h) ^ x] = s == CK_NAN ? 0u : q;
     }
   }

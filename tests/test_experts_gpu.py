@@ -333,7 +333,8 @@ def test_pack_weight_borders():
 @pytest.mark.parametrize("rows,K,N", [(1, 1, 1), (1, 7168, 256), (3, 129, 130), (16, 512, 1001),
                                       (17, 128, 64), (64, 2048, 96), (65, 300, 255),
                                       (127, 640, 128), (129, 1001, 257), (256, 896, 512),
-                                      (257, 4096, 513), (300, 130, 7), (1000, 384, 1536)])
+                                      (257, 4096, 513), (300, 130, 7), (1000, 384, 1536), (130, 300, 200),
+                                      (224, 2100, 1000), (225, 3000, 36), (449, 140, 8)])
 def test_linear(rows, K, N, io):
     laga = _laga()
     g = _gen(rows, K, N)

@@ -357,7 +357,8 @@ class Banded:
 
 
 @pytest.mark.parametrize("T,d,n,E,k,align", [(37, 129, 257, 5, 2, 1), (1, 1001, 64, 8, 3, 128),
-                                             (300, 256, 384, 3, 2, 128), (9, 7168, 33, 2, 1, 1)])
+                                             (300, 256, 384, 3, 2, 128), (9, 7168, 33, 2, 1, 1),
+                                             (260, 300, 200, 2, 2, 128)])
 def test_nothing_is_written_outside(T, d, n, E, k, align):
     laga = _laga()
     L = laga._lib
