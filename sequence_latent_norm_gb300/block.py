@@ -33,7 +33,7 @@ gradients, in fp32, straight from the codes.
 8-bit products (``linear8.py``): h, the attention's output and the gradients
 that meet a weight are packed on the way, the weights in every call.  The weight
 gradients come from the codes that were multiplied (h's from ``kept`` where it is
-given), in fp32.
+given), in fp32, with the latent's gradient rounded to the I/O dtype first.
 
 ``LagaResidualStack`` puts blocks on a residual stream, each with its norm in
 front, and its norm, gate and residual scale behind (``residual.py``); between
@@ -123,7 +123,7 @@ class LagaAttentionBlock:
         h_flat = h.reshape(B * S_r, d_model)
         fp8 = self.projections == "fp8"
         if fp8:
-            w_q, w_kva, w_o = (pack_weight8(w) for w in (w_q, w_kva, w_o))
+            w_q, w_kva, w_o = (pack_weight8(w.contiguous()) for w in (w_q, w_kva, w_o))
             h8 = pack8(h_flat.contiguous())
             q, c = (linear8(h8, w, dtype=h.dtype) for w in (w_q, w_kva))
         else:
@@ -202,11 +202,10 @@ class LagaResidualStack:
         x_{l+1} = x_l + alpha s N_post(y_l) gamma_post
 
     ``blocks``: one LagaAttentionBlock or RoutedExperts a layer (the latter on one
-    rank only).  norm_pre, norm_post ("none":
-    a plain gated residual add) and gate as for ResidualNorm.  ``ckpt`` holds
-    the normalised x and y of every layer as 8-bit checkpoints; the one of x
-    also serves the layer's dW_q and dW_kv_a, so neither x nor h is held in
-    the I/O type.  Gate logits are given as tensors and their gradients given
+    rank only).  norm_pre, norm_post ("none": a plain gated residual add) and
+    gate as for ResidualNorm.  ``ckpt`` holds the normalised x and y of every
+    layer as 8-bit checkpoints; the one of x also serves the layer's dW_q and
+    dW_kv_a, so neither x nor h is held in the I/O type.  Gate logits are given as tensors and their gradients given
     back; a gate that is computed from x or h on the way needs ResidualNorm in
     the caller's own loop."""
 
@@ -229,9 +228,10 @@ class LagaResidualStack:
     def forward(self, x, layers, cos, sin):
         """``layers``: per block a dict of w_q, w_kva, gamma, w_kvb, w_o (see
         LagaAttentionBlock.forward), or w_router, w_in, w_out and bias (see
-        RoutedExperts.forward; no bias: None or left out), and gamma_pre [d_model] and alpha [1] fp32,
-        and, where they apply, gamma_post [d_model] fp32 and gate logits [B,
-        S_r, d_model or 1].  Returns x behind the last block."""
+        RoutedExperts.forward; no bias: None or left out), and gamma_pre
+        [d_model] and alpha [1] fp32, and, where they apply, gamma_post
+        [d_model] fp32 and gate logits [B, S_r, d_model or 1].  Returns x behind
+        the last block."""
         if len(layers) != len(self.blocks):
             raise ValueError(f"{len(layers)} layers for {len(self.blocks)} blocks")
         r = self.first.forward(x, gamma_pre=layers[0]["gamma_pre"])

@@ -165,7 +165,8 @@ class RoutedExperts:
         elif (kept.rows, kept.d) != (rows, d):
             raise ValueError(f"kept: a checkpoint of {kept.rows} rows of {kept.d}, expected "
                              f"{rows} of {d}")
-        w_in, w_out = (w if isinstance(w, Weight8) else pack_weight8(w) for w in (w_in, w_out))
+        w_in, w_out = (w if isinstance(w, Weight8) else pack_weight8(w.contiguous())
+                       for w in (w_in, w_out))
         h_flat = h.reshape(rows, d).contiguous()
         logits = h_flat.float() @ w_router
         routes = self.router.forward(logits, bias)

@@ -87,6 +87,33 @@ def test_block_in_fp32_and_with_packed_weights():
         assert _rel(g[n], v) <= REL_FRO, n
 
 
+def test_transposed_weights():
+    """Weights that are views of another order give the same bits."""
+    from sequence_latent_norm_gb300.block import LagaAttentionBlock
+    laga = _laga()
+
+    def turned(w):
+        return w.transpose(-1, -2).contiguous().transpose(-1, -2)
+
+    x = _dev(_inputs(40, 256, 128, 4))
+    block = laga.RoutedExperts(4, 2, device=DEV)
+    y, g = _run(block, x)
+    y2, g2 = _run(block, dict(x, w_in=turned(x["w_in"]), w_out=turned(x["w_out"])))
+    assert torch.equal(y, y2) and all(torch.equal(g[n], g2[n]) for n in g)
+    wl = config(1, S=130, H=2, n_h_total=2, seed=6)
+    b = {n: v.to(DEV) for n, v in make_block_inputs(wl, 320).items()}
+    for n in ("h", "w_q", "w_kva", "w_kvb", "w_o", "dy"):
+        b[n] = b[n].to(torch.bfloat16)
+    blk = LagaAttentionBlock.single(wl.H, wl.S, device=torch.device(DEV), projections="fp8")
+    names = ("h", "w_q", "w_kva", "gamma", "w_kvb", "w_o", "cos", "sin")
+    y = blk.forward(*(b[n] for n in names))
+    t = dict(b, **{n: turned(b[n]) for n in ("w_q", "w_kva", "w_o")})
+    assert not t["w_q"].is_contiguous()
+    y2 = blk.forward(*(t[n] for n in names))
+    laga._lib.sync_check()
+    assert torch.equal(y, y2)
+
+
 def test_kept_checkpoint_serves_the_weight_gradients():
     laga = _laga()
     x = _dev(_inputs(90, 256, 64, 4))
