@@ -523,7 +523,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const long long ld = piece ? BN : p.n;
       const int lim = piece ? HALF : p.n - n0;            // columns that exist
       const int rows = piece ? CK_GROUP : p.d - m0;       // channels that exist
-      if (!polls) continue;
+      // One answer for the warp: its lanes turn and store each other's values.
+      const bool good = __all_sync(0xffffffffu, polls != 0);
+      if (!good) continue;
       if (p.wide && (piece || p.n % 8 == 0)) {
         // 32 columns at a time: four neighbouring lanes turn 4 rows x 32 columns
         // into 8 columns of all four rows each, so that a store of 32 bytes a lane
