@@ -442,11 +442,14 @@ size_t laga_route_workspace_bytes(const laga_route_dims* dims);
  *   weight = scale s, or scale s / (sum of the chosen s + 1e-20).
  * The order is that of c in 64 bits.  An expert whose logit or bias is -inf is
  * off; a choice that finds no expert on has expert -1 and weight 0.  A NaN
- * (or +inf under a softmax) counts as off and makes the token's weights NaN.
+ * (or +inf under a softmax) counts as off and makes all of the token's weights
+ * NaN, those of choices without an expert too; these have row -2, which
+ * laga_combine_fwd gives a NaN for: a token without any expert on is not lost.
  *   logits [tokens, experts]; bias [experts] fp32 or NULL
  *   expert [tokens, top_k] (output)   index among all experts, best first
  *   weight [tokens, top_k] fp32 (output)
- *   row    [tokens, top_k] (output)   the pair's row, -1: none on this rank
+ *   row    [tokens, top_k] (output)   the pair's row, -1: none on this rank, -2: no
+ *     expert in a token with a NaN
  *   pair   [laga_route_rows] (output) the row's pair, -1: none
  *   start  [local + 1] (output) */
 laga_status laga_route_fwd(const laga_route_dims* dims, const void* logits, const float* bias,
@@ -454,7 +457,9 @@ laga_status laga_route_fwd(const laga_route_dims* dims, const void* logits, cons
                            size_t ws_bytes, void* stream);
 
 /* Gradient of the logits for dweight [tokens, top_k] fp32, at fixed choice.
- * Choices of -1 take no part; an expert that `expert` holds twice counts twice. */
+ * Choices of -1 take no part; an expert that `expert` holds twice counts twice.
+ * A NaN logit under a softmax (or +inf) makes the token's gradients NaN; with
+ * sigmoids it makes its own one, in tokens that have a choice of -1. */
 laga_status laga_route_bwd(const laga_route_dims* dims, const void* logits, const int* expert,
                            const float* dweight, void* dlogits, void* stream);
 
@@ -493,7 +498,7 @@ laga_status laga_spread8(int rows, int tokens, int top_k, int d, const void* ck,
                          const int* end, void* out, void* stream);
 
 /* out[t] = sum_j weight[t, j] y[row[t, j]], in fp32, j ascending; weight NULL:
- * 1; a row of -1 adds nothing.  y [rows, d], out [tokens, d] (output). */
+ * 1; a row of -1 adds nothing, one of -2 makes out[t] NaN.  y [rows, d], out [tokens, d] (output). */
 laga_status laga_combine_fwd(int tokens, int top_k, int rows, int d, laga_dtype dtype,
                              const void* y, const float* weight, const int* row, void* out,
                              void* stream);

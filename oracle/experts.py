@@ -20,7 +20,8 @@ def scores(logits, score):
     m = logits.max(axis=1, keepdims=True)
     p = np.exp(logits - np.where(np.isfinite(m), m, 0.0))
     z = p.sum(axis=1, keepdims=True)
-    return np.divide(p, z, out=np.zeros_like(p), where=z > 0)
+    with np.errstate(invalid="ignore"):
+        return np.divide(p, z, out=np.zeros_like(p), where=z != 0)
 
 
 def best(v, n):
@@ -59,14 +60,17 @@ def choose(logits, bias, *, top_k, groups=1, top_groups=1, score="sigmoid", reno
         w = s[t, e]
         weight[t, :len(e)] = scale * (w / (w.sum() + TINY) if renormalise else w)
         if nan[t].any():
-            weight[t, :len(e)] = np.nan
+            weight[t] = np.nan
     return expert, weight
 
 
-def order(expert, *, first=0, local, align, rows):
-    """(row, pair, start) of the choices: pairs of the local experts, by expert."""
+def order(expert, *, first=0, local, align, rows, weight=None):
+    """(row, pair, start) of the choices: pairs of the local experts, by expert.  A
+    choice without an expert whose weight is a NaN has row -2."""
     T, k = expert.shape
     row, pair = np.full(T * k, -1, np.int32), np.full(rows, -1, np.int32)
+    if weight is not None:
+        row[((expert < 0) & np.isnan(weight)).reshape(-1)] = -2
     start = [0]
     flat = expert.reshape(-1)
     for e in range(first, first + local):
@@ -166,6 +170,8 @@ def combine(y, weight, row):
             if r >= 0:
                 out[t] += weight[t, j] * y[r]
                 mag[t] += np.abs(weight[t, j] * y[r])
+            elif r == -2:
+                out[t] = np.nan
     return out, mag
 
 

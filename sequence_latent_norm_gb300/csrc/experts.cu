@@ -40,7 +40,8 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// out_t = sum_j w_tj y[row_tj]: a thread V channels of a token.
+// out_t = sum_j w_tj y[row_tj]: a thread V channels of a token.  A choice that a
+// NaN left without an expert makes it a NaN, also under weights of 1.
 template <typename T, int V>
 __global__ void __launch_bounds__(256)
     combine_kernel(const T* __restrict__ y, const float* __restrict__ weight,
@@ -56,7 +57,13 @@ __global__ void __launch_bounds__(256)
     for (int k = 0; k < (V + 1) / 2; ++k) acc[k] = make_float2(0.f, 0.f);
     for (int j = 0; j < top_k; ++j) {
       const int r = row[t * top_k + j];
-      if (r < 0 || r >= rows) continue;
+      if (r < 0 || r >= rows) {
+        if (r == ROUTE_ROW_NAN)
+#pragma unroll
+          for (int k = 0; k < (V + 1) / 2; ++k)
+            acc[k].x = acc[k].y = __int_as_float(0x7fc00000);
+        continue;
+      }
       const float w = weight ? weight[t * top_k + j] : 1.f;
       float2 f[(V + 1) / 2];
       load_vec<V>(y + (long long)r * d + c, f);

@@ -41,6 +41,7 @@ cudaError_t launch_ckpt_dw(int rows, int d, int n, bool fp32, const void* ck, co
 
 // ---- routing and experts
 constexpr int ROUTE_MAX_EXPERTS = 1024, ROUTE_MAX_K = 32;
+constexpr int ROUTE_ROW_NAN = -2;   // `row` of a NaN token's choice that found no expert
 
 laga_status route_check(const laga_route_dims* dims);
 long long route_rows(const laga_route_dims& d);

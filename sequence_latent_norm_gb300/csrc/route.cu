@@ -641,7 +641,11 @@ LAGA_DEVINL void place(const RouteParams& p, unsigned* smem) {
     if (on && lane == __ffs(same) - 1) h[e] += __popc(same);
     __syncwarp();
     if (on) p.pair[at] = (int)(off + i + lane);
-    if (in) p.row[off + i + lane] = on ? (int)at : -1;
+    if (in) {
+      const bool none = e + p.first < 0;   // no expert was on
+      p.row[off + i + lane] =
+          on ? (int)at : none && isnan(p.weight[off + i + lane]) ? ROUTE_ROW_NAN : -1;
+    }
   }
 }
 
@@ -698,7 +702,7 @@ __global__ void __launch_bounds__(route_threads<NV>())
     if (nan) w = __int_as_float(0x7fc00000);
     if (lane < p.top_k) {
       p.expert[(long long)t * p.top_k + lane] = expert;
-      p.weight[(long long)t * p.top_k + lane] = expert >= 0 ? w : 0.f;
+      p.weight[(long long)t * p.top_k + lane] = expert >= 0 || nan ? w : 0.f;
       const int e = expert - p.first;
       if (expert >= 0 && e >= 0 && e < p.local) atomicAdd(&smem[e], 1u);
     }
@@ -719,7 +723,10 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const RouteParams p) 
 
 // Backward, one warp per token.  With weights w_j = scale s_j / D, D = sum s + tiny:
 // ds_j = scale (dw_j - (sum_i dw_i s_i) / D) / D (scale dw_j without the
-// division), then the scores' own slope.
+// division), then the scores' own slope.  A NaN logit's slope is a NaN, which a
+// softmax hands to the whole token.  With sigmoids the logits that were not chosen
+// are read only where a choice found no expert: that is every token without any,
+// and reading all of them would double the kernel's bytes.
 template <typename T>
 __global__ void __launch_bounds__(256)
     route_bwd_kernel(const T* __restrict__ logits, const int* __restrict__ expert,
@@ -730,20 +737,25 @@ __global__ void __launch_bounds__(256)
   float* g = rows + warp * E;
   for (long long t = blockIdx.x * 8LL + warp; t < p.tokens; t += gridDim.x * 8LL) {
     const T* l = logits + t * E;
-    for (int e = lane; e < E; e += 32) g[e] = 0.f;
+    const int e = lane < p.top_k ? expert[t * p.top_k + lane] : -1;
+    const bool on = e >= 0 && e < E;
+    if (p.sigmoid && __any_sync(ALL, lane < p.top_k && !on)) {
+      for (int i = lane; i < E; i += 32)
+        g[i] = isnan(to_f32(l[i])) ? __int_as_float(0x7fc00000) : 0.f;
+    } else {
+      for (int i = lane; i < E; i += 32) g[i] = 0.f;
+    }
     float top = 0.f, inv = 0.f;
     if (!p.sigmoid) {
       top = minus_inf<float>();
-      for (int e = lane; e < E; e += 32) top = fmaxf(top, to_f32(l[e]));
+      for (int i = lane; i < E; i += 32) top = fmaxf(top, to_f32(l[i]));
       top = warp_max(top);
       if (!(top > minus_inf<float>())) top = 0.f;
       float z = 0.f;
-      for (int e = lane; e < E; e += 32) z += expf(to_f32(l[e]) - top);
+      for (int i = lane; i < E; i += 32) z += expf(to_f32(l[i]) - top);
       z = warp_sum(z);
-      inv = z > 0.f ? 1.f / z : 0.f;
+      inv = z == 0.f ? 0.f : 1.f / z;
     }
-    const int e = lane < p.top_k ? expert[t * p.top_k + lane] : -1;
-    const bool on = e >= 0 && e < E;
     float s = 0.f, slope = 1.f, dw = 0.f;
     if (on) {
       const float x = to_f32(l[e]);

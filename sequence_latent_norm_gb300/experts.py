@@ -52,7 +52,8 @@ def _weight(routes, weighted, device):
 
 def combine(y: torch.Tensor, routes, *, weighted: bool = True, stream=None) -> torch.Tensor:
     """sum_j weight_tj y[row_tj] [tokens, d] of the experts' rows y [rows, d];
-    ``weighted=False`` takes weights of 1 (the gradient of spread8)."""
+    ``weighted=False`` takes weights of 1 (the gradient of spread8).  A token
+    that a NaN left without an expert (a row of -2) comes out as NaN."""
     p, rows, d = _matrix(y, "y")
     if rows != routes.rows:
         raise ValueError(f"y has {rows} rows, the routes {routes.rows}")

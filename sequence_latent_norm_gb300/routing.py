@@ -25,8 +25,9 @@ class Routes(NamedTuple):
     """A batch's choices and the rows that experts take them in.
 
     expert [T, k] int32 (best first; -1: no expert was on); weight [T, k]
-    fp32 (0 there); row [T, k] int32: the pair's row, -1 where it has none (on
-    this rank); pair [R] int32: the row's pair t k + j, -1 where it has none;
+    fp32 (0 there; NaN throughout a token that holds a NaN); row [T, k] int32:
+    the pair's row, -1 where it has none (on this rank), -2 where a token with
+    a NaN has no expert (combine makes that token NaN); pair [R] int32: the row's pair t k + j, -1 where it has none;
     start [E + 1] int32: expert e (of this rank's) takes the rows start[e] ..
     start[e + 1] - 1, of which the ones behind its pairs belong to none.
     start[e] are multiples of ``align``.  R rows are the most that a batch can
@@ -168,7 +169,8 @@ class Router:
 
     def backward(self, logits, routes: Routes, dweight, *, stream=None):
         """Gradient of the logits (their shape and dtype) for dweight [T, k]
-        fp32, with the choice held fixed; the bias has none."""
+        fp32, with the choice held fixed; the bias has none.  NaN for a token
+        whose logits all are."""
         p, T = self._logits(logits)
         pe = need(routes.expert, "routes.expert", torch.int32, self.device, (T, self.top_k))
         pw = need(dweight, "dweight", torch.float32, self.device, (T, self.top_k))
