@@ -186,11 +186,13 @@ __global__ void __launch_bounds__(256)
 // sigmoid(g) and 1 - sigmoid(g) = e^-g sigmoid(g), each within 6 units of its
 // last place: the exponent's product with log2 e is carried in two parts, since
 // what it loses moves codes across their borders.  Below -87.3 the sigmoid
-// would be subnormal: both are zero.
+// would be subnormal: both are zero.  Above 104 e^-g is zero, and g stops there:
+// from 2.4e38 on the product would be infinite and its second part no number.
+constexpr float C = -1.44269502f, C_LO = -1.92596303e-8f, LN2 = 0.693147182f;
 LAGA_DEVINL float2 sigmoid2(float g) {
-  constexpr float C = -1.44269502f, C_LO = -1.92596303e-8f, LN2 = 0.693147182f;
   float e, s;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(g) : "f"(g), "f"(-88.5f));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(g) : "f"(g), "f"(104.f));
   const float t = g * C;
   const float lo = fmaf(g, C_LO, fmaf(g, C, -t));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
@@ -198,7 +200,18 @@ LAGA_DEVINL float2 sigmoid2(float g) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
   return make_float2(s, e * s);
 }
-LAGA_DEVINL float sigmoid(float g) { return sigmoid2(g).x; }
+// sigmoid(g) alone, the same bits, for which e^-g may be infinite: there the
+// second part, which has no use, is left out.  (A test instead of two bounds: 16384
+// x 2048 bf16 takes 33.8 us, 35.6 us with sigmoid2.)
+LAGA_DEVINL float sigmoid(float g) {
+  float e, s;
+  const float t = g * C;
+  const float lo = fmaf(g, C_LO, fmaf(g, C, -t));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  if (fabsf(g) < 88.5f) e = fmaf(e, lo * LN2, e);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return s;
+}
 
 // Codes of a group's values, `lanes` neighbouring lanes of V each.
 template <int V>
