@@ -522,7 +522,7 @@ LAGA_DEVINL bool choose(const RouteParams& p, const T* l, const float (&x)[NV],
 LAGA_DEVINL void place(const RouteParams& p, unsigned* smem) {
   const int EL = p.local, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int warps = blockDim.x >> 5;
-  const int t0 = blockIdx.x * p.chunk, t1 = min(p.tokens, t0 + p.chunk);
+  const int t0 = blockIdx.x * p.chunk, t1 = t0 + min(p.chunk, p.tokens - t0);
   const int n = (t1 - t0) * p.top_k;
   const int share = max(((n + warps - 1) / warps + 31) / 32 * 32, 64);
   const int busy = min(warps, (n + share - 1) / share);
@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(route_threads<NV>())
     route_kernel(const T* __restrict__ logits, const RouteParams p) {
   extern __shared__ unsigned smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  const int t0 = blockIdx.x * p.chunk, t1 = min(p.tokens, t0 + p.chunk);
+  const int t0 = blockIdx.x * p.chunk, t1 = t0 + min(p.chunk, p.tokens - t0);
   for (int e = threadIdx.x; e < p.local; e += blockDim.x) smem[e] = 0;
   __syncthreads();
   float bias[NV];
@@ -790,7 +790,7 @@ __global__ void __launch_bounds__(256)
 }
 
 int route_chunk(int tokens, int warps) {
-  return std::max(warps, (tokens + 151) / 152);   // one block per SM, every warp a token at least
+  return std::max(warps, (tokens - 1) / 152 + 1);   // one block per SM, every warp a token at least
 }
 int route_warps(int experts) { return experts <= 256 ? 32 : experts <= 512 ? 16 : 8; }
 
@@ -803,7 +803,7 @@ RouteParams make_params(const laga_route_dims& d) {
   p.scale = d.scale;
   p.first = d.first; p.local = d.local; p.align = d.align;
   p.chunk = route_chunk(d.tokens, route_warps(d.experts));
-  p.chunks = (d.tokens + p.chunk - 1) / p.chunk;
+  p.chunks = (d.tokens - 1) / p.chunk + 1;     // (no sum of tokens here leaves 31 bits)
   p.cap = (int)route_rows(d);
   p.stride = (d.local + 3) / 4 * 4;
   return p;
