@@ -144,11 +144,6 @@ class LagaAttentionBlock:
         y = linear8(out_flat, w_o, dtype=h.dtype) if fp8 else out_flat @ w_o
         return y.reshape(B, S_r, d_model)
 
-    def _layer(self, h, w, cos, sin, **kept):
-        """forward with a layer's dict of weights."""
-        return self.forward(h, w["w_q"], w["w_kva"], w["gamma"], w["w_kvb"], w["w_o"], cos, sin,
-                            **kept)
-
     def _all_reduce(self, t, what):
         if not self.distributed:
             return t
@@ -195,6 +190,15 @@ class LagaAttentionBlock:
                     dw_kvb=dw_kvb, dgamma=dgamma)
 
 
+def _block_forward(block, h, w, cos, sin, **kept):
+    """A block's forward with its layer's dict of weights: RoutedExperts' call for
+    one, and for any other block whose dict holds experts' weights only;
+    LagaAttentionBlock's for the rest."""
+    if isinstance(block, RoutedExperts) or ("w_router" in w and "w_q" not in w):
+        return block.forward(h, w["w_router"], w["w_in"], w["w_out"], bias=w.get("bias"), **kept)
+    return block.forward(h, w["w_q"], w["w_kva"], w["gamma"], w["w_kvb"], w["w_o"], cos, sin, **kept)
+
+
 class LagaResidualStack:
     """Blocks on a residual stream x [B, S_r, d_model] (contiguous):
 
@@ -202,7 +206,7 @@ class LagaResidualStack:
         x_{l+1} = x_l + alpha s N_post(y_l) gamma_post
 
     ``blocks``: one LagaAttentionBlock or RoutedExperts a layer (the latter on one
-    rank only).  norm_pre, norm_post ("none": a plain gated residual add) and
+    rank only), or a block with the calls of either.  norm_pre, norm_post ("none": a plain gated residual add) and
     gate as for ResidualNorm.  ``ckpt`` holds the normalised x and y of every
     layer as 8-bit checkpoints; the one of x also serves the layer's dW_q and
     dW_kv_a, so neither x nor h is held in the I/O type.  Gate logits are given as tensors and their gradients given
@@ -239,8 +243,8 @@ class LagaResidualStack:
         behind = []                           # of the residual half behind block l
         for i, (block, w) in enumerate(zip(self.blocks, layers)):
             in_bits = self.first.ckpt
-            y = block._layer(r.h, w, cos, sin, kept=kept[i].x if in_bits else None,
-                             kept_gain=w["gamma_pre"] if in_bits else None)
+            y = _block_forward(block, r.h, w, cos, sin, kept=kept[i].x if in_bits else None,
+                               kept_gain=w["gamma_pre"] if in_bits else None)
             ends = i + 1 == len(layers)
             step = self.last if ends else self.between
             r = step.forward(r.x, y, gate=w.get("gate"), alpha=w["alpha"],

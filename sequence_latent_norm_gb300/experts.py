@@ -181,10 +181,6 @@ class RoutedExperts:
     def _outputs(self, a8, w_out, routes):
         return linear8(a8, w_out, routes=routes, dtype=self.dtype)
 
-    def _layer(self, h, w, cos, sin, **kept):
-        """forward with a layer's dict of weights (cos and sin are attention's)."""
-        return self.forward(h, w["w_router"], w["w_in"], w["w_out"], bias=w.get("bias"), **kept)
-
     def _all_reduce(self, t, what):
         return t
 
