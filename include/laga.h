@@ -385,6 +385,12 @@ laga_status laga_ckpt_pack(int rows, int d, laga_dtype dtype, const void* x, voi
 laga_status laga_ckpt_unpack(int rows, int d, laga_dtype dtype, const void* ck, void* x,
                              void* stream);
 
+/* laga_ckpt_pack of the rows in front of *end (device address, e.g. of the number
+ * of experts' rows in use; `rows` at the most): the others are neither read nor
+ * written. */
+laga_status laga_ckpt_pack_rows(int rows, int d, laga_dtype dtype, const void* x, const int* end,
+                                void* ck, void* stream);
+
 /* Bytes of scratch laga_ckpt_dw needs (0 for invalid sizes or none).
  * Host-only. */
 size_t laga_ckpt_dw_workspace_bytes(int rows, int d, int n, laga_dtype dy_dtype);

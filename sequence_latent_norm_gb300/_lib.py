@@ -30,7 +30,8 @@ EXPORTED = ("laga_workspace_bytes", "laga_workspace_tensor", "laga_fwd", "laga_f
             "laga_profile_enable", "laga_profile_reset", "laga_profile_read",
             "laga_norm_rope_bwd_noalloc", "laga_selftest_wait_timeout", "laga_diag_mma_rate",
             "laga_res_fwd", "laga_res_bwd", "laga_res_workspace_bytes", "laga_ckpt_row_bytes",
-            "laga_ckpt_pack", "laga_ckpt_unpack", "laga_ckpt_dw", "laga_ckpt_dw_workspace_bytes",
+            "laga_ckpt_pack", "laga_ckpt_pack_rows", "laga_ckpt_unpack", "laga_ckpt_dw",
+            "laga_ckpt_dw_workspace_bytes",
             "laga_route_rows", "laga_route_workspace_bytes", "laga_route_fwd", "laga_route_bwd",
             "laga_weight_pack", "laga_mm8", "laga_mm8_workspace_bytes", "laga_experts_dw",
             "laga_experts_dw_workspace_bytes", "laga_spread8", "laga_combine_fwd",
@@ -124,6 +125,8 @@ def load(path: str = LIB_PATH):
     lib.laga_ckpt_row_bytes.restype = S
     lib.laga_ckpt_pack.argtypes = [I, I, I, P, P, P]
     lib.laga_ckpt_pack.restype = I
+    lib.laga_ckpt_pack_rows.argtypes = [I, I, I, P, P, P, P]
+    lib.laga_ckpt_pack_rows.restype = I
     lib.laga_ckpt_unpack.argtypes = [I, I, I, P, P, P]
     lib.laga_ckpt_unpack.restype = I
     lib.laga_ckpt_dw.argtypes = [I, I, I, I, P, P, P, P, P, S, P]
@@ -292,6 +295,12 @@ def ckpt_row_bytes(d: int) -> int:
 def ckpt_pack(rows, d, dtype, x, ck, stream=0):
     """laga_ckpt_pack with raw device addresses (ints); dtype "bf16" or "fp32"."""
     _check(load().laga_ckpt_pack(rows, d, DTYPES[dtype], x, ck, stream), "laga_ckpt_pack")
+
+
+def ckpt_pack_rows(rows, d, dtype, x, end, ck, stream=0):
+    """laga_ckpt_pack_rows with raw device addresses (ints)."""
+    _check(load().laga_ckpt_pack_rows(rows, d, DTYPES[dtype], x, end, ck, stream),
+           "laga_ckpt_pack_rows")
 
 
 def ckpt_unpack(rows, d, dtype, ck, x, stream=0):

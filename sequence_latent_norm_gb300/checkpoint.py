@@ -137,15 +137,24 @@ def empty_checkpoint(shape, device):
     return Checkpoint8(data, d, shape)
 
 
-def pack8(x: torch.Tensor, stream=None) -> Checkpoint8:
-    """x [..., d] (bf16 or fp32, contiguous, on a CUDA device) in 8 bits."""
+def pack8(x: torch.Tensor, stream=None, *, routes=None) -> Checkpoint8:
+    """x [..., d] (bf16 or fp32, contiguous, on a CUDA device) in 8 bits; with
+    ``routes`` (a Routes; x has its rows) the rows in use alone."""
     if not isinstance(x, torch.Tensor) or x.dtype not in IO_NAME:
         raise TypeError("pack8 takes a bf16 or fp32 tensor")
     ptr = need(x, "x", x.dtype)
     rows, d = rows_of(x.shape)
-    with on_stream(x.device, stream, x) as st:
+    end = 0
+    if routes is not None:
+        end = routes.check(x.device)[3]
+        if rows != routes.rows:
+            raise ValueError(f"x has {rows} rows, the routes {routes.rows}")
+    with on_stream(x.device, stream, x, routes and routes.start) as st:
         ck = empty_checkpoint(x.shape, x.device)
-        _lib.ckpt_pack(rows, d, IO_NAME[x.dtype], ptr, ck.data.data_ptr(), st)
+        if routes is None:
+            _lib.ckpt_pack(rows, d, IO_NAME[x.dtype], ptr, ck.data.data_ptr(), st)
+        else:
+            _lib.ckpt_pack_rows(rows, d, IO_NAME[x.dtype], ptr, end, ck.data.data_ptr(), st)
     return ck
 
 

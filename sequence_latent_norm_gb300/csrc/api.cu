@@ -442,7 +442,22 @@ laga_status laga_ckpt_pack(int rows, int d, laga_dtype dtype, const void* x, voi
   c.need(rows > 0, ck);
   if (c.status() != LAGA_OK) return c.status();
   return run_launches("laga_ckpt_pack", [&] {
-    return cuda_status(launch_ckpt_pack(rows, d, dtype == LAGA_FP32, x, ck,
+    return cuda_status(launch_ckpt_pack(rows, d, dtype == LAGA_FP32, x, nullptr, ck,
+                                        static_cast<cudaStream_t>(stream)));
+  });
+}
+
+laga_status laga_ckpt_pack_rows(int rows, int d, laga_dtype dtype, const void* x, const int* end,
+                                void* ck, void* stream) {
+  t_launches = 0;
+  if (rows < 0 || d < 1 || d > CK_MAX_D || !dtype_ok(dtype)) return LAGA_ERR_ARG;
+  PtrCheck c;
+  c.need(rows > 0, x);
+  c.need(rows > 0, ck);
+  if (c.status() != LAGA_OK) return c.status();
+  if (rows > 0 && !end) return LAGA_ERR_ARG;
+  return run_launches("laga_ckpt_pack_rows", [&] {
+    return cuda_status(launch_ckpt_pack(rows, d, dtype == LAGA_FP32, x, end, ck,
                                         static_cast<cudaStream_t>(stream)));
   });
 }

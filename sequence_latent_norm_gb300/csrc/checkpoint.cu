@@ -1,4 +1,5 @@
-// 8-bit checkpoints (include/laga.h: laga_ckpt_pack, laga_ckpt_unpack).
+// 8-bit checkpoints (include/laga.h: laga_ckpt_pack, laga_ckpt_pack_rows,
+// laga_ckpt_unpack).
 #include <algorithm>
 
 #include "ckpt8.cuh"
@@ -47,7 +48,9 @@ LAGA_DEVINL void store8(__nv_bfloat16* p, const float2 (&f)[4]) {
 
 template <typename T>
 __global__ void __launch_bounds__(256) ckpt_pack8_kernel(const T* __restrict__ x, uint8_t* ck,
-                                                         int rows, int d) {
+                                                         const int* __restrict__ end, int rows,
+                                                         int d) {
+  if (end) rows = min(rows, *end);
   const int cols = ck_cols(d), vpr = cols / 8, pitch = ck_pitch(d);
   const int pad = pitch - cols - cols / CK_GROUP;
   for (long long r0 = (long long)blockIdx.x * ROWS; r0 < rows; r0 += (long long)gridDim.x * ROWS) {
@@ -120,7 +123,9 @@ __global__ void __launch_bounds__(256) ckpt_unpack8_kernel(const uint8_t* __rest
 // Other widths: one warp per 128-channel group, 4 channels a lane.
 template <typename T>
 __global__ void __launch_bounds__(256) ckpt_pack_kernel(const T* __restrict__ x, uint8_t* ck,
-                                                        int rows, int d) {
+                                                        const int* __restrict__ end, int rows,
+                                                        int d) {
+  if (end) rows = min(rows, *end);
   const int cols = ck_cols(d), groups = cols / CK_GROUP, pitch = ck_pitch(d);
   const int lane = threadIdx.x & 31;
   const long long n = (long long)rows * groups;
@@ -179,21 +184,22 @@ int warp_grid(int rows, int d) {
 
 }  // namespace
 
-cudaError_t launch_ckpt_pack(int rows, int d, bool fp32, const void* x, void* ck, cudaStream_t st) {
+cudaError_t launch_ckpt_pack(int rows, int d, bool fp32, const void* x, const int* end, void* ck,
+                             cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
   LaunchScope ls_("ckpt_pack", st);
   if (d % 8 == 0 && fp32)
     ckpt_pack8_kernel<<<row_grid(rows), 256, 0, st>>>(static_cast<const float*>(x),
-                                                      static_cast<uint8_t*>(ck), rows, d);
+                                                      static_cast<uint8_t*>(ck), end, rows, d);
   else if (d % 8 == 0)
     ckpt_pack8_kernel<<<row_grid(rows), 256, 0, st>>>(static_cast<const __nv_bfloat16*>(x),
-                                                      static_cast<uint8_t*>(ck), rows, d);
+                                                      static_cast<uint8_t*>(ck), end, rows, d);
   else if (fp32)
     ckpt_pack_kernel<float><<<warp_grid(rows, d), 256, 0, st>>>(
-        static_cast<const float*>(x), static_cast<uint8_t*>(ck), rows, d);
+        static_cast<const float*>(x), static_cast<uint8_t*>(ck), end, rows, d);
   else
     ckpt_pack_kernel<__nv_bfloat16><<<warp_grid(rows, d), 256, 0, st>>>(
-        static_cast<const __nv_bfloat16*>(x), static_cast<uint8_t*>(ck), rows, d);
+        static_cast<const __nv_bfloat16*>(x), static_cast<uint8_t*>(ck), end, rows, d);
   return cudaGetLastError();
 }
 

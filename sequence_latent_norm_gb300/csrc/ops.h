@@ -28,7 +28,9 @@ size_t res_ws_bytes(const laga_res_dims& d);
 cudaError_t launch_res_fwd(const laga_res_dims& d, const ResPtrs& x, cudaStream_t st);
 cudaError_t launch_res_bwd(const laga_res_dims& d, const ResPtrs& x, cudaStream_t st);
 
-cudaError_t launch_ckpt_pack(int rows, int d, bool fp32, const void* x, void* ck, cudaStream_t st);
+// end: device address of the number of rows, or null: all of them.
+cudaError_t launch_ckpt_pack(int rows, int d, bool fp32, const void* x, const int* end, void* ck,
+                             cudaStream_t st);
 cudaError_t launch_ckpt_unpack(int rows, int d, bool fp32, const void* ck, void* x,
                                cudaStream_t st);
 

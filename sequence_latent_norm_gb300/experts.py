@@ -192,10 +192,10 @@ class RoutedExperts:
         a8 = swiglu8(gu, routes=routes)
         d_rows, dweight = combine_grad(dy_flat, routes, y=self._outputs(a8, w_out, routes))
         dw_out = weight_grad8(a8, d_rows, routes=routes)
-        da = linear8_dx(pack8(d_rows), w_out, routes=routes, dtype=self.dtype)
+        da = linear8_dx(pack8(d_rows, routes=routes), w_out, routes=routes, dtype=self.dtype)
         dgu = swiglu8_grad(gu, da, routes=routes)
         dw_in = weight_grad8(spread8(kept, routes), dgu, gain, routes=routes)
-        dx = linear8_dx(pack8(dgu), w_in, routes=routes, dtype=self.dtype)
+        dx = linear8_dx(pack8(dgu, routes=routes), w_in, routes=routes, dtype=self.dtype)
         dlogits = self.router.backward(logits, routes, dweight)
         dh = combine(dx, routes, weighted=False) + (dlogits @ w_router.t()).to(self.dtype)
         return dict(dh=dh.reshape(shape), dw_router=weight_grad8(kept, dlogits, gain), dw_in=dw_in,
