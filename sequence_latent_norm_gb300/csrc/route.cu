@@ -375,6 +375,8 @@ LAGA_DEVINL bool pick(const RouteParams& p, const T* l, unsigned (&key)[M], cons
   const bool equal = mine == l1 && b == b1 && lane + 1 < p.top_k;
   const bool close = lane < min(p.top_k, 31) && expert >= 0 && e1 >= 0 && !equal &&
                      !(value - v1 > 2.f * lost + (fabsf(value) + fabsf(v1)) * 0x1p-24f);
+  // (A choice of 32 has no lane for the one below it, and goes over the whole token
+  // again: 16384 x 256 take 857 us, 111 us with 31 choices.)
   if (__any_sync(ALL, close) || p.top_k == 32) {
     // everything that may belong to the best top_k, whose last one may have lost
     // as much as what is below it
@@ -396,6 +398,15 @@ LAGA_DEVINL bool pick(const RouteParams& p, const T* l, unsigned (&key)[M], cons
     score = 0.f;
   }
   return true;
+}
+
+// v[I + i], i < N, by selections, since registers have no index.
+template <int I, int N, int M>
+LAGA_DEVINL unsigned element(const unsigned (&v)[M], int i) {
+  if constexpr (N == 1)
+    return v[I];
+  else
+    return i & N / 2 ? element<I + N / 2, N / 2>(v, i) : element<I, N / 2>(v, i);
 }
 
 // The choice in fp32: lane j's expert.  `score`: its score.  `reach`: no sum of
@@ -487,24 +498,30 @@ LAGA_DEVINL bool choose(const RouteParams& p, const T* l, const float (&x)[NV],
                  ? regroup_wide<NV, T>(p, l, top, inv, mine, in, out, tol, lost, lane) : 0u;
       if (keep == 0u) return false;
     }
-    if constexpr (NV == 8) {
-      // groups of a register, four of them at most: what is left in four, which
-      // the rounds go over (16384 x 256, 4 of 8 groups: 47 us -> 41 us)
-      if (p.group_size == 32 && p.top_groups <= 4) {
-        unsigned live[4];
-        int first[4];
+    if constexpr (NV >= 2 && NV <= 16) {
+      // Groups of whole registers, no more than half of which are kept: the rounds
+      // go over the kept ones only.  (16384 tokens, forward, without and with: 8 groups
+      // of 32, 4 kept 47 and 41 us; 4 of 64, 2 kept 43.3 and 42.2; 4 of 32, 2 kept 28.3
+      // and 27.8; 16 of 32, 8 kept 79 and 73; 32 of 32, 8 kept 184 and 189, where the
+      // selections cost more than the rounds save.)
+      constexpr int H = NV / 2;
+      if (p.group_size % 32 == 0 && p.top_groups * (p.group_size / 32) <= H) {
+        unsigned kept = keep;                // registers; the same for all lanes
+        if (p.group_size != 32) {
+          kept = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int i = keep ? __ffs(keep) - 1 : 0;   // the same for all lanes
-          const bool b0 = i & 1, b1 = i & 2, b2 = i & 4;
-          const unsigned k01 = b0 ? key[1] : key[0], k23 = b0 ? key[3] : key[2];
-          const unsigned k45 = b0 ? key[5] : key[4], k67 = b0 ? key[7] : key[6];
-          const unsigned low = b1 ? k23 : k01, high = b1 ? k67 : k45;
-          live[j] = keep ? b2 ? high : low : KEY_OFF;
-          first[j] = 32 * i + lane;
-          keep &= keep - 1;
+          for (int i = 0; i < NV; ++i) kept |= (keep >> group[i] & 1u) << i;
         }
-        return pick<NV, 4, T>(p, l, live, first, top, inv, lost, lane, expert, score);
+        unsigned live[H];
+        int first[H];
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+          const int i = kept ? __ffs(kept) - 1 : 0;
+          live[j] = kept ? element<0, NV>(key, i) : KEY_OFF;
+          first[j] = 32 * i + lane;
+          kept &= kept - 1;
+        }
+        return pick<NV, H, T>(p, l, live, first, top, inv, lost, lane, expert, score);
       }
     }
 #pragma unroll
