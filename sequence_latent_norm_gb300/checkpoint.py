@@ -24,6 +24,11 @@ from . import _lib
 
 IO_NAME = {torch.bfloat16: "bf16", torch.float32: "fp32"}
 
+# Handle of a device's current stream.  Every call asks for it: 0.1 us by torch's own
+# short way, 1.1 us by the public one, which serves where torch has no such name.
+_current_handle = (getattr(torch._C, "_cuda_getCurrentRawStream", None) or
+                   (lambda index: torch.cuda.current_stream(index).cuda_stream))
+
 
 class on_stream:
     """Run on ``device`` and ``stream`` (None: the device's current stream);
@@ -51,7 +56,7 @@ class on_stream:
             self.inner.__enter__()
         if self.stream is not None:
             return self.stream.cuda_stream
-        return torch._C._cuda_getCurrentRawStream(self.device.index)   # a tenth of the public way
+        return _current_handle(self.device.index)
 
     def __exit__(self, *exc):
         if self.inner is not None:
