@@ -589,7 +589,7 @@ static bool mm8_sizes_ok(int rows, int k, int n, int experts, laga_dtype dtype) 
 
 size_t laga_mm8_workspace_bytes(int rows, int k, int n, int experts, laga_dtype out_dtype) {
   return mm8_sizes_ok(rows, k, n, experts, out_dtype)
-             ? mm8_ws_bytes(rows, k, n, experts, out_dtype == LAGA_FP32)
+             ? mm8_ws_bytes(rows, k, n, experts)
              : 0;
 }
 
@@ -599,7 +599,7 @@ laga_status laga_mm8(int rows, int k, int n, int experts, laga_dtype out_dtype, 
   t_launches = 0;
   if (!mm8_sizes_ok(rows, k, n, experts, out_dtype)) return LAGA_ERR_ARG;
   const bool fp32 = out_dtype == LAGA_FP32;
-  const size_t need_bytes = mm8_ws_bytes(rows, k, n, experts, fp32);
+  const size_t need_bytes = mm8_ws_bytes(rows, k, n, experts);
   PtrCheck c;
   c.need(rows > 0, a);
   c.need(rows > 0, b);

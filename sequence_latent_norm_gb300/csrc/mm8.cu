@@ -608,7 +608,7 @@ cudaError_t out_map(CUtensorMap* out, void* base, uint64_t n, uint64_t rows, boo
 
 }  // namespace
 
-size_t mm8_ws_bytes(int rows, int K, int N, int experts, bool fp32) {
+size_t mm8_ws_bytes(int rows, int K, int N, int experts) {
   if (rows == 0) return 0;
   const Mm8Plan pl = mm8_plan(rows, K, N, experts);
   return pl.splits > 1 ? (size_t)pl.splits * rows * N * 4 : 0;

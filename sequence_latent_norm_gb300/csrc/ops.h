@@ -69,7 +69,7 @@ cudaError_t launch_swiglu_bwd(int rows, int f, bool fp32, const void* gu, const 
 
 cudaError_t launch_weight_pack(int experts, int K, int N, bool fp32, const void* w, void* fwd,
                                void* bwd, cudaStream_t st);
-size_t mm8_ws_bytes(int rows, int K, int N, int experts, bool fp32);
+size_t mm8_ws_bytes(int rows, int K, int N, int experts);
 cudaError_t launch_mm8(int rows, int K, int N, int experts, bool fp32, const void* a,
                        const void* b, const int* start, const int* pair, void* y,
                        unsigned char* ws, int* err, cudaStream_t st);
