@@ -69,7 +69,8 @@ class LagaAttentionBlock:
     given, "fp8": in 8 bits, on a CUDA device); ``projections`` how W_q, W_kv_a
     and W_o are multiplied ("io": in the I/O type, "fp8": in 8 bits, widths up to
     16384, on a CUDA device; h is then held in 8 bits whatever ``checkpoint``
-    says)."""
+    says, and the latent's fp32 gradient is rounded to the I/O type before it
+    makes dW_kv_a's, which ``checkpoint="fp8"`` alone takes from fp32)."""
 
     def __init__(self, attn, n_h: int, group=None, distributed: bool = False,
                  checkpoint: str = "none", projections: str = "io"):
@@ -172,7 +173,9 @@ class LagaAttentionBlock:
         dq_flat = dq.reshape(rows, -1)
         dc_flat = dc.reshape(rows, -1)
         if fp8:
-            dc_flat = dc_flat.to(dq.dtype)   # (in fp32 its weight gradient would take three products)
+            # (in fp32 its weight gradient would take three products: a step of 7.30 ms
+            # instead of 6.99)
+            dc_flat = dc_flat.to(dq.dtype)
             dh = (linear8_dx(pack8(dq_flat), w_q, dtype=dq.dtype) +
                   linear8_dx(pack8(dc_flat), w_kva, dtype=dq.dtype)).reshape(h_shape)
         else:

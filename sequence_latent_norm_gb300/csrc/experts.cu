@@ -1,5 +1,6 @@
 // Rows to experts and back, and the experts' gated activation (include/laga.h:
-// laga_spread8, laga_combine_*, laga_swiglu_*).  All of it is bound by HBM.
+// laga_spread8, laga_combine_*, laga_swiglu_*).  What moves rows is bound by HBM, the
+// activation by HBM and its instructions.
 #include <algorithm>
 
 #include "ckpt8.cuh"
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------ activation
 // Each kernel moves 4 to 10 bytes a channel and has some 25 instructions for it
 // at that rate, so the sigmoid is two special functions; channels come in
-// vectors of 8 where the width allows.  (16384 x 2048 bf16: 33 us forward, and 82 us
+// vectors of 8 where the width allows.  (16384 x 2048 bf16: 34 us forward, and 82 us
 // with expf, a division and single channels.)
 
 // sigmoid(g) and 1 - sigmoid(g) = e^-g sigmoid(g), each within 6 units of its

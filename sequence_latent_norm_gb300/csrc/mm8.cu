@@ -25,15 +25,15 @@
 // other fills, and four sets of scales.
 //
 // What bounds it (16384 x 7168 x 7168, bf16 out: 531 us, 3170 TFLOP/s, 0.83 of
-// twice the measured bf16 rate): the supply of operands, next to the issuing
-// thread.  MMAs alone run at 4500 TFLOP/s.  Every wait, commit and copy of
-// scales that stands between them takes 60 to 150 clocks of the one thread that
-// issues: with a wait per 128 of i instead of 256 and scales fetched 4 steps at a
-// time it took 690 us.  Without its loads it takes 468 us, and 508 us where all of
-// them hit the same lines of L2: they write 45 bytes a clock into a shared
-// memory that the MMAs read at the same time.  Short K
-// (16384 x 2048 x 7168: 216 us) adds the output's 235 MB; a few rows are bound by
-// b's bytes.
+// twice the measured bf16 rate): what stands between the MMAs, which keep the
+// tensor pipe busy for 65 % of the clocks at 16384 x 7168 x 1536.  A step takes
+// some 690 clocks of a pair, 448 of them its MMAs at the nominal rate; the rest are
+// the waits, commits and copies of scales of the one thread that issues (with a
+// wait per 128 of i instead of 256 and scales fetched 4 steps at a time 690 us), and
+// loads of 45 bytes a clock into a shared memory that the MMAs read at the same
+// time.  Short K (16384 x 2048 x 7168: 216 us) adds the output's 235 MB; a few rows
+// are bound by b's bytes, one token by the 56 of 76 pairs that its pieces of K fill,
+// and the launch that joins them (7168 x 7168: 28 us).
 #include <algorithm>
 
 #include "ckpt8.cuh"
@@ -334,8 +334,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      // This thread's own instructions are a good part of the pace (MMAs take 112
-      // clocks): what can be is carried along instead of computed.
+      // This thread's own instructions are a good part of the pace (an MMA takes 112
+      // clocks at the nominal rate): what can be is carried along, not computed.
       uint32_t group = 0, set = 0, tile = 0;
       uint32_t st = 0, parity = 0;         // the next stage and its phase
       bool ok = true;

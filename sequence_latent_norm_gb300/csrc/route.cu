@@ -13,7 +13,7 @@
 // runs at 2 operations a clock and SM on this part: a second run of the whole
 // token costs 10 us of latency, and with one for every close score the kernel
 // took 78 us for 16384 x 256, and 46 us without any; it takes some 30 us now,
-// bound by its instructions, 1330 a token and warp.
+// bound by its instructions, 1340 a token and warp.
 //
 // The order of the rows: a block counts its chunk's rows by expert; the second
 // kernel (the same one, where the batch is one chunk) adds up the chunks in

@@ -12,8 +12,10 @@ namespace {
 // 128-byte pieces of the rows of W^T (fwd) and of W (bwd).  A thread loads 8
 // columns of 8 rows.  The codes are turned in shared memory in words of 4: word w
 // of row r sits at w ^ (r / 4), so that reading rows 4 l .. 4 l + 3 of one word by
-// lane l, like writing, meets every bank once.  Bound by HBM from some 10^7 values
-// on (7168 x 1536 bf16: 10 us within a graph).
+// lane l, like writing, meets every bank once.  It moves 0.7 of what HBM could at
+// 32 x 7168 x 4096 (799 us): every row of a block ends in a scale byte, which one lane
+// stores, and the bf16 kernel spills 64 bytes at its 64 registers.  (7168 x 1536
+// bf16: 10 us within a graph.)
 // The values stay as they were loaded until they are coded, so that four blocks of
 // bf16 weights fit an SM (32 x 7168 x 4096: 881 us as floats, three blocks).
 constexpr int WB = CK_GROUP;
