@@ -504,7 +504,8 @@ laga_status laga_spread8(int rows, int tokens, int top_k, int d, const void* ck,
                          const int* end, void* out, void* stream);
 
 /* out[t] = sum_j weight[t, j] y[row[t, j]], in fp32, j ascending; weight NULL:
- * 1; a row of -1 adds nothing, one of -2 makes out[t] NaN.  y [rows, d], out [tokens, d] (output). */
+ * 1; a row of -1 adds nothing, one of -2 makes out[t] NaN.  y [rows, d], out
+ * [tokens, d] (output). */
 laga_status laga_combine_fwd(int tokens, int top_k, int rows, int d, laga_dtype dtype,
                              const void* y, const float* weight, const int* row, void* out,
                              void* stream);

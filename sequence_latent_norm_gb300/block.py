@@ -209,12 +209,13 @@ class LagaResidualStack:
         x_{l+1} = x_l + alpha s N_post(y_l) gamma_post
 
     ``blocks``: one LagaAttentionBlock or RoutedExperts a layer (the latter on one
-    rank only), or a block with the calls of either.  norm_pre, norm_post ("none": a plain gated residual add) and
-    gate as for ResidualNorm.  ``ckpt`` holds the normalised x and y of every
-    layer as 8-bit checkpoints; the one of x also serves the layer's dW_q and
-    dW_kv_a, so neither x nor h is held in the I/O type.  Gate logits are given as tensors and their gradients given
-    back; a gate that is computed from x or h on the way needs ResidualNorm in
-    the caller's own loop."""
+    rank only), or a block with the calls of either.  norm_pre, norm_post
+    ("none": a plain gated residual add) and gate as for ResidualNorm.  ``ckpt``
+    holds the normalised x and y of every layer as 8-bit checkpoints; the one of
+    x also serves the layer's dW_q and dW_kv_a, so neither x nor h is held in the
+    I/O type.  Gate logits are given as tensors and their gradients given back; a
+    gate that is computed from x or h on the way needs ResidualNorm in the
+    caller's own loop."""
 
     def __init__(self, blocks, d_model: int, *, norm_pre: str = "rms", norm_post: str = "none",
                  gate: str = "none", ckpt: bool = False, io_dtype: str = "bf16", eps: float = 1e-5,

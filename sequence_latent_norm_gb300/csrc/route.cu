@@ -502,8 +502,8 @@ LAGA_DEVINL bool choose(const RouteParams& p, const T* l, const float (&x)[NV],
       // Groups of whole registers, no more than half of which are kept: the rounds
       // go over the kept ones only.  (16384 tokens, forward, without and with: 8 groups
       // of 32, 4 kept 47 and 41 us; 4 of 64, 2 kept 43.3 and 42.2; 4 of 32, 2 kept 28.3
-      // and 27.8; 16 of 32, 8 kept 79 and 73; 32 of 32, 8 kept 184 and 189, where the
-      // selections cost more than the rounds save.)
+      // and 27.8; 16 of 32, 8 kept 79 and 73.  Of 32 registers the selections cost more
+      // than the rounds save: 32 of 32, 8 kept 184 and 186; 16 of 64, 8 kept 168 and 180.)
       constexpr int H = NV / 2;
       if (p.group_size % 32 == 0 && p.top_groups * (p.group_size / 32) <= H) {
         unsigned kept = keep;                // registers; the same for all lanes

@@ -27,12 +27,12 @@ class Routes(NamedTuple):
     expert [T, k] int32 (best first; -1: no expert was on); weight [T, k]
     fp32 (0 there; NaN throughout a token that holds a NaN); row [T, k] int32:
     the pair's row, -1 where it has none (on this rank), -2 where a token with
-    a NaN has no expert (combine makes that token NaN); pair [R] int32: the row's pair t k + j, -1 where it has none;
-    start [E + 1] int32: expert e (of this rank's) takes the rows start[e] ..
-    start[e + 1] - 1, of which the ones behind its pairs belong to none.
-    start[e] are multiples of ``align``.  R rows are the most that a batch can
-    need; buffers of rows have that many, and what is behind row start[E] - 1
-    is never written or read."""
+    a NaN has no expert (combine makes that token NaN); pair [R] int32: the
+    row's pair t k + j, -1 where it has none; start [E + 1] int32: expert e (of
+    this rank's) takes the rows start[e] .. start[e + 1] - 1, of which the ones
+    behind its pairs belong to none.  start[e] are multiples of ``align``.  R
+    rows are the most that a batch can need; buffers of rows have that many, and
+    what is behind row start[E] - 1 is never written or read."""
 
     expert: torch.Tensor
     weight: torch.Tensor
